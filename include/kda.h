@@ -12,6 +12,11 @@
  * with its state updated in place in its cache row.  Checkpoints can be
  * parked compressed: kda_ckpt_quantize_scatter / kda_ckpt_dequantize_gather
  * move states between packed buffers and an INT8 checkpoint store.
+ * Hybrid models interleave KDA layers with latent-attention layers over the
+ * same packed batch: kda_latent_prefill and kda_latent_decode are those
+ * layers' attention, and kda_page_fork / kda_page_compact / kda_page_free keep
+ * the pages of a latent cache (and the rows of a state cache) shared, dense
+ * and reclaimed.
  *
  * Sources (web pages, cited by title and section):
  *  [P1] "vllm-ascend 的 KDA 状态复制 Triton 集成：PR 17301 对齐的预编译 worker
@@ -359,6 +364,235 @@ kda_status_t kda_ckpt_quantize_scatter(const kda_int8_store_t* store, const void
 kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const void* indices, kda_index_t index_type,
                                         int64_t num_selected, const uint8_t* flags, void* packed,
                                         kda_dtype_t packed_dtype, void* stream);
+
+/*
+ * Arguments of kda_latent_prefill: attention with keys and values expanded per
+ * head from one latent vector a token, over a packed batch.  All pointers are
+ * device pointers; every tensor's last dim is dense and its other dims have
+ * the element strides given.
+ *  T, S, N, H      -- query tokens, key tokens, sequences, heads.
+ *  D, R, E         -- key dim per head (8..128), rotary key dim shared by the
+ *                     heads (0..64), value dim (8..128); multiples of 8.
+ *  dtype           -- of q, k, k_rope, v and out: KDA_BF16.
+ *  q               -- [T, H, D+R]; q_stride = {token, head}.
+ *  k               -- [S, H, D];   k_stride = {token, head}.
+ *  k_rope          -- [S, R], one row a token for all heads; k_rope_stride =
+ *                     token stride (NULL with R == 0).
+ *  v               -- [S, H, E];   v_stride = {token, head}.
+ *                     q, k, k_rope and v are 16-byte aligned and their strides
+ *                     are multiples of 8 elements, 0 .. 2^40 (0: a broadcast dim).
+ *  cu_seqlens_q    -- [N+1] int32 offsets of the sequences' queries in q.
+ *  cu_seqlens_k    -- [N+1] int32 offsets of their keys in k, k_rope and v.
+ *                     Both non-decreasing (not checked; the kernel clamps, so
+ *                     bad offsets cannot address outside the tensors).
+ *  out             -- [T, H, E] contiguous, 8-byte aligned.
+ *  lse             -- [T, H] fp32, or NULL.
+ *  scale           -- factor of the scores, positive and finite.
+ *  causal          -- nonzero: query i of a sequence with Lq queries and Lk
+ *                     keys sees keys j < Lk - (Lq - 1 - i), so its queries are
+ *                     the last Lq of Lk positions; zero: it sees all Lk keys.
+ * For query i and head h of a sequence, over the keys j it sees:
+ *   s_j = scale (q_i[:D] . k_j + q_i[D:] . k_rope_j)
+ *   out_i = sum_j exp(s_j - lse_i) v_j,   lse_i = log sum_j exp(s_j)
+ * A query that sees no key gets out 0 and lse -inf.  Rows of q that belong to
+ * no sequence have their out and lse rows left as they were.
+ * Precision: products of bf16 operands with fp32 sums; scores, the running
+ * maximum and sum and the output accumulate in fp32; the softmax weights are
+ * rounded to bf16 as operands of the second product.
+ * A NaN or infinite value row v_j can reach queries that do not see key j but
+ * see another key of the same 64 (their weight 0 multiplies it); keys and
+ * rotary keys that a query does not see never reach it.
+ */
+typedef struct {
+  int64_t T, S, N, H, D, R, E;
+  kda_dtype_t dtype;
+  const void* q;
+  int64_t q_stride[2];
+  const void* k;
+  int64_t k_stride[2];
+  const void* k_rope;
+  int64_t k_rope_stride;
+  const void* v;
+  int64_t v_stride[2];
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  void* out;
+  float* lse;
+  float scale;
+  int causal;
+} kda_latent_prefill_args_t;
+
+/*
+ * kda_latent_prefill -- see kda_latent_prefill_args_t.  Aliasing (checked on
+ * the host, KDA_E_ALIAS): out and lse overlap neither each other nor any
+ * input.  T == 0 or N == 0 enqueues nothing.
+ * Errors: KDA_E_NULL, KDA_E_DTYPE, KDA_E_SHAPE, KDA_E_LAYOUT (alignment or
+ * strides), KDA_E_UNSUPPORTED, KDA_E_ALIAS, KDA_E_HIP.
+ */
+kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* args, void* stream);
+
+/*
+ * Arguments of kda_latent_decode: Q new tokens for each of N sequences against
+ * a paged cache of latent rows, in the absorbed form (the key up-projection
+ * folded into q, the value up-projection applied to out by the caller).
+ *  N, Q, H         -- sequences, new tokens a sequence (>= 1), heads; Q * H <= 1024.
+ *  L, R            -- latent dim (8..512), rotary key dim (0..64); multiples of 8.
+ *  dtype           -- of the cache, q, q_rope and out: KDA_BF16.
+ *  cache           -- [num_pages, page_size, L+R], dense inner dims, page_stride
+ *                     elements (>= page_size (L+R), multiple of 8) from page to
+ *                     page; 16-byte aligned.  Row = one token's latent vector,
+ *                     then its rotary key.
+ *  page_table      -- [N, max_pages] int32, rows table_stride apart; entry j of
+ *                     row n is the page of sequence n's tokens j page_size ...
+ *  lengths         -- [N] int32 tokens in the cache, the Q new ones included.
+ *  q, q_rope       -- [N, Q, H, L], [N, Q, H, R] with strides {n, query, head}
+ *                     (multiples of 8 elements), last dim dense, 16-byte
+ *                     aligned; q_rope NULL with R == 0.
+ *  out             -- [N, Q, H, L] contiguous, 16-byte aligned.
+ *  lse             -- [N, Q, H] fp32, or NULL.
+ *  scale           -- factor of the scores, positive and finite.
+ *  workspace       -- device scratch, 16-byte aligned, of at least
+ *                     kda_latent_decode_workspace_size(N, Q, H, L) bytes.
+ * Query i of sequence n sees the rows j < lengths[n] - (Q - 1 - i):
+ *   s_j = scale (q . row_j[:L] + q_rope . row_j[L:]),  out = sum_j softmax(s)_j row_j[:L]
+ * A query that sees no row gets out 0 and lse -inf.  Rows whose page_table
+ * entry lies outside [0, num_pages) are not seen; lengths are clamped to
+ * [0, max_pages * page_size] (which may not exceed 2^30).  Rows of a page
+ * behind a sequence's length are not read.  The result does not depend on the
+ * order of workgroups; how a sequence is split depends on the whole batch's
+ * lengths, so its rounding may change with its neighbours' lengths.
+ * Precision as kda_latent_prefill; partial results of split sequences are fp32.
+ * A non-finite row a later query of the same call sees can reach its earlier
+ * queries, as in kda_latent_prefill.
+ */
+typedef struct {
+  int64_t N, Q, H, L, R;
+  kda_dtype_t dtype;
+  const void* cache;
+  int64_t num_pages, page_size, page_stride;
+  const int32_t* page_table;
+  int64_t table_stride, max_pages;
+  const int32_t* lengths;
+  const void* q;
+  int64_t q_stride[3];
+  const void* q_rope;
+  int64_t q_rope_stride[3];
+  void* out;
+  float* lse;
+  float scale;
+  void* workspace;
+  size_t workspace_bytes;
+} kda_latent_decode_args_t;
+
+/* Bytes of device workspace kda_latent_decode needs for these sizes. */
+size_t kda_latent_decode_workspace_size(int64_t N, int64_t Q, int64_t H, int64_t L);
+
+/*
+ * kda_latent_decode -- see kda_latent_decode_args_t.  Aliasing (checked,
+ * KDA_E_ALIAS): out, lse and the workspace overlap neither each other nor any
+ * input.  Calls that can run at the same time need workspaces of their own.
+ * N == 0 enqueues nothing.  The call can be captured: its work follows the
+ * lengths and the table that each replay finds.
+ * Errors: KDA_E_NULL, KDA_E_DTYPE, KDA_E_SHAPE, KDA_E_LAYOUT, KDA_E_OVERLAP,
+ * KDA_E_UNSUPPORTED, KDA_E_WORKSPACE, KDA_E_ALIAS, KDA_E_HIP.
+ */
+kda_status_t kda_latent_decode(const kda_latent_decode_args_t* args, void* stream);
+
+/*
+ * The bookkeeping of a cache's pages, all on the device: sequence slot s holds
+ * lengths[s] tokens in the pages table[s * table_stride + j],
+ * j < ceil(lengths[s] / page_size); refs[p] says how many slots hold page p,
+ * and a page is free when refs[p] <= 0.  A slot of length 0 is empty.  A state
+ * cache is a pool with page_size 1, one page a slot and lengths 0 or 1.
+ *  num_seqs, max_pages, num_pages, page_size -- positive; num_seqs <= 2^24,
+ *   max_pages <= 2^20, num_pages <= 2^30, page_size <= 2^30.
+ *   table_stride >= max_pages.
+ */
+typedef struct {
+  int32_t* table;
+  int64_t table_stride, num_seqs, max_pages;
+  int32_t* lengths;
+  int32_t* refs;
+  int64_t num_pages, page_size;
+} kda_page_pool_t;
+
+/*
+ * One layer's pages: page p is the page_bytes bytes at data + p * page_stride
+ * (bytes; page_stride >= page_bytes > 0).  The gap between pages is never
+ * read or written.  A pool serves any number of stores; layers that lie side
+ * by side in one page are one store.
+ */
+typedef struct {
+  void* data;
+  int64_t page_stride, page_bytes;
+} kda_page_store_t;
+
+/*
+ * kda_page_fork -- slot dst[i] becomes a child of slot src[i], i < num_forks.
+ *  share != 0: the child holds the parent's full pages too (refs + 1) and
+ *   takes one free page for a copy of a partly filled last page.  For pages
+ *   that are only appended to.
+ *  share == 0: the child takes as many free pages as the parent has and all
+ *   are copied.  For pages that are updated in place (recurrent states).
+ * Entries are served in order, and free pages are taken in ascending order.
+ * status[i] receives
+ *  2 if src[i] or dst[i] is no slot, both are the same, dst[i] is not empty or
+ *    is an earlier entry's dst too, the parent's length is negative or above
+ *    max_pages * page_size, or one of the parent's pages is outside
+ *    [0, num_pages) or has refs <= 0;
+ *  1 if the pages of this entry and the served or unserved sound ones before
+ *    it are not all free;
+ *  0 if it was served: table row dst[i] holds the child's pages and -1 behind
+ *    them, lengths[dst[i]] = lengths[src[i]], the pages taken have refs 1 and
+ *    every store's copies are done.
+ * Unserved entries change nothing.  All entries see the pool as it was before
+ * the call.
+ *  src, dst  -- [num_forks] int32 or int64 device arrays.
+ *  stores    -- host array of num_stores stores (0 .. 4096; NULL with 0).
+ *  status    -- [num_forks] int32 device output.
+ *  workspace -- device scratch (4-byte aligned) of
+ *               kda_page_fork_workspace_size bytes.
+ * Aliasing (checked, KDA_E_ALIAS): table, lengths, refs, status, the workspace
+ * and the stores' spans are disjoint from each other and from src and dst.
+ * num_forks == 0 enqueues nothing.  Errors: KDA_E_NULL, KDA_E_DTYPE,
+ * KDA_E_SHAPE, KDA_E_OVERLAP, KDA_E_UNSUPPORTED, KDA_E_WORKSPACE, KDA_E_ALIAS,
+ * KDA_E_HIP.
+ */
+kda_status_t kda_page_fork(const kda_page_pool_t* pool, const kda_page_store_t* stores, int64_t num_stores,
+                           const void* src, const void* dst, kda_index_t index_type, int64_t num_forks, int share,
+                           int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace kda_page_fork needs for these sizes. */
+size_t kda_page_fork_workspace_size(int64_t num_forks, int64_t max_pages, int64_t num_pages, int share);
+
+/*
+ * kda_page_compact -- moves the pages in use to the front.  With n pages in
+ * use (refs > 0), the k-th page in use of index >= n goes to the k-th free
+ * page of index < n: every store's page is copied, refs moves along and the
+ * slots' table entries are renamed (those within a slot's length).  Pages
+ * below n that are in use stay where they are; afterwards pages [0, n) are in
+ * use and all others free.
+ *  live      -- device output, one int32: n; or NULL.
+ *  workspace -- device scratch (4-byte aligned) of
+ *               kda_page_compact_workspace_size(num_pages) bytes.
+ * Aliasing and errors as for kda_page_fork.
+ */
+kda_status_t kda_page_compact(const kda_page_pool_t* pool, const kda_page_store_t* stores, int64_t num_stores,
+                              int32_t* live, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace kda_page_compact needs. */
+size_t kda_page_compact_workspace_size(int64_t num_pages);
+
+/*
+ * kda_page_free -- for every slot s with release[s] != 0 ([num_seqs] bytes on
+ * the device): refs - 1 for each of its pages (entries outside
+ * [0, num_pages) are passed over), its entries -1, its length 0.  Page
+ * contents stay.  Aliasing (checked): table, lengths, refs and release are
+ * disjoint.
+ * Errors: KDA_E_NULL, KDA_E_SHAPE, KDA_E_OVERLAP, KDA_E_UNSUPPORTED,
+ * KDA_E_ALIAS, KDA_E_HIP.
+ */
+kda_status_t kda_page_free(const kda_page_pool_t* pool, const uint8_t* release, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* kda_status_string(kda_status_t status);

@@ -16,6 +16,9 @@ STATUS_NAMES = {0: "KDA_OK", 1: "KDA_E_NULL", 2: "KDA_E_DTYPE", 3: "KDA_E_SHAPE"
 EXPORTED = ("kda_state_gather", "kda_state_scatter", "kda_chunk_prefill", "kda_chunk_prefill_workspace_size",
             "kda_chunk_prefill_noalloc",
             "kda_recurrent_decode", "kda_ckpt_quantize_scatter", "kda_ckpt_dequantize_gather",
+            "kda_latent_prefill", "kda_latent_decode", "kda_latent_decode_workspace_size",
+            "kda_page_fork", "kda_page_fork_workspace_size", "kda_page_compact", "kda_page_compact_workspace_size",
+            "kda_page_free",
             "kda_status_string", "kda_last_error_detail")
 
 
@@ -52,6 +55,41 @@ class Int8Store(ctypes.Structure):
     _fields_ = [("qdata", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("num_slots", ctypes.c_int64),
                 ("H", ctypes.c_int64), ("V", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("qdata_stride0", ctypes.c_int64), ("scale_stride0", ctypes.c_int64)]
+
+
+class LatentPrefillArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("S", ctypes.c_int64), ("N", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("R", ctypes.c_int64), ("E", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
+                ("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 2),
+                ("k_rope", ctypes.c_void_p), ("k_rope_stride", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64 * 2),
+                ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int)]
+
+
+class LatentDecodeArgs(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("Q", ctypes.c_int64), ("H", ctypes.c_int64), ("L", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("cache", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 3),
+                ("q_rope", ctypes.c_void_p), ("q_rope_stride", ctypes.c_int64 * 3),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("lengths", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64)]
+
+
+class PageStore(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
 
 
 class KDAError(RuntimeError):
@@ -93,6 +131,24 @@ def load_library(path: str = LIB_PATH):
     lib.kda_ckpt_dequantize_gather.restype = ctypes.c_int
     lib.kda_chunk_prefill_workspace_size.argtypes = [i64, i64, i64, i64, i64]
     lib.kda_chunk_prefill_workspace_size.restype = ctypes.c_size_t
+    lib.kda_latent_prefill.argtypes = [ctypes.POINTER(LatentPrefillArgs), vp]
+    lib.kda_latent_prefill.restype = ctypes.c_int
+    lib.kda_latent_decode.argtypes = [ctypes.POINTER(LatentDecodeArgs), vp]
+    lib.kda_latent_decode.restype = ctypes.c_int
+    lib.kda_latent_decode_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.kda_latent_decode_workspace_size.restype = ctypes.c_size_t
+    pool, stores = ctypes.POINTER(PagePool), ctypes.POINTER(PageStore)
+    lib.kda_page_fork.argtypes = [pool, stores, i64, vp, vp, ctypes.c_int, i64, ctypes.c_int, vp, vp, ctypes.c_size_t,
+                                  vp]
+    lib.kda_page_fork.restype = ctypes.c_int
+    lib.kda_page_fork_workspace_size.argtypes = [i64, i64, i64, ctypes.c_int]
+    lib.kda_page_fork_workspace_size.restype = ctypes.c_size_t
+    lib.kda_page_compact.argtypes = [pool, stores, i64, vp, vp, ctypes.c_size_t, vp]
+    lib.kda_page_compact.restype = ctypes.c_int
+    lib.kda_page_compact_workspace_size.argtypes = [i64]
+    lib.kda_page_compact_workspace_size.restype = ctypes.c_size_t
+    lib.kda_page_free.argtypes = [pool, vp, vp]
+    lib.kda_page_free.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error_detail.argtypes = []

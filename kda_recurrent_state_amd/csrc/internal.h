@@ -36,4 +36,19 @@ size_t chunk_prefill_workspace_bytes(int64_t T, int64_t N, int64_t H, int64_t K,
 // scratch array (KDA_NOALLOC_SCRATCH_BYTES bytes), looked up once per device.
 hipError_t noalloc_scratch(void** ptr);
 
+// Latent attention; arguments already validated.
+hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t stream);
+hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t stream);
+size_t latent_decode_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L);
+
+// Page pool operators; arguments already validated.
+hipError_t launch_page_fork(const kda_page_pool_t& a, const kda_page_store_t* stores, int64_t num_stores,
+                            const void* src, const void* dst, bool index64, int64_t num_forks, bool share,
+                            int32_t* status, void* workspace, hipStream_t stream);
+size_t page_fork_workspace_bytes(int64_t num_forks, int64_t max_pages, int64_t num_pages, bool share);
+hipError_t launch_page_compact(const kda_page_pool_t& a, const kda_page_store_t* stores, int64_t num_stores,
+                               int32_t* live, void* workspace, hipStream_t stream);
+size_t page_compact_workspace_bytes(int64_t num_pages);
+hipError_t launch_page_free(const kda_page_pool_t& a, const uint8_t* release, hipStream_t stream);
+
 }  // namespace kda

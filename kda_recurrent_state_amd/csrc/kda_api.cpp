@@ -6,6 +6,7 @@
 // synchronisation, no environment scan, no conversion of int32 indices; a bad
 // layout returns an error and enqueues nothing; an empty selection validates
 // the cache view and enqueues nothing.
+#include <math.h>
 #include <string.h>
 
 #include "internal.h"
@@ -294,6 +295,232 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
                                         int64_t num_selected, const uint8_t* flags, void* packed,
                                         kda_dtype_t packed_dtype, void* stream) {
   return int8_common(false, store, indices, index_type, num_selected, flags, packed, packed_dtype, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxSpan = (int64_t)1 << 46;  // elements a tensor may span
+
+bool aligned(const void* p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
+// Span in elements of a tensor with a dense last dim of ``last`` elements and
+// ``n`` outer dims; false if a stride is negative or no multiple of 8, or the
+// span passes kMaxSpan.
+bool outer_span(const int64_t* size, const int64_t* stride, int n, int64_t last, int64_t* span) {
+  int64_t end = last;
+  for (int i = 0; i < n; ++i) {
+    if (size[i] == 1) continue;  // its stride plays no part
+    if (stride[i] < 0 || stride[i] % 8 != 0) return false;
+    if (stride[i] > 0 && size[i] - 1 > (kMaxSpan - end) / stride[i]) return false;
+    end += (size[i] - 1) * stride[i];
+  }
+  *span = end;
+  return true;
+}
+
+bool dim8(int64_t x, int64_t lo, int64_t hi) { return x >= lo && x <= hi && x % 8 == 0; }
+
+kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
+  if (!a) return KDA_E_NULL;
+  if (a->T < 0 || a->S < 0 || a->N < 0 || a->H <= 0 || a->D <= 0 || a->R < 0 || a->E <= 0) return KDA_E_SHAPE;
+  if (a->N == 0 && a->T != 0) return KDA_E_SHAPE;
+  if (a->dtype != KDA_BF16) return KDA_E_DTYPE;
+  if (!dim8(a->D, 8, 128) || !dim8(a->R, 0, 64) || !dim8(a->E, 8, 128)) return KDA_E_UNSUPPORTED;
+  if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
+  if (a->T > 0x7fffffff || a->S > 0x7fffffff || a->H > 65536) return KDA_E_UNSUPPORTED;
+  // one workgroup for each 32 queries of a head at least: the grid stays in 31 bits
+  if ((a->T / 32 + a->N + 1) > (int64_t)0x7fffff00 / a->H) return KDA_E_UNSUPPORTED;
+  if (a->T == 0 || a->N == 0) return KDA_OK;
+  if (!a->q || !a->cu_seqlens_q || !a->cu_seqlens_k || !a->out) return KDA_E_NULL;
+  if (a->S > 0 && (!a->k || !a->v || (a->R > 0 && !a->k_rope))) return KDA_E_NULL;
+  int64_t qn = 0, kn = 0, rn = 0, vn = 0;
+  const int64_t th[2] = {a->T, a->H}, sh[2] = {a->S > 0 ? a->S : 1, a->H};
+  if (!outer_span(th, a->q_stride, 2, a->D + a->R, &qn) || !outer_span(sh, a->k_stride, 2, a->D, &kn) ||
+      !outer_span(sh, a->v_stride, 2, a->E, &vn) || (a->R > 0 && !outer_span(sh, &a->k_rope_stride, 1, a->R, &rn)))
+    return KDA_E_LAYOUT;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || (a->R > 0 && !aligned(a->k_rope, 16)) ||
+      !aligned(a->out, 8))
+    return KDA_E_LAYOUT;
+  if (a->S == 0) kn = vn = rn = 0;
+  const Span ins[6] = {{a->q, qn * 2},
+                       {a->k, kn * 2},
+                       {a->R > 0 ? a->k_rope : nullptr, rn * 2},
+                       {a->v, vn * 2},
+                       {a->cu_seqlens_q, (a->N + 1) * 4},
+                       {a->cu_seqlens_k, (a->N + 1) * 4}};
+  const Span outs[2] = {{a->out, a->T * a->H * a->E * 2}, {a->lse, a->T * a->H * 4}};
+  const int same[2] = {-1, -1};
+  return alias_error(outs, same, 2, ins, 6) ? KDA_E_ALIAS : KDA_OK;
+}
+
+kda_status_t check_latent_decode(const kda_latent_decode_args_t* a) {
+  if (!a) return KDA_E_NULL;
+  if (a->N < 0 || a->Q <= 0 || a->H <= 0 || a->L <= 0 || a->R < 0) return KDA_E_SHAPE;
+  if (a->num_pages <= 0 || a->page_size <= 0 || a->max_pages <= 0) return KDA_E_SHAPE;
+  if (a->dtype != KDA_BF16) return KDA_E_DTYPE;
+  if (!dim8(a->L, 8, 512) || !dim8(a->R, 0, 64)) return KDA_E_UNSUPPORTED;
+  if (a->Q > 1024 || a->H > 1024 || a->Q * a->H > 1024) return KDA_E_UNSUPPORTED;
+  if (a->N > 65535) return KDA_E_UNSUPPORTED;  // sequences are a grid dimension
+  if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 30, row = a->L + a->R;
+  if (a->page_size > most || a->max_pages > most / a->page_size || a->num_pages > 0x7fffffff) return KDA_E_UNSUPPORTED;
+  if (a->N > 1 && a->table_stride < a->max_pages) return KDA_E_OVERLAP;
+  if (a->page_stride < a->page_size * row) return KDA_E_OVERLAP;
+  if (a->page_stride % 8 != 0) return KDA_E_LAYOUT;
+  if (a->page_stride > kMaxSpan / a->num_pages || (a->N > 1 && a->table_stride > kMaxSpan / a->N)) return KDA_E_SHAPE;
+  if (a->N == 0) return KDA_OK;
+  if (!a->cache || !a->page_table || !a->lengths || !a->q || (a->R > 0 && !a->q_rope) || !a->out) return KDA_E_NULL;
+  const int64_t nqh[3] = {a->N, a->Q, a->H};
+  int64_t qn = 0, rn = 0;
+  if (!outer_span(nqh, a->q_stride, 3, a->L, &qn) || (a->R > 0 && !outer_span(nqh, a->q_rope_stride, 3, a->R, &rn)))
+    return KDA_E_LAYOUT;
+  if (!aligned(a->cache, 16) || !aligned(a->q, 16) || (a->R > 0 && !aligned(a->q_rope, 16)) || !aligned(a->out, 16))
+    return KDA_E_LAYOUT;
+  const size_t need = kda::latent_decode_workspace_bytes(a->N, a->Q, a->H, a->L);
+  if (!a->workspace || a->workspace_bytes < need) return KDA_E_WORKSPACE;
+  if (!aligned(a->workspace, 16)) return KDA_E_LAYOUT;
+  const int64_t rows = a->N * a->Q * a->H;
+  const Span ins[5] = {{a->cache, ((a->num_pages - 1) * a->page_stride + a->page_size * row) * 2},
+                       {a->page_table, ((a->N - 1) * a->table_stride + a->max_pages) * 4},
+                       {a->lengths, a->N * 4},
+                       {a->q, qn * 2},
+                       {a->R > 0 ? a->q_rope : nullptr, rn * 2}};
+  const Span outs[3] = {{a->out, rows * a->L * 2}, {a->lse, rows * 4}, {a->workspace, (int64_t)need}};
+  const int same[3] = {-1, -1, -1};
+  return alias_error(outs, same, 3, ins, 5) ? KDA_E_ALIAS : KDA_OK;
+}
+
+kda_status_t check_pool(const kda_page_pool_t* p, Span* spans) {
+  if (!p) return KDA_E_NULL;
+  if (p->num_seqs <= 0 || p->max_pages <= 0 || p->num_pages <= 0 || p->page_size <= 0) return KDA_E_SHAPE;
+  if (p->num_seqs > ((int64_t)1 << 24) || p->max_pages > ((int64_t)1 << 20) || p->num_pages > ((int64_t)1 << 30) ||
+      p->page_size > ((int64_t)1 << 30))
+    return KDA_E_UNSUPPORTED;
+  if (p->num_seqs > 1 && p->table_stride < p->max_pages) return KDA_E_OVERLAP;
+  if (p->num_seqs > 1 && p->table_stride > kMaxSpan / p->num_seqs) return KDA_E_SHAPE;
+  if (!p->table || !p->lengths || !p->refs) return KDA_E_NULL;
+  spans[0] = {p->table, ((p->num_seqs - 1) * p->table_stride + p->max_pages) * 4};
+  spans[1] = {p->lengths, p->num_seqs * 4};
+  spans[2] = {p->refs, p->num_pages * 4};
+  return KDA_OK;
+}
+
+kda_status_t check_stores(const kda_page_store_t* s, int64_t n, int64_t num_pages) {
+  if (n < 0) return KDA_E_SHAPE;
+  if (n > 4096) return KDA_E_UNSUPPORTED;
+  if (n > 0 && !s) return KDA_E_NULL;
+  for (int64_t i = 0; i < n; ++i) {
+    if (s[i].page_bytes <= 0) return KDA_E_SHAPE;
+    if (s[i].page_stride < s[i].page_bytes) return KDA_E_OVERLAP;
+    if (s[i].page_stride > kMaxSpan / num_pages) return KDA_E_SHAPE;
+    if (!s[i].data) return KDA_E_NULL;
+  }
+  return KDA_OK;
+}
+
+Span store_span(const kda_page_store_t& s, int64_t num_pages) {
+  return {s.data, (num_pages - 1) * s.page_stride + s.page_bytes};
+}
+
+// Whether the stores overlap one another or one of ``spans``.
+bool stores_alias(const kda_page_store_t* s, int64_t n, int64_t num_pages, const Span* spans, int num_spans) {
+  for (int64_t i = 0; i < n; ++i) {
+    const Span a = store_span(s[i], num_pages);
+    for (int j = 0; j < num_spans; ++j)
+      if (spans_overlap(a, spans[j])) return true;
+    for (int64_t j = 0; j < i; ++j)
+      if (spans_overlap(a, store_span(s[j], num_pages))) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* a, void* stream) {
+  const kda_status_t st = check_latent_prefill(a);
+  if (st != KDA_OK || a->T == 0 || a->N == 0) return st;
+  return hip_status("kda_latent_prefill launch", kda::launch_latent_prefill(*a, static_cast<hipStream_t>(stream)));
+}
+
+size_t kda_latent_decode_workspace_size(int64_t N, int64_t Q, int64_t H, int64_t L) {
+  if (N <= 0 || Q <= 0 || H <= 0 || L <= 0 || Q > 1024 || H > 1024 || Q * H > 1024 || L > 512) return 0;
+  return kda::latent_decode_workspace_bytes(N, Q, H, L);
+}
+
+kda_status_t kda_latent_decode(const kda_latent_decode_args_t* a, void* stream) {
+  const kda_status_t st = check_latent_decode(a);
+  if (st != KDA_OK || a->N == 0) return st;
+  return hip_status("kda_latent_decode launch", kda::launch_latent_decode(*a, static_cast<hipStream_t>(stream)));
+}
+
+size_t kda_page_fork_workspace_size(int64_t num_forks, int64_t max_pages, int64_t num_pages, int share) {
+  if (num_forks <= 0 || max_pages <= 0 || num_pages <= 0) return 0;
+  return kda::page_fork_workspace_bytes(num_forks, max_pages, num_pages, share != 0);
+}
+
+kda_status_t kda_page_fork(const kda_page_pool_t* pool, const kda_page_store_t* stores, int64_t num_stores,
+                           const void* src, const void* dst, kda_index_t it, int64_t num_forks, int share,
+                           int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  Span spans[7];
+  kda_status_t st = check_pool(pool, spans);
+  if (st != KDA_OK) return st;
+  if ((st = check_stores(stores, num_stores, pool->num_pages)) != KDA_OK) return st;
+  if (it != KDA_I32 && it != KDA_I64) return KDA_E_DTYPE;
+  if (num_forks < 0) return KDA_E_SHAPE;
+  if (num_forks > ((int64_t)1 << 24)) return KDA_E_UNSUPPORTED;
+  if (num_forks == 0) return KDA_OK;
+  if (!src || !dst || !status) return KDA_E_NULL;
+  const size_t need = kda::page_fork_workspace_bytes(num_forks, pool->max_pages, pool->num_pages, share != 0);
+  if (!workspace || workspace_bytes < need) return KDA_E_WORKSPACE;
+  if (!aligned(workspace, 4)) return KDA_E_LAYOUT;
+  spans[3] = {status, num_forks * 4};
+  spans[4] = {workspace, (int64_t)need};
+  spans[5] = {src, num_forks * (it == KDA_I64 ? 8 : 4)};
+  spans[6] = {dst, num_forks * (it == KDA_I64 ? 8 : 4)};
+  const int none[5] = {-1, -1, -1, -1, -1};
+  if (alias_error(spans, none, 5, spans + 5, 2) || stores_alias(stores, num_stores, pool->num_pages, spans, 7))
+    return KDA_E_ALIAS;
+  return hip_status("kda_page_fork launch",
+                    kda::launch_page_fork(*pool, stores, num_stores, src, dst, it == KDA_I64, num_forks, share != 0,
+                                          status, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t kda_page_compact_workspace_size(int64_t num_pages) {
+  return num_pages <= 0 ? 0 : kda::page_compact_workspace_bytes(num_pages);
+}
+
+kda_status_t kda_page_compact(const kda_page_pool_t* pool, const kda_page_store_t* stores, int64_t num_stores,
+                              int32_t* live, void* workspace, size_t workspace_bytes, void* stream) {
+  Span spans[5];
+  kda_status_t st = check_pool(pool, spans);
+  if (st != KDA_OK) return st;
+  if ((st = check_stores(stores, num_stores, pool->num_pages)) != KDA_OK) return st;
+  const size_t need = kda::page_compact_workspace_bytes(pool->num_pages);
+  if (!workspace || workspace_bytes < need) return KDA_E_WORKSPACE;
+  if (!aligned(workspace, 4)) return KDA_E_LAYOUT;
+  spans[3] = {live, live ? 4 : 0};
+  spans[4] = {workspace, (int64_t)need};
+  const int none[5] = {-1, -1, -1, -1, -1};
+  if (alias_error(spans, none, 5, spans, 0) || stores_alias(stores, num_stores, pool->num_pages, spans, 5))
+    return KDA_E_ALIAS;
+  return hip_status("kda_page_compact launch",
+                    kda::launch_page_compact(*pool, stores, num_stores, live, workspace,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+kda_status_t kda_page_free(const kda_page_pool_t* pool, const uint8_t* release, void* stream) {
+  Span spans[4];
+  const kda_status_t st = check_pool(pool, spans);
+  if (st != KDA_OK) return st;
+  if (!release) return KDA_E_NULL;
+  spans[3] = {release, pool->num_seqs};
+  const int none[3] = {-1, -1, -1};
+  if (alias_error(spans, none, 3, spans + 3, 1)) return KDA_E_ALIAS;
+  return hip_status("kda_page_free launch", kda::launch_page_free(*pool, release, static_cast<hipStream_t>(stream)));
 }
 
 const char* kda_status_string(kda_status_t s) {

@@ -1,0 +1,341 @@
+"""Latent attention on the GPU (expanded varlen prefill, absorbed paged
+decode) against plain fp64 evaluations."""
+import math
+
+import pytest
+import torch
+
+from tests import latent_ref as ref
+from tests.helpers import ensure_built
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def _randn(gen, *shape):
+    return torch.randn(*shape, generator=gen).to(BF16)
+
+
+def _cu(lens):
+    out = [0]
+    for n in lens:
+        out.append(out[-1] + n)
+    return out
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# --- prefill ----------------------------------------------------------------
+
+def _prefill_inputs(lq, lk, H, D, R, E, seed=1):
+    gen = torch.Generator().manual_seed(seed)
+    T, S = sum(lq), sum(lk)
+    kv = _randn(gen, S, H, D + E).cuda()
+    rows = _randn(gen, S, 64 + R).cuda() if R else None
+    return dict(q=_randn(gen, T, H, D + R).cuda(), k=kv[..., :D], v=kv[..., D:],
+                k_rope=rows[:, 64:] if R else None)
+
+
+def _prefill(x, lq, lk, causal=True, scale=None, **kw):
+    import kda_recurrent_state_amd as kda
+    return kda.kda_latent_prefill(x["q"], x["k"], x["v"], _i32(_cu(lq)), k_rope=x["k_rope"],
+                                  cu_seqlens_k=_i32(_cu(lk)), causal=causal, scale=scale, with_lse=True, **kw)
+
+
+def _check_prefill(x, lq, lk, causal, got, scale=None):
+    want = ref.prefill(x["q"], x["k"], x["v"], x["k_rope"], _cu(lq), _cu(lk),
+                       x["q"].shape[2] ** -0.5 if scale is None else scale, causal)
+    ref.check(*got, want, "prefill")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,past", [
+    ([1], [0]), ([1], [200]), ([64], [0]), ([65, 1, 63], [0, 0, 0]), ([128, 129, 127, 2], [0, 64, 1, 500]),
+    ([0, 33, 0, 300, 0], [0, 31, 7, 0, 64]), ([517], [1])])
+def test_prefill_lengths(lq, past, causal):
+    lk = [a + b for a, b in zip(lq, past)]
+    x = _prefill_inputs(lq, lk, 2, 128, 64, 128)
+    _check_prefill(x, lq, lk, causal, _prefill(x, lq, lk, causal))
+
+
+@pytest.mark.parametrize("H,D,R,E", [(1, 128, 64, 128), (5, 64, 32, 64), (3, 128, 0, 128), (2, 96, 32, 80),
+                                     (2, 8, 0, 8), (4, 8, 8, 128), (3, 120, 56, 24), (2, 64, 64, 128)])
+def test_prefill_dims(H, D, R, E):
+    lq, lk = [70, 5, 200], [70, 90, 201]
+    x = _prefill_inputs(lq, lk, H, D, R, E)
+    _check_prefill(x, lq, lk, True, _prefill(x, lq, lk, True))
+
+
+def test_prefill_rows_that_see_nothing():
+    # more queries than keys: the first ones see none; and a sequence without keys
+    lq, lk = [100, 40, 70], [30, 0, 70]
+    x = _prefill_inputs(lq, lk, 3, 128, 64, 128)
+    out, lse = _prefill(x, lq, lk, True)
+    _check_prefill(x, lq, lk, True, (out, lse))
+    assert (out[:70] == 0).all() and (lse[:70] == -math.inf).all()
+    assert (out[100:140] == 0).all() and (lse[100:140] == -math.inf).all()
+
+
+def test_prefill_large_scores_and_scale():
+    # scores of several hundred: one weight takes all, the running maximum jumps
+    lq = lk = [150, 90]
+    x = _prefill_inputs(lq, lk, 2, 128, 64, 128)
+    x["q"] = x["q"] * 8
+    # (|s| reaches about 500: its fp32 rounding alone moves a weight by 2^-14,
+    # inside the bound's 2^-12; lse is held to 1e-4 as 500 x 2^-24 = 3e-5)
+    _check_prefill(x, lq, lk, True, _prefill(x, lq, lk, True, scale=0.5), scale=0.5)
+
+
+def test_prefill_strides_and_other_rows():
+    """Token and head strides of every tensor, a broadcast rotary key, and rows
+    of q before and behind the sequences, whose outputs stay as they were."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(3)
+    H, D, R, E, T, S = 3, 64, 16, 40, 200, 180
+    q = _randn(gen, H, T, 96).cuda().transpose(0, 1)[..., 8:8 + D + R]
+    k = _randn(gen, H, S, D).cuda().transpose(0, 1)
+    v = _randn(gen, S, 1, E).cuda().expand(S, H, E)
+    kr = _randn(gen, 1, R).cuda().expand(S, R)
+    cu_q, cu_k = [10, 60, 60, 187], [20, 70, 75, 180]
+    out = torch.full((T, H, E), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    kda.kda_latent_prefill(q, k, v, _i32(cu_q), k_rope=kr, cu_seqlens_k=_i32(cu_k), out=out, lse=lse, scale=0.1)
+    want = ref.prefill(q, k, v, kr, cu_q, cu_k, 0.1, True)
+    ref.check(out[10:187], lse[10:187], [w[10:187] for w in want], "strided")
+    assert (out[:10] == 7).all() and (out[187:] == 7).all() and (lse[:10] == 7).all() and (lse[187:] == 7).all()
+
+
+def test_prefill_unseen_keys_may_be_anything():
+    """NaN and infinities in keys that a query does not see, in value rows
+    behind a sequence, and in the padding between sequences."""
+    import kda_recurrent_state_amd as kda
+    lq, lk = [100, 30], [100, 50]
+    x = _prefill_inputs(lq, [100, 50, 60], 2, 128, 64, 128)
+    for t, bad in ((x["k"], math.nan), (x["v"], math.inf), (x["k_rope"], math.nan)):
+        t[150:] = bad
+    x["k"][80:100] = math.inf
+    x["k_rope"][90:100] = math.nan
+    out, lse = kda.kda_latent_prefill(x["q"], x["k"], x["v"], _i32(_cu(lq)), k_rope=x["k_rope"],
+                                      cu_seqlens_k=_i32(_cu(lk)), with_lse=True)
+    want = ref.prefill(x["q"], x["k"], x["v"], x["k_rope"], _cu(lq), _cu(lk), 192 ** -0.5, True)
+    for a, b in ((0, 80), (100, 130)):
+        ref.check(out[a:b], lse[a:b], [w[a:b] for w in want], "unseen %d" % a)
+
+
+def test_prefill_bad_offsets_stay_inside():
+    """Offsets outside the tensors are clamped: the call ends and the sound
+    sequence is right."""
+    import kda_recurrent_state_amd as kda
+    x = _prefill_inputs([90], [90], 2, 64, 32, 64)
+    out = torch.zeros(90, 2, 64, dtype=BF16, device="cuda")
+    kda.kda_latent_prefill(x["q"], x["k"], x["v"], _i32([0, 50, 4000, -7, 90]), k_rope=x["k_rope"],
+                           cu_seqlens_k=_i32([0, 50, 9000, 60, -1]), out=out)
+    torch.cuda.synchronize()
+    want = ref.prefill(x["q"][:50], x["k"][:50], x["v"][:50], x["k_rope"][:50], [0, 50], [0, 50], 96 ** -0.5, True)
+    ref.check(out[:50], None, want, "clamped")
+
+
+def test_prefill_many_sequences():
+    # more sequences than one scan step of a wave, most of them tiny
+    lq = [(7 * i) % 5 for i in range(150)] + [140, 1]
+    lk = [n + (i % 3) for i, n in enumerate(lq)]
+    x = _prefill_inputs(lq, lk, 2, 64, 32, 64)
+    _check_prefill(x, lq, lk, True, _prefill(x, lq, lk, True))
+
+
+def test_prefill_is_repeatable_and_follows_a_side_stream():
+    lq, lk = [300, 77], [400, 77]
+    x = _prefill_inputs(lq, lk, 4, 128, 64, 128)
+    one = _prefill(x, lq, lk)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    two = _prefill(x, lq, lk, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+
+
+# --- decode -----------------------------------------------------------------
+
+def _decode_inputs(lens, Q, H, L, R, page, seed=2, width=None, gap=0):
+    gen = torch.Generator().manual_seed(seed)
+    N = len(lens)
+    used = [-(-max(n, 0) // page) for n in lens]
+    width = width or max(used) + 1
+    pages = sum(used) + 3
+    perm = torch.randperm(pages, generator=gen).tolist()
+    table = torch.full((N, width), -1, dtype=torch.int32)
+    at = 0
+    for n, u in enumerate(used):
+        table[n, :u] = torch.tensor(perm[at:at + u], dtype=torch.int32)
+        at += u
+    flat = _randn(gen, pages, page * (L + R) + gap).cuda()
+    cache = torch.as_strided(flat, (pages, page, L + R), (page * (L + R) + gap, L + R, 1))
+    return dict(cache=cache, table=table.cuda(), lens=_i32(lens), q=_randn(gen, N, Q, H, L).cuda(),
+                q_rope=_randn(gen, N, Q, H, R).cuda() if R else None)
+
+
+def _decode(x, scale=0.07, **kw):
+    import kda_recurrent_state_amd as kda
+    return kda.kda_latent_decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], scale=scale, with_lse=True,
+                                 **kw)
+
+
+def _check_decode(x, got, scale=0.07, name="decode"):
+    ref.check(*got, ref.decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], scale), name)
+
+
+@pytest.mark.parametrize("lens", [[1], [64], [65], [0], [1000], [3, 0, 130, 64, 0, 1], [700, 63, 2000],
+                                  [40] * 70, [1] * 300])
+@pytest.mark.parametrize("H", [3, 32])
+def test_decode_lengths(lens, H):
+    x = _decode_inputs(lens, 1, H, 512, 64, 64)
+    _check_decode(x, _decode(x))
+
+
+@pytest.mark.parametrize("Q,H,L,R,page", [(1, 1, 512, 64, 16), (2, 8, 256, 32, 48), (3, 20, 128, 64, 1),
+                                          (1, 128, 512, 64, 64), (1, 40, 384, 0, 128), (4, 5, 8, 8, 7),
+                                          (2, 64, 504, 56, 33), (1, 16, 136, 0, 64), (5, 1, 256, 64, 200),
+                                          (1, 17, 512, 64, 64)])
+def test_decode_dims(Q, H, L, R, page):
+    x = _decode_inputs([300, 1, 2, 77, 129], Q, H, L, R, page)
+    _check_decode(x, _decode(x))
+
+
+def test_decode_long_context_is_split():
+    x = _decode_inputs([30000, 5], 1, 32, 512, 64, 64)
+    _check_decode(x, _decode(x, scale=0.3), scale=0.3)
+
+
+def test_decode_queries_before_the_first_token():
+    # three new tokens, lengths 0 .. 3: the first queries see nothing
+    x = _decode_inputs([0, 1, 2, 3], 3, 4, 512, 64, 64)
+    out, lse = _decode(x)
+    _check_decode(x, (out, lse))
+    assert (out[1, :2] == 0).all() and (lse[1, :2] == -math.inf).all() and (out[0] == 0).all()
+
+
+def test_decode_bad_pages_and_lengths():
+    """Table entries outside the pool are not seen (a whole tile of them too),
+    lengths outside the table are clamped."""
+    x = _decode_inputs([500, 300, 128, 90], 2, 8, 512, 64, 16)
+    x["table"][0, 3] = -1
+    x["table"][0, 8:12] = 1 << 30
+    x["table"][2, :] = -5
+    x["lens"][1] = 1 << 29
+    x["lens"][3] = -4
+    out, lse = _decode(x)
+    _check_decode(x, (out, lse))
+    assert (out[2] == 0).all() and (lse[2] == -math.inf).all() and (out[3] == 0).all()
+
+
+def test_decode_rows_behind_the_length_may_be_anything():
+    x = _decode_inputs([70, 130, 10], 1, 16, 512, 64, 64, gap=64)
+    used = {(int(x["table"][n, j // 64]), j % 64) for n, k in enumerate([70, 130, 10]) for j in range(k)}
+    mask = torch.ones(x["cache"].shape[:2], dtype=torch.bool)
+    for p, s in used:
+        mask[p, s] = False
+    want = ref.decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], 0.07)
+    x["cache"][mask.cuda()] = math.nan
+    ref.check(*_decode(x), want, "behind")
+
+
+def test_decode_strides():
+    """q as the transposed result of a product by head, q_rope as the end of a
+    joint projection, pages with a gap, rows of a wider table, 3-D q."""
+    import kda_recurrent_state_amd as kda
+    x = _decode_inputs([100, 217, 64], 1, 12, 256, 32, 16, gap=24, width=40)
+    gen = torch.Generator().manual_seed(9)
+    q = _randn(gen, 12, 3, 256).cuda().transpose(0, 1)
+    q_rope = _randn(gen, 3, 12, 96).cuda()[..., 64:]
+    table = x["table"][:, :20]
+    out, lse = kda.kda_latent_decode(x["cache"], table, x["lens"], q, q_rope, scale=0.1, with_lse=True)
+    assert out.shape == (3, 12, 256) and lse.shape == (3, 12)
+    ref.check(out, lse, ref.decode(x["cache"], table, x["lens"], q[:, None], q_rope[:, None], 0.1), "strided")
+
+
+def test_decode_cache_beyond_four_gib():
+    """Pages far apart: row addresses pass 32 bits."""
+    stride = (1 << 31) // 2 + 8 * 64   # elements: 2 GiB and a gap from page to page
+    flat = torch.zeros(5 * stride + 16 * 144, dtype=BF16, device="cuda")
+    cache = torch.as_strided(flat, (6, 16, 144), (stride, 144, 1))
+    gen = torch.Generator().manual_seed(4)
+    cache.copy_(_randn(gen, 6, 16, 144))
+    x = dict(cache=cache, table=_i32([[5, 0, 3], [4, 1, 2]]), lens=_i32([48, 33]),
+             q=_randn(gen, 2, 1, 4, 128).cuda(), q_rope=_randn(gen, 2, 1, 4, 16).cuda())
+    _check_decode(x, _decode(x))
+
+
+def test_decode_graph_follows_lengths_and_table():
+    """A captured call replayed with other lengths, pages and queries between
+    eager calls; two graphs with workspaces of their own."""
+    import kda_recurrent_state_amd as kda
+    x = _decode_inputs([300, 20, 700], 1, 32, 512, 64, 64, width=32)
+    out = torch.empty_like(x["q"])
+    ws = [torch.empty(kda.kda_latent_decode_workspace_size(3, 1, 32, 512), dtype=torch.uint8, device="cuda")
+          for _ in range(2)]
+    outs = [torch.empty_like(x["q"]) for _ in range(2)]
+    _decode(x, out=out)
+    graphs = []
+    for w, o in zip(ws, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kda.kda_latent_decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], scale=0.07, out=o,
+                                  workspace=w)
+        graphs.append(g)
+    gen = torch.Generator().manual_seed(8)
+    for lens in ([300, 20, 700], [1, 0, 64], [901, 65, 3], [500, 500, 500]):
+        x["lens"].copy_(_i32(lens))
+        x["table"].copy_(torch.randint(0, x["cache"].shape[0], x["table"].shape, generator=gen, dtype=torch.int32))
+        x["q"].copy_(_randn(gen, *x["q"].shape))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        eager = _decode(x, out=out)[0].clone()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], eager) and torch.equal(outs[1], eager)
+        _check_decode(x, (eager, None), name="graph %s" % lens)
+
+
+def test_decode_on_a_side_stream_and_shared_pages():
+    # two sequences share pages (a forked prefix); the binding allocates on the side stream's behalf
+    x = _decode_inputs([200, 260], 1, 32, 512, 64, 64)
+    x["table"][1, :3] = x["table"][0, :3]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = _decode(x, stream=side)
+    torch.cuda.synchronize()
+    _check_decode(x, got)
+
+
+def test_decode_matches_the_expanded_form():
+    """One head's up-projections applied on either side: absorbed decode of the
+    last token equals expanded prefill of it, up to both roundings."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(11)
+    T, H, L, R, D, E = 150, 4, 512, 64, 128, 128
+    c = torch.randn(T, L, generator=gen).to(BF16)
+    kr = _randn(gen, T, R)
+    uk = (torch.randn(H, D, L, generator=gen) * L ** -0.5)
+    uv = (torch.randn(H, E, L, generator=gen) * L ** -0.5)
+    qn, qr = torch.randn(1, H, D, generator=gen), _randn(gen, 1, H, R)
+    scale = (D + R) ** -0.5
+    k = torch.einsum("tl,hdl->thd", c.float(), uk)
+    v = torch.einsum("tl,hel->the", c.float(), uv)
+    exp_out, _ = kda.kda_latent_prefill(torch.cat([qn.to(BF16), qr], -1).cuda(), k.to(BF16).cuda(), v.to(BF16).cuda(),
+                                        _i32([0, 1]), k_rope=kr.cuda(), cu_seqlens_k=_i32([0, T]))
+    ql = torch.einsum("nhd,hdl->nhl", qn.to(BF16).float(), uk).to(BF16)
+    cache = torch.zeros(3, 64, L + R, dtype=BF16)
+    cache.view(192, L + R)[:T] = torch.cat([c, kr], -1)
+    lat, _ = kda.kda_latent_decode(cache.cuda(), _i32([[0, 1, 2]]), _i32([T]), ql.cuda(), qr.cuda(), scale=scale)
+    abs_out = torch.einsum("nhl,hel->nhe", lat.float().cpu(), uv)
+    # roundings to bf16 (2^-8 each at most) on the way: k or q_latent (moves a
+    # score by up to 2^-8 of sum |q k| / ..., here under 0.02), v, weights, latent
+    # output, output: 5 x 2^-8 = 0.02 and the scores' 0.02 of |v| of order 1
+    assert (abs_out - exp_out.float().cpu()).abs().max() <= 0.04
