@@ -26,7 +26,20 @@ __device__ __forceinline__ void load_lds16(const void* g, void* lds) {
 }
 
 // Waits for the wave's loads to LDS (a barrier then shows them to the others).
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0, the other counters free
+  asm volatile("" ::: "memory");
+}
+
+// Barrier of the workgroup for LDS: the wave's LDS accesses are done, its
+// loads (to registers or to LDS) may still be under way.  (__syncthreads
+// waits for those too, which would end every prefetch at the next barrier.)
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0, the other counters free
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // Transposed 8-byte LDS read: in each group of 16 lanes, lane i reads the four
 // bf16 of row i / 4, columns 4 (i % 4) .. + 3 of a 4 x 16 block (its address
@@ -35,12 +48,24 @@ __device__ __forceinline__ s16x4 read_tr(const void* lds) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lds);
 }
 
+// x, as a value the compiler cannot trace: what is computed from it inside a
+// loop stays there and does not occupy registers around it.
+__device__ __forceinline__ int keep_here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ bf16x8 join(const s16x4& lo, const s16x4& hi) {
   typedef short s16x8 __attribute__((ext_vector_type(8)));
   return __builtin_bit_cast(bf16x8, (s16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The scheduler moves nothing across this.  By itself it puts each LDS read
+// right before the product that needs it and waits for it, so the product
+// loops read the next operands between two of these.
+__device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // x combined with the lane 32 (16) further on, the same bits in both
 __device__ __forceinline__ float max_halves(float x) {

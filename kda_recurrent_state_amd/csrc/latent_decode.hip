@@ -25,13 +25,16 @@ namespace {
 using namespace latent;
 
 constexpr int kTile = 64;      // tokens a tile
-constexpr int kThreads = 256;  // 4 waves
+constexpr int kThreads = 512;  // 8 waves
+constexpr int kWaves = kThreads / 64;
 
 struct DecodeParams {
   const __bf16* cache;
   int64_t page_stride;  // elements
   int64_t num_pages;
   int page_size, L, R;
+  uint32_t page_mul;  // j / page_size = j page_mul >> page_shift, 0 <= j < 2^31
+  int page_shift;
   const int32_t* table;
   int64_t table_stride;
   int max_pages;
@@ -43,9 +46,10 @@ struct DecodeParams {
   __bf16* out;
   float* lse;
   int N, Q, H, rows, row_blocks, groups;
-  float scale2;   // scale log2 e
-  float* part;    // [row_blocks][2 groups][MB][L] normalised outputs
-  float* plse;    // [row_blocks][2 groups][MB] log2 of the sums
+  float scale2;    // scale log2 e
+  float* part;     // [row_blocks][2 groups][MB][L] normalised outputs
+  float* plse;     // [row_blocks][2 groups][MB] log2 of the sums
+  int32_t* shared; // [N][2] first and last share of a sequence
 };
 
 __device__ __forceinline__ int seq_tokens(const DecodeParams& p, int n) {
@@ -53,20 +57,20 @@ __device__ __forceinline__ int seq_tokens(const DecodeParams& p, int n) {
   const int64_t room = (int64_t)p.max_pages * p.page_size;
   return len < 0 ? 0 : (len > room ? (int)room : len);
 }
-__device__ __forceinline__ int seq_tiles(const DecodeParams& p, int n) {
-  return (int)(((int64_t)seq_tokens(p, n) + kTile - 1) / kTile);
-}
+__device__ __forceinline__ int tiles_of(int tokens) { return (int)(((int64_t)tokens + kTile - 1) / kTile); }
 
 // Sum of the sequences' tiles, the same in all threads.
 __device__ int64_t total_tiles(const DecodeParams& p, int64_t* red) {
   int64_t mine = 0;
-  for (int n = threadIdx.x; n < p.N; n += kThreads) mine += seq_tiles(p, n);
+  for (int n = threadIdx.x; n < p.N; n += kThreads) mine += tiles_of(seq_tokens(p, n));
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) mine += __shfl_xor(mine, d, 64);
-  __syncthreads();
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mine;
   __syncthreads();
-  return red[0] + red[1] + red[2] + red[3];
+  int64_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) all += red[i];
+  return all;
 }
 
 // The sequence that holds tile x of the line, and the line position of its
@@ -74,7 +78,7 @@ __device__ int64_t total_tiles(const DecodeParams& p, int64_t* red) {
 __device__ void find_tile(const DecodeParams& p, int64_t x, int lane, int* seq, int64_t* first) {
   int64_t base = 0;
   for (int n0 = 0; n0 < p.N; n0 += 64) {
-    const int c = n0 + lane < p.N ? seq_tiles(p, n0 + lane) : 0;
+    const int c = n0 + lane < p.N ? tiles_of(seq_tokens(p, n0 + lane)) : 0;
     const int incl = wave_scan(c, lane);
     const unsigned long long past = __ballot(base + incl > x);
     if (past) {
@@ -89,25 +93,133 @@ __device__ void find_tile(const DecodeParams& p, int64_t x, int lane, int* seq, 
   *first = base;
 }
 
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t lane64(int64_t x, int src) {  // src is uniform
+  const int lo = __builtin_amdgcn_readlane((int)x, src), hi = __builtin_amdgcn_readlane((int)(x >> 32), src);
+  return ((int64_t)hi << 32) | (unsigned)lo;
+}
+
 // LP, RP: L and R rounded up to what the kernel is built for; NB: blocks of 16
 // query rows a workgroup.
 template <int LP, int RP, int NB>
-__global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeParams p) {
-  constexpr int MB = 16 * NB;
-  constexpr int DP = LP + RP;
-  constexpr int KC = DP / 8;        // 16-byte chunks of a staged row
-  constexpr int KS = DP / 32;       // contraction steps of the scores
-  constexpr int MT = LP / 64;       // 16-column blocks of the output a wave
-  constexpr int TB = NB;            // 16-token blocks a wave scores
-  // staged row r: chunk c at position c ^ (r & 7), so that the 16 rows x 16 B
-  // of a score operand and the 4 rows x 32 B of a transposed value read both
-  // fall on distinct banks
-  __shared__ __attribute__((aligned(16))) __bf16 tile[kTile * DP];
+struct Decode {
+  static constexpr int MB = 16 * NB;
+  static constexpr int DP = LP + RP;
+  static constexpr int LC = LP / 8;               // 16-byte chunks of a staged latent row
+  static constexpr int KS = DP / 32;              // contraction steps of the scores
+  static constexpr int MT = LP / (16 * kWaves);   // 16-column blocks of the output a wave
+  static constexpr int TG = NB >= 4 ? kWaves / NB : 4;  // groups of tokens the waves score
+  static constexpr int TB = kTile / 16 / TG;      // 16-token blocks a wave scores
+  static constexpr int kScoring = NB * TG;        // waves that score (4 of 8 with NB == 1)
+  static constexpr int kStage = kTile * DP;       // elements of a staged tile
+  static constexpr int kRows = kTile / kWaves;    // rows a wave fetches
+
+  // Chunk c of latent row r is staged at position c ^ 2 (r & 7): the 8 rows x
+  // 16 B of a score operand and the 4 rows x 32 B of a transposed value read
+  // then fall on distinct banks.  Rotary rows (128 B) follow the latent rows;
+  // their chunk c is at c ^ ((r >> 1) & 7).
+
+  // Fetches the tile whose rows lie at ``at`` (lane i: token i).
+  static __device__ __forceinline__ void fetch(const DecodeParams& p, int64_t at, int wave, int lane,
+                                               __bf16* __restrict__ buf) {
+    constexpr int RI = 64 / LC;  // rows an instruction covers
+    lane = keep_here(lane);
+#pragma unroll
+    for (int i = 0; i < kRows / RI; ++i) {
+      const int r = i * RI + lane / LC;  // of the wave's rows
+      const int src = (lane & (LC - 1)) ^ ((r & 7) << 1);
+      const int64_t ro = RI == 1 ? lane64(at, wave * kRows + i) : __shfl(at, wave * kRows + r, 64);
+      if (src * 8 < p.L)
+        load_lds16(reinterpret_cast<const char*>(p.cache + ro) + (unsigned)(src * 16),
+                   buf + (wave * kRows + i * RI) * LP);
+    }
+    if (RP > 0) {
+      const int r = lane >> 3, src = (lane & 7) ^ (((wave * kRows + r) >> 1) & 7);
+      const int64_t ro = __shfl(at, wave * kRows + r, 64);
+      if (src * 8 < p.R) load_lds16(p.cache + ro + p.L + src * 8, buf + kTile * LP + wave * kRows * RP);
+    }
+  }
+
+  // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i
+  // of each block.  Operands are read a group ahead of their products.
+  static __device__ __forceinline__ void scores(const __bf16* __restrict__ tile, const bf16x8 (&qf)[KS], int tok0,
+                                                int ln, int lg, f32x4 (&s)[TB]) {
+#pragma unroll
+    for (int j = 0; j < TB; ++j) s[j] = f32x4{0, 0, 0, 0};
+    const int r0 = tok0 + ln;  // block j adds 16: the same position in its row
+    const char* lat = reinterpret_cast<const char*>(tile + r0 * LP);
+    const char* rot = reinterpret_cast<const char*>(tile + kTile * LP + r0 * RP);
+    const int x = (lg ^ ((r0 & 7) << 1)) * 16, y = (lg ^ ((r0 >> 1) & 7)) * 16;
+    constexpr int F = KS * TB, G = 6;
+    bf16x8 kf[2][G];
+    auto read = [&](int g) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int f = g * G + i, k = f / TB, j = f % TB;
+        if (f >= F) continue;
+        const char* at = k < LP / 32 ? lat + (x ^ ((k & 3) * 64)) + (k >> 2) * 256 + j * 16 * LP * 2
+                                     : rot + (y ^ ((k - LP / 32) * 64)) + j * 16 * RP * 2;
+        kf[g & 1][i] = *reinterpret_cast<const bf16x8*>(at);
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int g = 0; g < (F + G - 1) / G; ++g) {
+      if ((g + 1) * G < F) read(g + 1);
+      hold_order();
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int f = g * G + i;
+        if (f < F) s[f % TB] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[g & 1][i], qf[f / TB], s[f % TB], 0, 0, 0);
+      }
+      hold_order();
+    }
+  }
+
+  // out^T[column][row] += rows^T P^T for the wave's columns, the operands read
+  // one block of NB products ahead
+  static __device__ __forceinline__ void values(const __bf16* __restrict__ tile, const __bf16* __restrict__ prob,
+                                                int wave, int ln, int lg, f32x4 (&acc)[MT][NB]) {
+    const int r0 = 8 * lg + (ln >> 2);  // rows r0 and r0 + 4 of each 32
+    const int c0 = wave * (MT * 2) + ((ln & 3) >> 1);
+    const char* rows = reinterpret_cast<const char*>(tile + r0 * LP) + (ln & 1) * 8;
+    constexpr int B = kTile / 32 * MT;
+    bf16x8 pf[2][NB], vf[2];
+    auto weights = [&](int k) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        pf[k & 1][j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kTile + (((4 * k + lg) ^ (ln & 7)) << 3));
+    };
+    auto read = [&](int b) {
+      const int k = b / MT, i = b % MT;
+      const int x = ((c0 + 2 * i) ^ ((r0 & 7) << 1)) * 16;
+      vf[b & 1] = join(read_tr(rows + x + k * 32 * LP * 2), read_tr(rows + (x ^ 128) + (k * 32 + 4) * LP * 2));
+    };
+    weights(0);
+    read(0);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (b + 1 < B) read(b + 1);
+      if (b == (MT > 1 ? 1 : 0)) weights(1);
+      hold_order();
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[b % MT][j] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[b & 1], pf[b / MT][j], acc[b % MT][j], 0, 0, 0);
+      hold_order();
+    }
+  }
+};
+
+template <int LP, int RP, int NB>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_decode_kernel(DecodeParams p) {
+  using D = Decode<LP, RP, NB>;
+  constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG, TB = D::TB;
+  __shared__ __attribute__((aligned(16))) __bf16 stage[2][D::kStage];
   __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kTile];
-  __shared__ float smax[4][16];
-  __shared__ float ssum[4][16];
-  __shared__ int64_t row_at[kTile];
-  __shared__ int64_t red[4];
+  __shared__ float smax[TG][MB];  // of a tile; at a piece's end the sums
+  __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
+  __shared__ int64_t red[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, lg = lane >> 4;
@@ -116,275 +228,293 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeParams
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
   const int rb = idx % p.row_blocks, w = (idx / p.row_blocks) * 8 + xcd;
 
-  const int64_t total = total_tiles(p, red);
+  const int64_t total = lane64(total_tiles(p, red), 0);
   const int64_t shares = total < p.groups ? total : p.groups;  // none is empty
   if (w >= shares) return;
-  int64_t t0 = w * total / shares;
-  const int64_t t1 = (w + 1) * total / shares;
+  const int64_t t0 = w * total / shares;
+  int left = uniform((int)((w + 1) * total / shares - t0));  // tiles of this share not fetched yet
   int n = 0;
   int64_t first = 0;
   find_tile(p, t0, lane, &n, &first);
-  n = __builtin_amdgcn_readfirstlane(n);
+  n = uniform(n);
 
   if (p.L < LP || p.R < RP) {  // padding columns are zero from here on
-    for (int i = tid; i < kTile * KC; i += kThreads) reinterpret_cast<u32x4*>(tile)[i] = u32x4{0, 0, 0, 0};
+    for (int i = tid; i < 2 * D::kStage / 8; i += kThreads) reinterpret_cast<u32x4*>(stage[0])[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
-  const int rblock = NB == 2 ? (wave & 1) : 0;          // query rows this wave scores
-  const int tok0 = NB == 2 ? 32 * (wave >> 1) : 16 * wave;  // and tokens
+  const bool scoring = wave < D::kScoring;
+  const int rblock = wave % NB;                  // query rows this wave scores
+  const int tg = (wave / NB) % TG;               // and tokens
+  const int tok0 = tg * (kTile / TG);
+  const int qrow = rb * MB + rblock * 16 + ln;
+  const int sees_less = p.Q - 1 - (qrow < p.rows ? qrow / p.H : 0);  // this lane's row sees so many tokens less
 
-  while (t0 < t1) {
-    // ---- one piece: tiles [a, b) of sequence n
-    int tiles = seq_tiles(p, n);
-    while (first + tiles <= t0) {  // (empty sequences have no tiles)
-      first += tiles;
-      ++n;
-      tiles = seq_tiles(p, n);
+  // page of token 64 t + lane of sequence s, which has len tokens (the last
+  // one's page for lanes behind it), and that row's place; -1: no such row
+  auto page_of = [&](int pos) { return (unsigned)(((uint64_t)(unsigned)pos * p.page_mul) >> p.page_shift); };
+  auto lookup = [&](int s, int t, int len) {
+    const int pos = t * kTile + lane;
+    return (p.table + s * p.table_stride)[page_of(pos < len ? pos : len - 1)];
+  };
+  auto place = [&](int page, int t, int len) {
+    const int pos = t * kTile + lane;
+    const bool there = pos < len && page >= 0 && page < p.num_pages;
+    return there ? page * p.page_stride + (int64_t)(pos - (int)page_of(pos) * p.page_size) * (p.L + p.R) : (int64_t)-1;
+  };
+  // Rows that are not there are fetched from the first one that is (their
+  // weights are 0); a tile without any is not fetched and not computed.
+  auto start = [&](int64_t at, unsigned long long live, __bf16* buf) {
+    if (live == 0) return;
+    if (live != ~0ull) {
+      const int64_t some = lane64(at, __ffsll(live) - 1);
+      at = at < 0 ? some : at;
     }
-    const int a = (int)(t0 - first);
-    const int b = (int)((t1 - first) < tiles ? (t1 - first) : tiles);
-    const int len = seq_tokens(p, n);
-    const int32_t* table = p.table + n * p.table_stride;
-
-    // query operand: row ln of the wave's row block, 8 values a step
-    bf16x8 qf[KS];
-    const int qrow = rb * MB + rblock * 16 + ln;
-    {
-      const bool have = qrow < p.rows;
-      const int qi = have ? qrow / p.H : 0, qh = have ? qrow % p.H : 0;
-      const __bf16* qp = p.q + n * p.qs[0] + qi * p.qs[1] + qh * p.qs[2];
-      const __bf16* qrp = p.qr + n * p.qrs[0] + qi * p.qrs[1] + qh * p.qrs[2];
+    D::fetch(p, at, wave, lane, buf);
+  };
+  bf16x8 qf[KS];
+  auto load_q = [&](int s) {
+    const int row = keep_here(qrow), qi = row < p.rows ? row / p.H : 0, qh = row < p.rows ? row % p.H : 0;
+    const int lg = keep_here(lane >> 4);
+    const __bf16* qp = p.q + s * p.qs[0] + qi * p.qs[1] + qh * p.qs[2];
+    const __bf16* qrp = p.qr + s * p.qrs[0] + qi * p.qrs[1] + qh * p.qrs[2];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int c = 32 * s + 8 * lg;
-        bf16x8 x = {};
-        if (c < LP) {
-          if (have && c < p.L) x = *reinterpret_cast<const bf16x8*>(qp + c);
-        } else {
-          if (have && c - LP < p.R) x = *reinterpret_cast<const bf16x8*>(qrp + (c - LP));
-        }
-        qf[s] = x;
+    for (int k = 0; k < KS; ++k) {
+      const int c = 32 * k + 8 * lg;
+      bf16x8 x = {};
+      if (k < LP / 32) {
+        if (row < p.rows && c < p.L) x = *reinterpret_cast<const bf16x8*>(qp + c);
+      } else {
+        if (row < p.rows && c - LP < p.R) x = *reinterpret_cast<const bf16x8*>(qrp + (c - LP));
       }
+      qf[k] = x;
     }
-    const int sees = len - (p.Q - 1 - (qrow < p.rows ? qrow / p.H : 0));  // tokens this lane's row sees
-    const int all_see = len - (p.Q - 1);
+  };
 
-    float m[NB], l = 0.f;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) m[i] = -INFINITY;
-    f32x4 acc[MT][NB];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  // the tile being computed: t of sequence n; the one fetched next: ft of sequence fn
+  int t = uniform((int)(t0 - first)), len = uniform(seq_tokens(p, n)), tiles = tiles_of(len), begin = t;
+  int64_t at = place(lookup(n, t, len), t, len);
+  unsigned long long live = __ballot(at >= 0);
+  start(at, live, stage[0]);
+  if (scoring) load_q(n);
+  --left;
+  int fn = n, ft = t, flen = len, ftiles = tiles;
+  auto advance = [&]() {
+    if (++ft < ftiles) return;
+    ft = 0;
+    do flen = uniform(seq_tokens(p, ++fn));
+    while ((ftiles = tiles_of(flen)) == 0);
+  };
+  int page = 0;
+  if (left > 0) {
+    advance();
+    page = lookup(fn, ft, flen);
+  }
 
-    for (int t = a; t < b; ++t) {
-      // rows of this tile: lane i looks up token 64 t + i
-      const int pos = t * kTile + lane;
-      int64_t at = -1;
-      if (pos < len) {
-        const int pg = pos / p.page_size;
-        const int page = table[pg];
-        if (page >= 0 && page < p.num_pages)
-          at = page * p.page_stride + (int64_t)(pos - pg * p.page_size) * (p.L + p.R);
+  float m = -INFINITY, l = 0.f;  // of row ln of the wave's block, over its tokens; units of scale2 s
+  f32x4 acc[MT][NB];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  for (int cur = 0;; cur ^= 1) {
+    wait_loads();
+    lds_barrier();  // this tile has landed, and the other buffer's readers are done
+    const bool more = left > 0;
+    const int nn = fn, nt = ft, nlen = flen, ntiles = ftiles;
+    unsigned long long nlive = 0;
+    if (more) {
+      at = place(page, ft, flen);
+      nlive = __ballot(at >= 0);
+      if (--left > 0) {
+        // (before the tile's loads are issued: waiting for a length does not
+        // wait for them)
+        advance();
+        page = lookup(fn, ft, flen);
       }
-      const unsigned long long live = __ballot(at >= 0);
-      __syncthreads();  // the last tile's readers are done
-      if (wave == 0) row_at[lane] = at;
-      __syncthreads();
-#pragma unroll 6
-      for (int i = 0; i < kTile * KC / kThreads; ++i) {
-        const int c0 = (wave * (kTile * KC / kThreads) + i) * 64;
-        const int c = c0 + lane;
-        const int r = c / KC, src = (c - r * KC) ^ (r & 7);
-        const int64_t ro = row_at[r];
-        const int e = src < LP / 8 ? src * 8 : (src - LP / 8) * 8 + p.L;
-        const bool have = src < LP / 8 ? src * 8 < p.L : (src - LP / 8) * 8 < p.R;
-        if (have && ro >= 0) load_lds16(p.cache + ro + e, tile + c0 * 8);
-        if (have && ro < 0) reinterpret_cast<u32x4*>(tile)[c] = u32x4{0, 0, 0, 0};
-      }
-      wait_loads();
-      __syncthreads();
-
-      // ---- scores, transposed: S^T[token][row]; lane holds tokens 4 lg + i
+      start(at, nlive, stage[cur ^ 1]);
+    }
+    if (live) {
+      const __bf16* tile = stage[cur];
       f32x4 s[TB];
+      if (scoring) {
+        D::scores(tile, qf, tok0, ln, lg, s);
+        if (t * kTile + kTile > len - (p.Q - 1) || live != ~0ull) {
+          const int sees = len - sees_less;
 #pragma unroll
-      for (int j = 0; j < TB; ++j) s[j] = f32x4{0, 0, 0, 0};
+          for (int j = 0; j < TB; ++j)
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-          const int r = tok0 + 16 * j + ln;
-          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(tile + (r * KC + ((4 * k + lg) ^ (r & 7))) * 8);
-          s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[k], s[j], 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+              const int tk = tok0 + 16 * j + 4 * lg + i;
+              if (t * kTile + tk >= sees || !((live >> tk) & 1)) s[j][i] = -INFINITY;
+            }
         }
-      }
-      if (t * kTile + kTile > all_see || live != ~0ull) {
+        float mx = s[0][0];
 #pragma unroll
         for (int j = 0; j < TB; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tk = tok0 + 16 * j + 4 * lg + i;
-            if (t * kTile + tk >= sees || !((live >> tk) & 1)) s[j][i] = -INFINITY;
-          }
+          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
+        mx = max_halves(max_quarters(mx));
+        if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
       }
-      float mx = s[0][0];
+      lds_barrier();
+      if (scoring) {
+        float mx = smax[0][rblock * 16 + ln];
 #pragma unroll
-      for (int j = 0; j < TB; ++j)
+        for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
+        mx *= p.scale2;
+        // The maximum in use follows the true one only when that has grown by
+        // more than 8 (a factor of 256): the weights stay far inside the
+        // range, and the output is seldom rescaled.
+        const float mn = mx > m + 8.f || m == -INFINITY ? fmaxf(mx, m) : m;
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float fac = exp2_hw(m - base);
+        m = mn;
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
-      mx = max_halves(max_quarters(mx));
-      if (lg == 0) smax[wave][ln] = mx;
-      __syncthreads();
-      float alpha[NB], mb[NB];
+        for (int j = 0; j < TB; ++j) {
+          bf16x4 pb;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
+            sum += e;
+            // the weights go to the matrix unit in bf16, the values' own
+            // type; their sum stays in fp32 (and alone carries a NaN)
+            pb[i] = (__bf16)fmaxf(e, 0.f);
+          }
+          const int tk = tok0 + 16 * j + 4 * lg;
+          *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+        }
+        l = l * fac + sum;
+        if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
+      }
+      lds_barrier();
+      float fac[NB];
+      bool same = true;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        float x;
-        if (NB == 2) {
-          x = fmaxf(smax[j][ln], smax[j + 2][ln]);
-        } else {
-          x = fmaxf(fmaxf(smax[0][ln], smax[1][ln]), fmaxf(smax[2][ln], smax[3][ln]));
-        }
-        const float mn = fmaxf(m[j], x * p.scale2);
-        mb[j] = mn == -INFINITY ? 0.f : mn;
-        alpha[j] = exp2_hw(m[j] - mb[j]);
-        m[j] = mn;
+        fac[j] = sfac[j * 16 + ln];
+        same &= fac[j] == 1.f;
       }
-      const float base = NB == 2 && rblock ? mb[NB - 1] : mb[0];
-      const float al = NB == 2 && rblock ? alpha[NB - 1] : alpha[0];
-      float sum = 0.f;
+      if (!__all(same)) {
 #pragma unroll
-      for (int j = 0; j < TB; ++j) {
-        bf16x4 pb;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
-          sum += e;
-          // the weights go to the matrix unit in bf16, the values' own type;
-          // their sum stays in fp32
-          pb[i] = (__bf16)e;
-        }
-        const int r = rblock * 16 + ln, tk = tok0 + 16 * j + 4 * lg;
-        *reinterpret_cast<bf16x4*>(prob + r * kTile + (((tk >> 3) ^ (r & 7)) << 3) + (tk & 7)) = pb;
+          for (int j = 0; j < NB; ++j) acc[i][j] *= fac[j];
       }
-      l = l * al + sum;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] *= alpha[j];
-      __syncthreads();
-
-      // ---- out^T[column][row] += rows^T P^T; the wave's columns
-#pragma unroll
-      for (int k = 0; k < kTile / 32; ++k) {
-        bf16x8 pf[NB];
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int r = j * 16 + ln;
-          pf[j] = *reinterpret_cast<const bf16x8*>(prob + r * kTile + (((4 * k + lg) ^ (r & 7)) << 3));
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int col = wave * (LP / 4) + 16 * i + 4 * (ln & 3);
-          const int r0 = 32 * k + 8 * lg + (ln >> 2), r1 = r0 + 4;
-          const s16x4 lo = read_tr(tile + (r0 * KC + ((col >> 3) ^ (r0 & 7))) * 8 + (col & 7));
-          const s16x4 hi = read_tr(tile + (r1 * KC + ((col >> 3) ^ (r1 & 7))) * 8 + (col & 7));
-          const bf16x8 vf = join(lo, hi);
-#pragma unroll
-          for (int j = 0; j < NB; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[j], acc[i][j], 0, 0, 0);
-        }
-      }
+      D::values(tile, prob, wave, ln, lg, acc);
     }
 
-    // ---- the piece's sums over the lanes and waves that share a row
-    l = sum_halves(sum_quarters(l));
-    __syncthreads();
-    if (lg == 0) ssum[wave][ln] = l;
-    __syncthreads();
-    const bool whole = a == 0 && b == tiles;
-    const int slot = 2 * w + (a > 0 ? 0 : 1);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const float sum = NB == 2 ? ssum[j][ln] + ssum[j + 2][ln]
-                                : (ssum[0][ln] + ssum[1][ln]) + (ssum[2][ln] + ssum[3][ln]);
-      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-      const int row = rb * MB + j * 16 + ln;
-      if (row >= p.rows) continue;
-      const float lse2 = sum == 0.f ? -INFINITY : m[j] + __log2f(sum);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int col = wave * (LP / 4) + 16 * i + 4 * lg;
-        if (col >= p.L) continue;
-        const f32x4 o = acc[i][j] * inv;
-        if (whole) {
-          const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-          *reinterpret_cast<bf16x4*>(p.out + ((int64_t)n * p.rows + row) * p.L + col) = ob;
-        } else {
-          *reinterpret_cast<f32x4*>(p.part + (((int64_t)rb * 2 * p.groups + slot) * MB + j * 16 + ln) * p.L + col) = o;
-        }
+    if (!more || nn != n) {
+      // ---- the end of a piece: tiles [begin, t] of sequence n
+      l = sum_halves(sum_quarters(l));
+      lds_barrier();
+      const int ln = keep_here(lane & 15), lg = keep_here(lane >> 4);
+      if (scoring && lg == 0) {
+        smax[tg][rblock * 16 + ln] = l;
+        if (tg == 0) sfac[rblock * 16 + ln] = m;
       }
-      if (wave == 0 && lg == 0) {
-        if (whole) {
-          if (p.lse) p.lse[(int64_t)n * p.rows + row] = lse2 * kLn2;
-        } else {
-          p.plse[((int64_t)rb * 2 * p.groups + slot) * MB + j * 16 + ln] = lse2;
-        }
+      lds_barrier();
+      const bool whole = begin == 0 && t == tiles - 1;
+      const int slot = 2 * w + (begin > 0 ? 0 : 1);
+      if (tid == 0 && rb == 0) {
+        if (begin == 0) p.shared[2 * n] = w;
+        if (t == tiles - 1) p.shared[2 * n + 1] = w;
       }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int row = rb * MB + j * 16 + ln;
+        if (row < p.rows) {
+          float sum = smax[0][j * 16 + ln];
+#pragma unroll
+          for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
+          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+          const float lse2 = sum == 0.f ? -INFINITY : sfac[j * 16 + ln] + __log2f(sum);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const int col = wave * (MT * 16) + 16 * i + 4 * lg;
+            if (col < p.L) {
+              const f32x4 o = acc[i][j] * inv;
+              if (whole) {
+                const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+                *reinterpret_cast<bf16x4*>(p.out + ((int64_t)n * p.rows + row) * p.L + col) = ob;
+              } else {
+                *reinterpret_cast<f32x4*>(p.part + (((int64_t)rb * 2 * p.groups + slot) * MB + j * 16 + ln) * p.L +
+                                          col) = o;
+              }
+            }
+          }
+          if (wave == 0 && lg == 0) {
+            if (whole) {
+              if (p.lse) p.lse[(int64_t)n * p.rows + row] = lse2 * kLn2;
+            } else {
+              p.plse[((int64_t)rb * 2 * p.groups + slot) * MB + j * 16 + ln] = lse2;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][j] = f32x4{0, 0, 0, 0};
+      }
+      if (!more) return;
+      m = -INFINITY;
+      l = 0.f;
+      begin = nt;
+      if (scoring) load_q(nn);
     }
-    t0 = first + b;
+    n = nn;
+    t = nt;
+    len = nlen;
+    tiles = ntiles;
+    live = nlive;
   }
 }
 
-// Joins the pieces of sequences that several workgroups share, and writes the
-// outputs of empty sequences.  Grid: (query row pairs, sequences); 128
-// threads a row.
+// Joins the pieces of a sequence that several workgroups share, and writes
+// the outputs of empty sequences.  Grid: (query rows, sequences); 128 threads
+// take a quarter of the pieces each, 4 columns a thread.
 __global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, int MB) {
-  __shared__ int64_t red[4];
-  const int n = blockIdx.y, lane = threadIdx.x & 63;
-  const int tiles = seq_tiles(p, n);
-  const int row = blockIdx.x * 2 + (threadIdx.x >> 7), c = (threadIdx.x & 127) * 4;
-  if (tiles == 0) {
-    if (row < p.rows) {
-      for (int k = c; k < p.L; k += 512)
-        *reinterpret_cast<bf16x4*>(p.out + ((int64_t)n * p.rows + row) * p.L + k) = bf16x4{};
-      if (p.lse && c == 0) p.lse[(int64_t)n * p.rows + row] = -INFINITY;
-    }
+  __shared__ f32x4 osum[3][128];
+  const int n = blockIdx.y, row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int c = (tid & 127) * 4, part = tid >> 7;
+  const int64_t at_out = ((int64_t)n * p.rows + row) * p.L + c;
+  if (seq_tokens(p, n) == 0) {
+    if (c < p.L && part == 0) *reinterpret_cast<bf16x4*>(p.out + at_out) = bf16x4{};
+    if (p.lse && tid == 0) p.lse[(int64_t)n * p.rows + row] = -INFINITY;
     return;
   }
-  const int64_t total = total_tiles(p, red);
-  int64_t first = 0;  // line position of the sequence's first tile
-  for (int n0 = 0; n0 < n; n0 += 64) {
-    int x = n0 + lane < n ? seq_tiles(p, n0 + lane) : 0;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
-    first += x;
-  }
-  // the shares that hold its first and its last tile
-  const int64_t shares = total < p.groups ? total : p.groups;
-  const int w0 = (int)(((first + 1) * shares - 1) / total), w1 = (int)(((first + tiles) * shares - 1) / total);
-  if (w0 == w1 || row >= p.rows) return;
-  const int rb = row / MB, rr = row % MB;
+  const int w0 = p.shared[2 * n], w1 = p.shared[2 * n + 1];
+  if (w0 == w1) return;
+  const int64_t at = ((int64_t)(row / MB) * 2 * p.groups) * MB + row % MB;
   // share w0 holds the sequence's beginning (slot 2 w0 + 1), the later ones
   // begin in mid-sequence (slot 2 w)
-  const int64_t at = ((int64_t)rb * 2 * p.groups) * MB + rr;
+  auto slot = [&](int w) { return at + (int64_t)(2 * w + (w == w0 ? 1 : 0)) * MB; };
   float top = -INFINITY;
-  for (int w = w0; w <= w1; ++w) top = fmaxf(top, p.plse[at + (int64_t)(2 * w + (w == w0 ? 1 : 0)) * MB]);
+  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.plse[slot(w)]);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
   const float base = top == -INFINITY ? 0.f : top;
-  f32x4 o = {0, 0, 0, 0};
   float sum = 0.f;
-  for (int w = w0; w <= w1; ++w) {
-    const int64_t s = at + (int64_t)(2 * w + (w == w0 ? 1 : 0)) * MB;
-    const float f = exp2_hw(p.plse[s] - base);
-    sum += f;
-    if (c < p.L) o += f * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
+  for (int w = w0 + lane; w <= w1; w += 64) sum += exp2_hw(p.plse[slot(w)] - base);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+  f32x4 o = {0, 0, 0, 0};
+  if (c < p.L) {
+#pragma unroll 4
+    for (int w = w0 + part; w <= w1; w += 4) {
+      const int64_t s = slot(w);
+      o += exp2_hw(p.plse[s] - base) * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
+    }
   }
+  if (part > 0) osum[part - 1][tid & 127] = o;
+  __syncthreads();
+  if (part > 0) return;
+  o += osum[0][tid] + osum[1][tid] + osum[2][tid];
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
   if (c < p.L) {
     const bf16x4 ob = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
-    *reinterpret_cast<bf16x4*>(p.out + ((int64_t)n * p.rows + row) * p.L + c) = ob;
+    *reinterpret_cast<bf16x4*>(p.out + at_out) = ob;
   }
-  if (p.lse && c == 0)
+  if (p.lse && tid == 0)
     p.lse[(int64_t)n * p.rows + row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
@@ -392,26 +522,34 @@ struct Shape {
   int nb, row_blocks, groups;
 };
 
-// Query rows a workgroup and shares of the line.  Two workgroups fit a CU
-// (LDS), so 512 in all; the shares are a multiple of 8, one set an XCD.
+// Query rows a workgroup (16, 32 or 64) and shares of the line: one
+// workgroup fits a CU (LDS), 256 in all; the shares are a multiple of 8, one
+// set an XCD.
 Shape decode_shape(int64_t Q, int64_t H) {
   Shape s;
   const int64_t rows = Q * H;
-  s.nb = rows <= 16 ? 1 : 2;
+  s.nb = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   s.row_blocks = (int)((rows + 16 * s.nb - 1) / (16 * s.nb));
-  int g = 512 / s.row_blocks;
-  g = g / 8 * 8;
+  const int g = 256 / s.row_blocks / 8 * 8;
   s.groups = g < 8 ? 8 : g;
   return s;
 }
 
+int64_t part_rows(const Shape& s) { return (int64_t)s.row_blocks * 2 * s.groups * 16 * s.nb; }
+
 template <int LP, int RP>
 hipError_t launch_nb(const DecodeParams& p, int nb, hipStream_t stream) {
   const dim3 grid((unsigned)(p.groups * p.row_blocks));
-  if (nb == 1)
-    hipLaunchKernelGGL((latent_decode_kernel<LP, RP, 1>), grid, dim3(kThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL((latent_decode_kernel<LP, RP, 2>), grid, dim3(kThreads), 0, stream, p);
+  switch (nb) {
+    case 1:
+      hipLaunchKernelGGL((latent_decode_kernel<LP, RP, 1>), grid, dim3(kThreads), 0, stream, p);
+      break;
+    case 2:
+      hipLaunchKernelGGL((latent_decode_kernel<LP, RP, 2>), grid, dim3(kThreads), 0, stream, p);
+      break;
+    default:
+      hipLaunchKernelGGL((latent_decode_kernel<LP, RP, 4>), grid, dim3(kThreads), 0, stream, p);
+  }
   return hipGetLastError();
 }
 
@@ -423,10 +561,7 @@ hipError_t launch_r(const DecodeParams& p, int nb, hipStream_t stream) {
 }  // namespace
 
 size_t latent_decode_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L) {
-  (void)N;
-  const Shape s = decode_shape(Q, H);
-  const int64_t slots = (int64_t)s.row_blocks * 2 * s.groups * 16 * s.nb;
-  return (size_t)slots * (size_t)(L + 1) * 4;
+  return (size_t)(part_rows(decode_shape(Q, H)) * (L + 1) + 2 * N) * 4;
 }
 
 hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t stream) {
@@ -438,6 +573,12 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   p.page_size = (int)a.page_size;
   p.L = (int)a.L;
   p.R = (int)a.R;
+  // j / d = j m >> (31 + s) with 2^s >= d and m = floor(2^(31+s) / d) + 1: m d
+  // passes 2^(31+s) by at most d <= 2^s, too little to matter for j < 2^31
+  int sh = 0;
+  while ((1 << sh) < p.page_size) ++sh;
+  p.page_shift = 31 + sh;
+  p.page_mul = (uint32_t)(((uint64_t)1 << (31 + sh)) / (uint32_t)p.page_size + 1);
   p.table = a.page_table;
   p.table_stride = a.table_stride;
   p.max_pages = (int)a.max_pages;
@@ -457,14 +598,14 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   p.row_blocks = s.row_blocks;
   p.groups = s.groups;
   p.scale2 = a.scale * kLog2e;
-  const int64_t slots = (int64_t)s.row_blocks * 2 * s.groups * 16 * s.nb;
   p.part = static_cast<float*>(a.workspace);
-  p.plse = p.part + slots * a.L;
+  p.plse = p.part + part_rows(s) * a.L;
+  p.shared = reinterpret_cast<int32_t*>(p.plse + part_rows(s));
   hipError_t e = a.L <= 128 ? launch_r<128>(p, s.nb, stream)
                             : (a.L <= 256 ? launch_r<256>(p, s.nb, stream) : launch_r<512>(p, s.nb, stream));
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)((p.rows + 1) / 2), (unsigned)p.N), dim3(kThreads), 0, stream,
-                     p, 16 * s.nb);
+  hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)p.rows, (unsigned)p.N), dim3(kThreads), 0, stream, p,
+                     16 * s.nb);
   return hipGetLastError();
 }
 
