@@ -119,21 +119,21 @@ struct Decode {
   // then fall on distinct banks.  Rotary rows (128 B) follow the latent rows;
   // their chunk c is at c ^ ((r >> 1) & 7).
 
-  // Fetches the tile whose rows lie at ``at`` (lane i: token i).
-  static __device__ __forceinline__ void fetch(const DecodeParams& p, int64_t at, int wave, int lane,
+  // Load i of the wave's kLoads for the tile whose rows lie at ``at`` (lane i:
+  // token i).
+  static constexpr int RI = 64 / LC;  // latent rows a load covers
+  static constexpr int kLoads = kRows / RI + (RP > 0 ? 1 : 0);
+  static __device__ __forceinline__ void fetch(const DecodeParams& p, int i, int64_t at, int wave, int lane,
                                                __bf16* __restrict__ buf) {
-    constexpr int RI = 64 / LC;  // rows an instruction covers
     lane = keep_here(lane);
-#pragma unroll
-    for (int i = 0; i < kRows / RI; ++i) {
+    if (i < kRows / RI) {
       const int r = i * RI + lane / LC;  // of the wave's rows
       const int src = (lane & (LC - 1)) ^ ((r & 7) << 1);
       const int64_t ro = RI == 1 ? lane64(at, wave * kRows + i) : __shfl(at, wave * kRows + r, 64);
       if (src * 8 < p.L)
         load_lds16(reinterpret_cast<const char*>(p.cache + ro) + (unsigned)(src * 16),
                    buf + (wave * kRows + i * RI) * LP);
-    }
-    if (RP > 0) {
+    } else {
       const int r = lane >> 3, src = (lane & 7) ^ (((wave * kRows + r) >> 1) & 7);
       const int64_t ro = __shfl(at, wave * kRows + r, 64);
       if (src * 8 < p.R) load_lds16(p.cache + ro + p.L + src * 8, buf + kTile * LP + wave * kRows * RP);
@@ -141,9 +141,11 @@ struct Decode {
   }
 
   // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i
-  // of each block.  Operands are read a group ahead of their products.
+  // of each block.  Operands are read a group ahead of their products, and
+  // load(i), 0 <= i < kLoads, is called along the way.
+  template <typename Load>
   static __device__ __forceinline__ void scores(const __bf16* __restrict__ tile, const bf16x8 (&qf)[KS], int tok0,
-                                                int ln, int lg, f32x4 (&s)[TB]) {
+                                                int ln, int lg, f32x4 (&s)[TB], const Load& load) {
 #pragma unroll
     for (int j = 0; j < TB; ++j) s[j] = f32x4{0, 0, 0, 0};
     const int r0 = tok0 + ln;  // block j adds 16: the same position in its row
@@ -162,11 +164,14 @@ struct Decode {
         kf[g & 1][i] = *reinterpret_cast<const bf16x8*>(at);
       }
     };
+    constexpr int NG = (F + G - 1) / G, LG = (kLoads + NG - 1) / NG;
     read(0);
 #pragma unroll
-    for (int g = 0; g < (F + G - 1) / G; ++g) {
-      if ((g + 1) * G < F) read(g + 1);
+    for (int g = 0; g < NG; ++g) {
+      if (g + 1 < NG) read(g + 1);
       hold_order();
+#pragma unroll
+      for (int i = g * LG; i < kLoads && i < (g + 1) * LG; ++i) load(i);
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         const int f = g * G + i;
@@ -219,6 +224,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kTile];
   __shared__ float smax[TG][MB];  // of a tile; at a piece's end the sums
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
+  __shared__ int grown[2];        // whether a row's maximum has grown much in this tile
   __shared__ int64_t red[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -242,6 +248,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     for (int i = tid; i < 2 * D::kStage / 8; i += kThreads) reinterpret_cast<u32x4*>(stage[0])[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
+  if (tid < 2) grown[tid] = 0;
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;                  // query rows this wave scores
   const int tg = (wave / NB) % TG;               // and tokens
@@ -260,16 +267,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const int pos = t * kTile + lane;
     const bool there = pos < len && page >= 0 && page < p.num_pages;
     return there ? page * p.page_stride + (int64_t)(pos - (int)page_of(pos) * p.page_size) * (p.L + p.R) : (int64_t)-1;
-  };
-  // Rows that are not there are fetched from the first one that is (their
-  // weights are 0); a tile without any is not fetched and not computed.
-  auto start = [&](int64_t at, unsigned long long live, __bf16* buf) {
-    if (live == 0) return;
-    if (live != ~0ull) {
-      const int64_t some = lane64(at, __ffsll(live) - 1);
-      at = at < 0 ? some : at;
-    }
-    D::fetch(p, at, wave, lane, buf);
   };
   bf16x8 qf[KS];
   auto load_q = [&](int s) {
@@ -292,9 +289,24 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
   // the tile being computed: t of sequence n; the one fetched next: ft of sequence fn
   int t = uniform((int)(t0 - first)), len = uniform(seq_tokens(p, n)), tiles = tiles_of(len), begin = t;
-  int64_t at = place(lookup(n, t, len), t, len);
-  unsigned long long live = __ballot(at >= 0);
-  start(at, live, stage[0]);
+  int64_t at;                  // the rows of the tile fetched next
+  unsigned long long live, nlive;  // which rows of the tile computed, and of that one, are there
+  // Rows that are not there are fetched from the first one that is (their
+  // weights are 0); a tile without any is not fetched and not computed.
+  auto locate = [&](int page, int t, int len) {
+    at = place(page, t, len);
+    nlive = __ballot(at >= 0);
+    if (nlive != 0 && nlive != ~0ull) {
+      const int64_t some = lane64(at, __ffsll(nlive) - 1);
+      at = at < 0 ? some : at;
+    }
+  };
+  locate(lookup(n, t, len), t, len);
+  live = nlive;
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < D::kLoads; ++i) D::fetch(p, i, at, wave, lane, stage[0]);
+  }
   if (scoring) load_q(n);
   --left;
   int fn = n, ft = t, flen = len, ftiles = tiles;
@@ -322,23 +334,50 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     lds_barrier();  // this tile has landed, and the other buffer's readers are done
     const bool more = left > 0;
     const int nn = fn, nt = ft, nlen = flen, ntiles = ftiles;
-    unsigned long long nlive = 0;
+    nlive = 0;
     if (more) {
-      at = place(page, ft, flen);
-      nlive = __ballot(at >= 0);
+      locate(page, ft, flen);
       if (--left > 0) {
         // (before the tile's loads are issued: waiting for a length does not
         // wait for them)
         advance();
         page = lookup(fn, ft, flen);
       }
-      start(at, nlive, stage[cur ^ 1]);
     }
+    auto load = [&](int i) {
+      if (nlive) D::fetch(p, i, at, wave, lane, stage[cur ^ 1]);
+    };
+    const bool scores_here = scoring && live != 0;
+    if (!scores_here) {
+#pragma unroll
+      for (int i = 0; i < D::kLoads; ++i) load(i);
+    }
+    if (tid == 0) grown[cur ^ 1] = 0;
     if (live) {
       const __bf16* tile = stage[cur];
       f32x4 s[TB];
+      float sum = 0.f, fac = 1.f;
+      // weights of the scores against the maximum in use, for the matrix unit
+      // in bf16, the values' own type; their sum stays in fp32 (and alone
+      // carries a NaN)
+      auto weigh = [&]() {
+        const float base = m == -INFINITY ? 0.f : m;
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+          bf16x4 pb;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
+            sum += e;
+            pb[i] = (__bf16)fmaxf(e, 0.f);
+          }
+          const int tk = tok0 + 16 * j + 4 * lg;
+          *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+        }
+      };
       if (scoring) {
-        D::scores(tile, qf, tok0, ln, lg, s);
+        D::scores(tile, qf, tok0, ln, lg, s, load);
         if (t * kTile + kTile > len - (p.Q - 1) || live != ~0ull) {
           const int sees = len - sees_less;
 #pragma unroll
@@ -354,54 +393,39 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         for (int j = 0; j < TB; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
-        mx = max_halves(max_quarters(mx));
+        mx = max_halves(max_quarters(mx)) * p.scale2;
         if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
-      }
-      lds_barrier();
-      if (scoring) {
-        float mx = smax[0][rblock * 16 + ln];
-#pragma unroll
-        for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
-        mx *= p.scale2;
         // The maximum in use follows the true one only when that has grown by
         // more than 8 (a factor of 256): the weights stay far inside the
-        // range, and the output is seldom rescaled.
-        const float mn = mx > m + 8.f || m == -INFINITY ? fmaxf(mx, m) : m;
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float fac = exp2_hw(m - base);
-        m = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-          bf16x4 pb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
-            sum += e;
-            // the weights go to the matrix unit in bf16, the values' own
-            // type; their sum stays in fp32 (and alone carries a NaN)
-            pb[i] = (__bf16)fmaxf(e, 0.f);
-          }
-          const int tk = tok0 + 16 * j + 4 * lg;
-          *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+        // range, and most tiles need no exchange of maxima between the waves
+        // and no rescaling of the output.
+        if (__any(mx > m + 8.f)) {
+          if (lane == 0) grown[cur] = 1;
         }
-        l = l * fac + sum;
-        if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
+        weigh();
       }
       lds_barrier();
-      float fac[NB];
-      bool same = true;
+      if (grown[cur]) {
+        if (scoring) {
+          float mx = smax[0][rblock * 16 + ln];
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        fac[j] = sfac[j * 16 + ln];
-        same &= fac[j] == 1.f;
+          for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
+          const float mn = mx > m + 8.f ? mx : m;
+          fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
+          m = mn;
+          if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
+        }
+        lds_barrier();  // (all have read the maxima; the weights are written again)
+        if (scoring) weigh();
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const float f = sfac[j * 16 + ln];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[i][j] *= f;
+        }
+        lds_barrier();
       }
-      if (!__all(same)) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < NB; ++j) acc[i][j] *= fac[j];
-      }
+      l = l * fac + sum;
       D::values(tile, prob, wave, ln, lg, acc);
     }
 
@@ -470,51 +494,66 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 }
 
 // Joins the pieces of a sequence that several workgroups share, and writes
-// the outputs of empty sequences.  Grid: (query rows, sequences); 128 threads
-// take a quarter of the pieces each, 4 columns a thread.
-__global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, int MB) {
-  __shared__ f32x4 osum[3][128];
-  const int n = blockIdx.y, row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  const int c = (tid & 127) * 4, part = tid >> 7;
+// the outputs of empty sequences.  A wave takes one query row (8 columns a
+// lane) and every ``parts``-th piece; grid: (groups of 8 / parts rows,
+// sequences).
+__global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, int MB, int parts) {
+  __shared__ f32x4 osum[kWaves][2][64];
+  const int n = blockIdx.y, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int row = blockIdx.x * (kWaves / parts) + wave / parts, part = wave % parts, c = lane * 8;
+  const bool have = row < p.rows;
   const int64_t at_out = ((int64_t)n * p.rows + row) * p.L + c;
-  if (seq_tokens(p, n) == 0) {
-    if (c < p.L && part == 0) *reinterpret_cast<bf16x4*>(p.out + at_out) = bf16x4{};
-    if (p.lse && tid == 0) p.lse[(int64_t)n * p.rows + row] = -INFINITY;
+  const int tokens = seq_tokens(p, n), w0 = p.shared[2 * n], w1 = p.shared[2 * n + 1];
+  if (tokens == 0) {
+    if (part != 0 || !have) return;
+    if (c < p.L) *reinterpret_cast<u32x4*>(p.out + at_out) = u32x4{0, 0, 0, 0};
+    if (p.lse && lane == 0) p.lse[(int64_t)n * p.rows + row] = -INFINITY;
     return;
   }
-  const int w0 = p.shared[2 * n], w1 = p.shared[2 * n + 1];
   if (w0 == w1) return;
   const int64_t at = ((int64_t)(row / MB) * 2 * p.groups) * MB + row % MB;
   // share w0 holds the sequence's beginning (slot 2 w0 + 1), the later ones
   // begin in mid-sequence (slot 2 w)
   auto slot = [&](int w) { return at + (int64_t)(2 * w + (w == w0 ? 1 : 0)) * MB; };
-  float top = -INFINITY;
-  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.plse[slot(w)]);
+  float top = -INFINITY, sum = 0.f, base = 0.f;
+  f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (have) {
+    for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.plse[slot(w)]);
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  for (int w = w0 + lane; w <= w1; w += 64) sum += exp2_hw(p.plse[slot(w)] - base);
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    base = top == -INFINITY ? 0.f : top;
+    for (int w = w0 + lane; w <= w1; w += 64) sum += exp2_hw(p.plse[slot(w)] - base);
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  f32x4 o = {0, 0, 0, 0};
-  if (c < p.L) {
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    if (c < p.L) {
 #pragma unroll 4
-    for (int w = w0 + part; w <= w1; w += 4) {
-      const int64_t s = slot(w);
-      o += exp2_hw(p.plse[s] - base) * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
+      for (int w = w0 + part; w <= w1; w += parts) {
+        const int64_t s = slot(w);
+        const float f = exp2_hw(p.plse[s] - base);
+        o[0] += f * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
+        o[1] += f * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c + 4);
+      }
     }
   }
-  if (part > 0) osum[part - 1][tid & 127] = o;
-  __syncthreads();
-  if (part > 0) return;
-  o += osum[0][tid] + osum[1][tid] + osum[2][tid];
+  if (parts > 1) {  // (uniform over the workgroup)
+    osum[wave][0][lane] = o[0];
+    osum[wave][1][lane] = o[1];
+    __syncthreads();
+    if (part == 0)
+      for (int i = 1; i < parts; ++i) {
+        o[0] += osum[wave + i][0][lane];
+        o[1] += osum[wave + i][1][lane];
+      }
+  }
+  if (part != 0 || !have) return;
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
   if (c < p.L) {
-    const bf16x4 ob = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
-    *reinterpret_cast<bf16x4*>(p.out + at_out) = ob;
+    bf16x8 ob;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ob[i] = (__bf16)(o[i >> 2][i & 3] * inv);
+    *reinterpret_cast<bf16x8*>(p.out + at_out) = ob;
   }
-  if (p.lse && tid == 0)
+  if (p.lse && lane == 0)
     p.lse[(int64_t)n * p.rows + row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
@@ -604,8 +643,12 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   hipError_t e = a.L <= 128 ? launch_r<128>(p, s.nb, stream)
                             : (a.L <= 256 ? launch_r<256>(p, s.nb, stream) : launch_r<512>(p, s.nb, stream));
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)p.rows, (unsigned)p.N), dim3(kThreads), 0, stream, p,
-                     16 * s.nb);
+  // few rows: more waves share a row's pieces
+  int parts = kWaves;
+  while (parts > 1 && (int64_t)p.rows * p.N * parts > 2048 * kWaves) parts >>= 1;
+  const int per = kWaves / parts;
+  hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)((p.rows + per - 1) / per), (unsigned)p.N), dim3(kThreads), 0,
+                     stream, p, 16 * s.nb, parts);
   return hipGetLastError();
 }
 
