@@ -31,6 +31,14 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+// 8 bytes to LDS.  The compiler would wait for every load to LDS under way
+// before a store that it cannot tell apart from them; lds_barrier() waits for
+// the store itself.
+__device__ __forceinline__ void store_lds8(void* lds, const bf16x4& x) {
+  const unsigned at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(__builtin_bit_cast(uint64_t, x)) : "memory");
+}
+
 // Barrier of the workgroup for LDS: the wave's LDS accesses are done, its
 // loads (to registers or to LDS) may still be under way.  (__syncthreads
 // waits for those too, which would end every prefetch at the next barrier.)

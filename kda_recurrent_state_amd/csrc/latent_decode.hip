@@ -31,8 +31,7 @@ constexpr int kWaves = kThreads / 64;
 struct DecodeParams {
   const __bf16* cache;
   int64_t page_stride;  // elements
-  int64_t num_pages;
-  int page_size, L, R;
+  int num_pages, page_size, L, R;
   uint32_t page_mul;  // j / page_size = j page_mul >> page_shift, 0 <= j < 2^31
   int page_shift;
   const int32_t* table;
@@ -99,6 +98,14 @@ __device__ __forceinline__ int64_t lane64(int64_t x, int src) {  // src is unifo
   return ((int64_t)hi << 32) | (unsigned)lo;
 }
 
+// The kernel's arguments, read again where this is called: what only the ends
+// of pieces need does not occupy scalar registers in the tile loop.
+__device__ __forceinline__ const DecodeParams* cold_params() {
+  auto k = (const __attribute__((address_space(4))) DecodeParams*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(k));
+  return (const DecodeParams*)k;
+}
+
 // LP, RP: L and R rounded up to what the kernel is built for; NB: blocks of 16
 // query rows a workgroup.
 template <int LP, int RP, int NB>
@@ -119,24 +126,39 @@ struct Decode {
   // then fall on distinct banks.  Rotary rows (128 B) follow the latent rows;
   // their chunk c is at c ^ ((r >> 1) & 7).
 
-  // Load i of the wave's kLoads for the tile whose rows lie at ``at`` (lane i:
-  // token i).
+  // Where this lane's loads of a tile start: the rows of each load (uniform
+  // where a load is one row), and of the rotary load.
   static constexpr int RI = 64 / LC;  // latent rows a load covers
-  static constexpr int kLoads = kRows / RI + (RP > 0 ? 1 : 0);
-  static __device__ __forceinline__ void fetch(const DecodeParams& p, int i, int64_t at, int wave, int lane,
-                                               __bf16* __restrict__ buf) {
-    lane = keep_here(lane);
-    if (i < kRows / RI) {
-      const int r = i * RI + lane / LC;  // of the wave's rows
-      const int src = (lane & (LC - 1)) ^ ((r & 7) << 1);
-      const int64_t ro = RI == 1 ? lane64(at, wave * kRows + i) : __shfl(at, wave * kRows + r, 64);
-      if (src * 8 < p.L)
-        load_lds16(reinterpret_cast<const char*>(p.cache + ro) + (unsigned)(src * 16),
-                   buf + (wave * kRows + i * RI) * LP);
+  static constexpr int kLat = kRows / RI;
+  static constexpr int kLoads = kLat + (RP > 0 ? 1 : 0);
+  struct Rows {
+    int64_t at[RI == 1 ? 1 : kLat], rot;
+  };
+  // ``at``: row of token ``lane``
+  static __device__ __forceinline__ void rows_of(int64_t at, int wave, int lane, Rows& r) {
+    if (RI == 1) {
+      r.at[0] = at;
     } else {
-      const int r = lane >> 3, src = (lane & 7) ^ (((wave * kRows + r) >> 1) & 7);
-      const int64_t ro = __shfl(at, wave * kRows + r, 64);
-      if (src * 8 < p.R) load_lds16(p.cache + ro + p.L + src * 8, buf + kTile * LP + wave * kRows * RP);
+#pragma unroll
+      for (int i = 0; i < kLat; ++i) r.at[RI == 1 ? 0 : i] = __shfl(at, wave * kRows + i * RI + (lane / LC), 64);
+    }
+    if (RP > 0) r.rot = __shfl(at, wave * kRows + (lane >> 3), 64);
+  }
+  // Load i of the wave's kLoads.  Padding columns (L < LP, R < RP) get copies
+  // of a row's last chunk: the queries are 0 there and the outputs not written.
+  static __device__ __forceinline__ void fetch(const DecodeParams& p, int i, const Rows& rows, int wave, int lane,
+                                               __bf16* __restrict__ buf) {
+    const unsigned ln = (unsigned)keep_here(lane);
+    if (i < kLat) {
+      const int64_t at = RI == 1 ? lane64(rows.at[0], wave * kRows + i) : rows.at[RI == 1 ? 0 : i];
+      const unsigned pos = ln % LC * 16, swz = RI == 1 ? (unsigned)(i & 7) * 32 : (i * RI + ln / LC) % 8 * 32;
+      const unsigned off = pos ^ swz, last = (unsigned)(p.L - 8) * 2;
+      load_lds16(reinterpret_cast<const char*>(p.cache + at) + (off < last ? off : last),
+                 buf + (wave * kRows + i * RI) * LP);
+    } else {
+      const unsigned off = (ln % 8 ^ ((wave * kRows + ln / 8) / 2 % 8)) * 16, last = (unsigned)(p.R - 8) * 2;
+      load_lds16(reinterpret_cast<const char*>(p.cache + rows.rot + p.L) + (off < last ? off : last),
+                 buf + kTile * LP + wave * kRows * RP);
     }
   }
 
@@ -244,10 +266,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   find_tile(p, t0, lane, &n, &first);
   n = uniform(n);
 
-  if (p.L < LP || p.R < RP) {  // padding columns are zero from here on
-    for (int i = tid; i < 2 * D::kStage / 8; i += kThreads) reinterpret_cast<u32x4*>(stage[0])[i] = u32x4{0, 0, 0, 0};
-    __syncthreads();
-  }
   if (tid < 2) grown[tid] = 0;
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;                  // query rows this wave scores
@@ -265,11 +283,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   };
   auto place = [&](int page, int t, int len) {
     const int pos = t * kTile + lane;
-    const bool there = pos < len && page >= 0 && page < p.num_pages;
-    return there ? page * p.page_stride + (int64_t)(pos - (int)page_of(pos) * p.page_size) * (p.L + p.R) : (int64_t)-1;
+    const bool there = pos < len && (unsigned)page < (unsigned)p.num_pages;
+    return there ? (int64_t)page * p.page_stride + (int64_t)(pos - (int)page_of(pos) * p.page_size) * (p.L + p.R) : (int64_t)-1;
   };
   bf16x8 qf[KS];
   auto load_q = [&](int s) {
+    const DecodeParams p = *cold_params();
     const int row = keep_here(qrow), qi = row < p.rows ? row / p.H : 0, qh = row < p.rows ? row % p.H : 0;
     const int lg = keep_here(lane >> 4);
     const __bf16* qp = p.q + s * p.qs[0] + qi * p.qs[1] + qh * p.qs[2];
@@ -289,23 +308,24 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
   // the tile being computed: t of sequence n; the one fetched next: ft of sequence fn
   int t = uniform((int)(t0 - first)), len = uniform(seq_tokens(p, n)), tiles = tiles_of(len), begin = t;
-  int64_t at;                  // the rows of the tile fetched next
+  typename D::Rows rows;           // of the tile fetched next
   unsigned long long live, nlive;  // which rows of the tile computed, and of that one, are there
   // Rows that are not there are fetched from the first one that is (their
   // weights are 0); a tile without any is not fetched and not computed.
   auto locate = [&](int page, int t, int len) {
-    at = place(page, t, len);
+    int64_t at = place(page, t, len);
     nlive = __ballot(at >= 0);
     if (nlive != 0 && nlive != ~0ull) {
       const int64_t some = lane64(at, __ffsll(nlive) - 1);
       at = at < 0 ? some : at;
     }
+    D::rows_of(at, wave, lane, rows);
   };
   locate(lookup(n, t, len), t, len);
   live = nlive;
   if (live) {
 #pragma unroll
-    for (int i = 0; i < D::kLoads; ++i) D::fetch(p, i, at, wave, lane, stage[0]);
+    for (int i = 0; i < D::kLoads; ++i) D::fetch(p, i, rows, wave, lane, stage[0]);
   }
   if (scoring) load_q(n);
   --left;
@@ -345,7 +365,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       }
     }
     auto load = [&](int i) {
-      if (nlive) D::fetch(p, i, at, wave, lane, stage[cur ^ 1]);
+      if (nlive) D::fetch(p, i, rows, wave, lane, stage[cur ^ 1]);
     };
     const bool scores_here = scoring && live != 0;
     if (!scores_here) {
@@ -373,7 +393,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
             pb[i] = (__bf16)fmaxf(e, 0.f);
           }
           const int tk = tok0 + 16 * j + 4 * lg;
-          *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+          store_lds8(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7), pb);
         }
       };
       if (scoring) {
@@ -439,6 +459,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (tg == 0) sfac[rblock * 16 + ln] = m;
       }
       lds_barrier();
+      const DecodeParams p = *cold_params();
       const bool whole = begin == 0 && t == tiles - 1;
       const int slot = 2 * w + (begin > 0 ? 0 : 1);
       if (tid == 0 && rb == 0) {
@@ -608,7 +629,7 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   DecodeParams p;
   p.cache = static_cast<const __bf16*>(a.cache);
   p.page_stride = a.page_stride;
-  p.num_pages = a.num_pages;
+  p.num_pages = (int)a.num_pages;
   p.page_size = (int)a.page_size;
   p.L = (int)a.L;
   p.R = (int)a.R;
