@@ -380,7 +380,8 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  *                     token stride (NULL with R == 0).
  *  v               -- [S, H, E];   v_stride = {token, head}.
  *                     q, k, k_rope and v are 16-byte aligned and their strides
- *                     are multiples of 8 elements, 0 .. 2^40 (0: a broadcast dim).
+ *                     are multiples of 8 elements, not negative (0: a broadcast
+ *                     dim); the token strides of k, k_rope and v are at most 2^24.
  *  cu_seqlens_q    -- [N+1] int32 offsets of the sequences' queries in q.
  *  cu_seqlens_k    -- [N+1] int32 offsets of their keys in k, k_rope and v.
  *                     Both non-decreasing (not checked; the kernel clamps, so

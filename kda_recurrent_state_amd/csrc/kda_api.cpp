@@ -343,6 +343,10 @@ kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
   if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || (a->R > 0 && !aligned(a->k_rope, 16)) ||
       !aligned(a->out, 8))
     return KDA_E_LAYOUT;
+  // (the kernel's offsets within a tile of 64 keys are 32-bit)
+  const int64_t far = (int64_t)1 << 24;
+  if (a->S > 1 && (a->k_stride[0] > far || a->v_stride[0] > far || (a->R > 0 && a->k_rope_stride > far)))
+    return KDA_E_UNSUPPORTED;
   if (a->S == 0) kn = vn = rn = 0;
   const Span ins[6] = {{a->q, qn * 2},
                        {a->k, kn * 2},

@@ -17,26 +17,37 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
-// 16 bytes from global memory straight to LDS.  ``lds`` is the wave's base:
-// lane i's 16 bytes land at lds + 16 i; lanes that are switched off load and
-// write nothing and leave their 16 bytes as they were.
-__device__ __forceinline__ void load_lds16(const void* g, void* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// Loads from global memory straight to LDS: lane i's bytes land at lds + 16 i
+// (4 i); lanes that are switched off load and write nothing.  ``lds`` is
+// a uniform byte offset (lds_offset).  They have no destination register that could be taken for written,
+// so nothing but LDS depends on their end, and that is waited for by hand:
+// wait_loads() and a barrier before the bytes are read, and a barrier between
+// the last read of a place and the next load to it.  (The compiler's own form
+// of these loads makes it wait for all of them before any LDS access that it
+// cannot tell apart, which ends the prefetch.)
+__device__ __forceinline__ unsigned lds_offset(const void* lds) {
+  return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
+}
+__device__ __forceinline__ void load_lds16(const char* base, unsigned offset, unsigned lds) {  // base is uniform
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void load_lds16(const char* lane_address, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(lane_address), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void* lane_address, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(lane_address), "s"(lds)
+               : "memory");
 }
 
-// Waits for the wave's loads to LDS (a barrier then shows them to the others).
+// Waits until at most kLeft of the wave's loads are under way (a barrier then
+// shows what loads to LDS have brought to the other waves).
+template <int kLeft = 0>
 __device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0, the other counters free
+  static_assert(kLeft < 64, "vmcnt has 6 bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4 << 14));  // the other counters free
   asm volatile("" ::: "memory");
-}
-
-// 8 bytes to LDS.  The compiler would wait for every load to LDS under way
-// before a store that it cannot tell apart from them; lds_barrier() waits for
-// the store itself.
-__device__ __forceinline__ void store_lds8(void* lds, const bf16x4& x) {
-  const unsigned at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-  asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(__builtin_bit_cast(uint64_t, x)) : "memory");
 }
 
 // Barrier of the workgroup for LDS: the wave's LDS accesses are done, its

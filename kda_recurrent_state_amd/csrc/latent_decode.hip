@@ -16,6 +16,8 @@
 // outputs with their log-sum, and the join kernel weighs them.  Both kernels
 // derive the shares from the lengths on the device, so a captured call
 // follows its lengths.
+#include <type_traits>
+
 #include "internal.h"
 #include "latent_common.h"
 
@@ -24,7 +26,9 @@ namespace {
 
 using namespace latent;
 
-constexpr int kTile = 64;      // tokens a tile
+constexpr int kTile = 64;      // tokens a tile of the line: two halves
+constexpr int kHalf = 32;      // tokens a stage
+constexpr int kStages = 4;
 constexpr int kThreads = 512;  // 8 waves
 constexpr int kWaves = kThreads / 64;
 
@@ -115,124 +119,113 @@ struct Decode {
   static constexpr int LC = LP / 8;               // 16-byte chunks of a staged latent row
   static constexpr int KS = DP / 32;              // contraction steps of the scores
   static constexpr int MT = LP / (16 * kWaves);   // 16-column blocks of the output a wave
-  static constexpr int TG = NB >= 4 ? kWaves / NB : 4;  // groups of tokens the waves score
-  static constexpr int TB = kTile / 16 / TG;      // 16-token blocks a wave scores
-  static constexpr int kScoring = NB * TG;        // waves that score (4 of 8 with NB == 1)
-  static constexpr int kStage = kTile * DP;       // elements of a staged tile
-  static constexpr int kRows = kTile / kWaves;    // rows a wave fetches
+  static constexpr int TG = 2;                    // groups of 16 tokens of a half
+  static constexpr int kScoring = NB * TG;        // waves that score (a row block and a group each)
+  static constexpr int kStage = kHalf * LP;       // elements of a stage
+  static constexpr int kRows = kHalf / kWaves;    // rows a wave fetches
 
   // Chunk c of latent row r is staged at position c ^ 2 (r & 7): the 8 rows x
   // 16 B of a score operand and the 4 rows x 32 B of a transposed value read
-  // then fall on distinct banks.  Rotary rows (128 B) follow the latent rows;
-  // their chunk c is at c ^ ((r >> 1) & 7).
+  // then fall on distinct banks.  Rotary rows (128 B) lie apart, two tiles of
+  // them; their chunk c is at c ^ ((r >> 1) & 7).
 
-  // Where this lane's loads of a tile start: the rows of each load (uniform
-  // where a load is one row), and of the rotary load.
-  static constexpr int RI = 64 / LC;  // latent rows a load covers
-  static constexpr int kLat = kRows / RI;
-  static constexpr int kLoads = kLat + (RP > 0 ? 1 : 0);
-  struct Rows {
-    int64_t at[RI == 1 ? 1 : kLat], rot;
+  static constexpr int RI = 64 / LC;       // latent rows a load covers
+  static constexpr int kLat = kRows / RI;  // latent loads of a wave for a half
+
+  // What a lane adds to its rows' addresses.  Padding columns (L < LP, R < RP)
+  // get copies of a row's last chunk: the queries are 0 there and the outputs
+  // not written.
+  struct Columns {
+    unsigned lat[kLat], rot;
   };
-  // ``at``: row of token ``lane``
-  static __device__ __forceinline__ void rows_of(int64_t at, int wave, int lane, Rows& r) {
-    if (RI == 1) {
-      r.at[0] = at;
-    } else {
+  static __device__ __forceinline__ Columns columns(const DecodeParams& p, int wave, unsigned lane) {
+    Columns c;
+    const unsigned last = (unsigned)(p.L - 8) * 2;
 #pragma unroll
-      for (int i = 0; i < kLat; ++i) r.at[RI == 1 ? 0 : i] = __shfl(at, wave * kRows + i * RI + (lane / LC), 64);
+    for (int i = 0; i < kLat; ++i) {
+      const unsigned off = (lane % LC * 16) ^ ((wave * kRows + i * RI + lane / LC) % 8 * 32);
+      c.lat[i] = off < last ? off : last;
     }
-    if (RP > 0) r.rot = __shfl(at, wave * kRows + (lane >> 3), 64);
+    const unsigned r = wave * 8 + lane / 8, off = (lane % 8 ^ r / 2 % 8) * 16, end = (unsigned)(p.R - 8) * 2;
+    c.rot = (RP > 0 && off < end ? off : end) + p.L * 2;
+    return c;
   }
-  // Load i of the wave's kLoads.  Padding columns (L < LP, R < RP) get copies
-  // of a row's last chunk: the queries are 0 there and the outputs not written.
-  static __device__ __forceinline__ void fetch(const DecodeParams& p, int i, const Rows& rows, int wave, int lane,
-                                               __bf16* __restrict__ buf) {
-    const unsigned ln = (unsigned)keep_here(lane);
-    if (i < kLat) {
-      const int64_t at = RI == 1 ? lane64(rows.at[0], wave * kRows + i) : rows.at[RI == 1 ? 0 : i];
-      const unsigned pos = ln % LC * 16, swz = RI == 1 ? (unsigned)(i & 7) * 32 : (i * RI + ln / LC) % 8 * 32;
-      const unsigned off = pos ^ swz, last = (unsigned)(p.L - 8) * 2;
-      load_lds16(reinterpret_cast<const char*>(p.cache + at) + (off < last ? off : last),
-                 buf + (wave * kRows + i * RI) * LP);
+  // Latent load i of half h of the tile whose rows lie at ``at`` (lane i:
+  // token i), to the stage at ``lds``.
+  static __device__ __forceinline__ void fetch(int i, int h, const char* at, int wave, int lane, const Columns& c,
+                                               unsigned lds) {
+    const int r = h * kHalf + wave * kRows + i * RI;
+    if (RI == 1) {
+      load_lds16((const char*)lane64((int64_t)at, r), c.lat[i], lds + (wave * kRows + i) * LP * 2);
     } else {
-      const unsigned off = (ln % 8 ^ ((wave * kRows + ln / 8) / 2 % 8)) * 16, last = (unsigned)(p.R - 8) * 2;
-      load_lds16(reinterpret_cast<const char*>(p.cache + rows.rot + p.L) + (off < last ? off : last),
-                 buf + kTile * LP + wave * kRows * RP);
+      load_lds16((const char*)__shfl((int64_t)at, r + lane / LC, 64) + c.lat[i], lds + (wave * kRows + i * RI) * LP * 2);
     }
+  }
+  // The tile's rotary rows, 8 a wave.
+  static __device__ __forceinline__ void fetch_rotary(const char* at, int wave, int lane, const Columns& c,
+                                                      unsigned lds) {
+    if (RP > 0) load_lds16((const char*)__shfl((int64_t)at, wave * 8 + lane / 8, 64) + c.rot, lds + wave * 8 * RP * 2);
   }
 
-  // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i
-  // of each block.  Operands are read a group ahead of their products, and
-  // load(i), 0 <= i < kLoads, is called along the way.
+  // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i.
+  // Operands are read a group ahead of their products, and load(i),
+  // 0 <= i < kLat, is called along the way.
   template <typename Load>
-  static __device__ __forceinline__ void scores(const __bf16* __restrict__ tile, const bf16x8 (&qf)[KS], int tok0,
-                                                int ln, int lg, f32x4 (&s)[TB], const Load& load) {
-#pragma unroll
-    for (int j = 0; j < TB; ++j) s[j] = f32x4{0, 0, 0, 0};
-    const int r0 = tok0 + ln;  // block j adds 16: the same position in its row
-    const char* lat = reinterpret_cast<const char*>(tile + r0 * LP);
-    const char* rot = reinterpret_cast<const char*>(tile + kTile * LP + r0 * RP);
-    const int x = (lg ^ ((r0 & 7) << 1)) * 16, y = (lg ^ ((r0 >> 1) & 7)) * 16;
-    constexpr int F = KS * TB, G = 6;
+  static __device__ __forceinline__ f32x4 scores(const __bf16* lat_row, const __bf16* rot_row, const bf16x8 (&qf)[KS],
+                                                 int ln, int lg, const Load& load) {
+    const char *lat = reinterpret_cast<const char*>(lat_row), *rot = reinterpret_cast<const char*>(rot_row);
+    const int x = (lg ^ ((ln & 7) << 1)) * 16, y = (lg ^ ((ln >> 1) & 7)) * 16;
+    constexpr int G = 6, NG = (KS + G - 1) / G, LG = (kLat + NG - 1) / NG;
     bf16x8 kf[2][G];
     auto read = [&](int g) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const int f = g * G + i, k = f / TB, j = f % TB;
-        if (f >= F) continue;
-        const char* at = k < LP / 32 ? lat + (x ^ ((k & 3) * 64)) + (k >> 2) * 256 + j * 16 * LP * 2
-                                     : rot + (y ^ ((k - LP / 32) * 64)) + j * 16 * RP * 2;
+        const int k = g * G + i;
+        if (k >= KS) continue;
+        const char* at = k < LP / 32 ? lat + (x ^ ((k & 3) * 64)) + (k >> 2) * 256 : rot + (y ^ ((k - LP / 32) * 64));
         kf[g & 1][i] = *reinterpret_cast<const bf16x8*>(at);
       }
     };
-    constexpr int NG = (F + G - 1) / G, LG = (kLoads + NG - 1) / NG;
+    f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains of products
     read(0);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if (g + 1 < NG) read(g + 1);
       hold_order();
 #pragma unroll
-      for (int i = g * LG; i < kLoads && i < (g + 1) * LG; ++i) load(i);
+      for (int i = g * LG; i < kLat && i < (g + 1) * LG; ++i) load(i);
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const int f = g * G + i;
-        if (f < F) s[f % TB] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[g & 1][i], qf[f / TB], s[f % TB], 0, 0, 0);
-      }
+      for (int i = 0; i < G; ++i)
+        if (g * G + i < KS)
+          s[i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[g & 1][i], qf[g * G + i], s[i & 1], 0, 0, 0);
       hold_order();
     }
+    return s[0] + s[1];
   }
 
   // out^T[column][row] += rows^T P^T for the wave's columns, the operands read
   // one block of NB products ahead
-  static __device__ __forceinline__ void values(const __bf16* __restrict__ tile, const __bf16* __restrict__ prob,
+  static __device__ __forceinline__ void values(const __bf16* __restrict__ half, const __bf16* __restrict__ prob,
                                                 int wave, int ln, int lg, f32x4 (&acc)[MT][NB]) {
-    const int r0 = 8 * lg + (ln >> 2);  // rows r0 and r0 + 4 of each 32
+    const int r0 = 8 * lg + (ln >> 2);  // rows r0 and r0 + 4
     const int c0 = wave * (MT * 2) + ((ln & 3) >> 1);
-    const char* rows = reinterpret_cast<const char*>(tile + r0 * LP) + (ln & 1) * 8;
-    constexpr int B = kTile / 32 * MT;
-    bf16x8 pf[2][NB], vf[2];
-    auto weights = [&](int k) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        pf[k & 1][j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kTile + (((4 * k + lg) ^ (ln & 7)) << 3));
-    };
-    auto read = [&](int b) {
-      const int k = b / MT, i = b % MT;
+    const char* rows = reinterpret_cast<const char*>(half + r0 * LP) + (ln & 1) * 8;
+    bf16x8 pf[NB], vf[2];
+    auto read = [&](int i) {
       const int x = ((c0 + 2 * i) ^ ((r0 & 7) << 1)) * 16;
-      vf[b & 1] = join(read_tr(rows + x + k * 32 * LP * 2), read_tr(rows + (x ^ 128) + (k * 32 + 4) * LP * 2));
+      vf[i & 1] = join(read_tr(rows + x), read_tr(rows + (x ^ 128) + 4 * LP * 2));
     };
-    weights(0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      pf[j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kHalf + ((lg ^ ((ln >> 1) & 3)) << 3));
     read(0);
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (b + 1 < B) read(b + 1);
-      if (b == (MT > 1 ? 1 : 0)) weights(1);
+    for (int i = 0; i < MT; ++i) {
+      if (i + 1 < MT) read(i + 1);
       hold_order();
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        acc[b % MT][j] =
-            __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[b & 1], pf[b / MT][j], acc[b % MT][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[i & 1], pf[j], acc[i][j], 0, 0, 0);
       hold_order();
     }
   }
@@ -241,12 +234,14 @@ struct Decode {
 template <int LP, int RP, int NB>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_decode_kernel(DecodeParams p) {
   using D = Decode<LP, RP, NB>;
-  constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG, TB = D::TB;
-  __shared__ __attribute__((aligned(16))) __bf16 stage[2][D::kStage];
-  __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kTile];
-  __shared__ float smax[TG][MB];  // of a tile; at a piece's end the sums
+  constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG;
+  __shared__ __attribute__((aligned(16))) __bf16 stage[kStages][D::kStage];
+  __shared__ __attribute__((aligned(16))) __bf16 rotary[2][RP > 0 ? kTile * RP : 8];
+  __shared__ __attribute__((aligned(16))) __bf16 prob[2][MB * kHalf];
+  __shared__ float smax[TG][MB];  // of a half; at a piece's end the sums
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
-  __shared__ int grown[2];        // whether a row's maximum has grown much in this tile
+  __shared__ int32_t pages[2][kWaves][64];  // page of token 64 t + lane of the tile fetched next
+  __shared__ int grown[4];        // whether a row's maximum has grown much in half u, at u % 4
   __shared__ int64_t red[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -266,20 +261,19 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   find_tile(p, t0, lane, &n, &first);
   n = uniform(n);
 
-  if (tid < 2) grown[tid] = 0;
+  if (tid < 4) grown[tid] = 0;
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;                  // query rows this wave scores
   const int tg = (wave / NB) % TG;               // and tokens
-  const int tok0 = tg * (kTile / TG);
   const int qrow = rb * MB + rblock * 16 + ln;
   const int sees_less = p.Q - 1 - (qrow < p.rows ? qrow / p.H : 0);  // this lane's row sees so many tokens less
 
-  // page of token 64 t + lane of sequence s, which has len tokens (the last
-  // one's page for lanes behind it), and that row's place; -1: no such row
+  // where the page of token 64 t + lane of sequence s is, which has len tokens
+  // (the last one's for lanes behind it), and that row's place; -1: no such row
   auto page_of = [&](int pos) { return (unsigned)(((uint64_t)(unsigned)pos * p.page_mul) >> p.page_shift); };
   auto lookup = [&](int s, int t, int len) {
     const int pos = t * kTile + lane;
-    return (p.table + s * p.table_stride)[page_of(pos < len ? pos : len - 1)];
+    return p.table + s * p.table_stride + page_of(pos < len ? pos : len - 1);
   };
   auto place = [&](int page, int t, int len) {
     const int pos = t * kTile + lane;
@@ -308,25 +302,32 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
   // the tile being computed: t of sequence n; the one fetched next: ft of sequence fn
   int t = uniform((int)(t0 - first)), len = uniform(seq_tokens(p, n)), tiles = tiles_of(len), begin = t;
-  typename D::Rows rows;           // of the tile fetched next
+  const char* at;                  // rows of the tile fetched next
   unsigned long long live, nlive;  // which rows of the tile computed, and of that one, are there
   // Rows that are not there are fetched from the first one that is (their
-  // weights are 0); a tile without any is not fetched and not computed.
+  // weights are 0), or, if there is none, from the cache's first (a half
+  // without rows is not computed): every half has the same number of loads.
   auto locate = [&](int page, int t, int len) {
-    int64_t at = place(page, t, len);
-    nlive = __ballot(at >= 0);
-    if (nlive != 0 && nlive != ~0ull) {
-      const int64_t some = lane64(at, __ffsll(nlive) - 1);
-      at = at < 0 ? some : at;
+    int64_t row = place(page, t, len);
+    nlive = __ballot(row >= 0);
+    if (nlive != ~0ull) {
+      const int64_t some = nlive != 0 ? lane64(row, __ffsll(nlive) - 1) : 0;
+      row = row < 0 ? some : row;
     }
-    D::rows_of(at, wave, lane, rows);
+    at = reinterpret_cast<const char*>(p.cache + row);
   };
-  locate(lookup(n, t, len), t, len);
+  const unsigned stage_at = lds_offset(stage), rotary_at = lds_offset(rotary), pages_at = lds_offset(pages[0][wave]);
+  constexpr unsigned kStageBytes = D::kStage * 2, kRotaryBytes = sizeof(rotary[0]), kPagesBytes = sizeof(pages[0]);
+  const typename D::Columns columns = D::columns(p, wave, lane);
+
+  auto of_half = [](unsigned long long x, int h) { return (unsigned)(x >> (h * 32)); };
+  locate(*lookup(n, t, len), t, len);
   live = nlive;
-  if (live) {
+  D::fetch_rotary(at, wave, lane, columns, rotary_at);
 #pragma unroll
-    for (int i = 0; i < D::kLoads; ++i) D::fetch(p, i, rows, wave, lane, stage[0]);
-  }
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < D::kLat; ++i) D::fetch(i, h, at, wave, lane, columns, stage_at + h * kStageBytes);
   if (scoring) load_q(n);
   --left;
   int fn = n, ft = t, flen = len, ftiles = tiles;
@@ -336,10 +337,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     do flen = uniform(seq_tokens(p, ++fn));
     while ((ftiles = tiles_of(flen)) == 0);
   };
-  int page = 0;
   if (left > 0) {
     advance();
-    page = lookup(fn, ft, flen);
+    load_lds4(lookup(fn, ft, flen), pages_at);
   }
 
   float m = -INFINITY, l = 0.f;  // of row ln of the wave's block, over its tokens; units of scale2 s
@@ -349,108 +349,131 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  for (int cur = 0;; cur ^= 1) {
-    wait_loads();
-    lds_barrier();  // this tile has landed, and the other buffer's readers are done
-    const bool more = left > 0;
-    const int nn = fn, nt = ft, nlen = flen, ntiles = ftiles;
-    nlive = 0;
-    if (more) {
-      locate(page, ft, flen);
-      if (--left > 0) {
-        // (before the tile's loads are issued: waiting for a length does not
-        // wait for them)
-        advance();
-        page = lookup(fn, ft, flen);
-      }
+  // The loop's unit is a half (32 tokens).  While half u is scored, the output
+  // product of half u - 1 follows without a barrier in between, so that one
+  // wave's products overlap the other wave's softmax on the same SIMD, and
+  // halves u + 1 and u + 2 are on their way.
+  f32x4 s = {0, 0, 0, 0};
+  float sum = 0.f;
+  bool pending = false, more = false;
+  int par = 0;  // of the tile: its stages are 2 par, 2 par + 1
+  int nn = n, nt = t, nlen = len, ntiles = tiles;
+
+  // Weights of the scores against the maximum in use, for the matrix unit in
+  // bf16, the values' own type; their sum stays in fp32.
+  auto weigh = [&](int h) {
+    const float base = m == -INFINITY ? 0.f : m;
+    bf16x4 pb;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = exp2_hw(fmaf(s[i], p.scale2, -base));
+      sum += e;
+      pb[i] = (__bf16)e;
     }
-    auto load = [&](int i) {
-      if (nlive) D::fetch(p, i, rows, wave, lane, stage[cur ^ 1]);
-    };
-    const bool scores_here = scoring && live != 0;
-    if (!scores_here) {
-#pragma unroll
-      for (int i = 0; i < D::kLoads; ++i) load(i);
-    }
-    if (tid == 0) grown[cur ^ 1] = 0;
-    if (live) {
-      const __bf16* tile = stage[cur];
-      f32x4 s[TB];
-      float sum = 0.f, fac = 1.f;
-      // weights of the scores against the maximum in use, for the matrix unit
-      // in bf16, the values' own type; their sum stays in fp32 (and alone
-      // carries a NaN)
-      auto weigh = [&]() {
-        const float base = m == -INFINITY ? 0.f : m;
-        sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-          bf16x4 pb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
-            sum += e;
-            pb[i] = (__bf16)fmaxf(e, 0.f);
-          }
-          const int tk = tok0 + 16 * j + 4 * lg;
-          store_lds8(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7), pb);
-        }
-      };
+    const int tk = 16 * tg + 4 * lg;
+    *reinterpret_cast<bf16x4*>(prob[h] + (rblock * 16 + ln) * kHalf + (((tk >> 3) ^ ((ln >> 1) & 3)) << 3) +
+                               (tk & 7)) = pb;
+  };
+  // Half u - 1 (of parity h), whose weights all waves have written: takes its
+  // sums, after a new exchange of maxima if some row's has grown.  The maximum
+  // in use follows the true one only when that is larger by more than 8 (a
+  // factor of 256): the weights stay far inside the range, and most halves
+  // need neither the exchange nor a rescaling of the output.
+  auto settle = [&](int h, int u) {
+    float fac = 1.f;
+    if (grown[u]) {
       if (scoring) {
-        D::scores(tile, qf, tok0, ln, lg, s, load);
-        if (t * kTile + kTile > len - (p.Q - 1) || live != ~0ull) {
-          const int sees = len - sees_less;
+        const float mx = fmaxf(smax[0][rblock * 16 + ln], smax[1][rblock * 16 + ln]);
+        const float mn = mx > m + 8.f ? mx : m;
+        fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
+        m = mn;
+        if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
+      }
+      lds_barrier();  // (all have read the maxima; the weights are written again)
+      if (scoring) weigh(h);
 #pragma unroll
-          for (int j = 0; j < TB; ++j)
+      for (int j = 0; j < NB; ++j) {
+        const float f = sfac[j * 16 + ln];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tk = tok0 + 16 * j + 4 * lg + i;
-              if (t * kTile + tk >= sees || !((live >> tk) & 1)) s[j][i] = -INFINITY;
-            }
-        }
-        float mx = s[0][0];
-#pragma unroll
-        for (int j = 0; j < TB; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
-        mx = max_halves(max_quarters(mx)) * p.scale2;
-        if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
-        // The maximum in use follows the true one only when that has grown by
-        // more than 8 (a factor of 256): the weights stay far inside the
-        // range, and most tiles need no exchange of maxima between the waves
-        // and no rescaling of the output.
-        if (__any(mx > m + 8.f)) {
-          if (lane == 0) grown[cur] = 1;
-        }
-        weigh();
+        for (int i = 0; i < MT; ++i) acc[i][j] *= f;
       }
       lds_barrier();
-      if (grown[cur]) {
-        if (scoring) {
-          float mx = smax[0][rblock * 16 + ln];
-#pragma unroll
-          for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
-          const float mn = mx > m + 8.f ? mx : m;
-          fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
-          m = mn;
-          if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
-        }
-        lds_barrier();  // (all have read the maxima; the weights are written again)
-        if (scoring) weigh();
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const float f = sfac[j * 16 + ln];
-#pragma unroll
-          for (int i = 0; i < MT; ++i) acc[i][j] *= f;
-        }
-        lds_barrier();
-      }
-      l = l * fac + sum;
-      D::values(tile, prob, wave, ln, lg, acc);
     }
+    l = l * fac + sum;
+  };
 
+  auto half = [&](auto hc) {
+    constexpr int h = decltype(hc)::value;
+    const int u = 2 * par + h, before = (u + 3) & 3, after = (u + 2) & 3;  // stages of halves u, u - 1, u + 2
+    // Half u has landed when at most the loads issued after it are under way:
+    // those of half u + 1, after the first half's with the next tile's rotary
+    // rows and pages.
+    wait_loads<D::kLat + (h == 1 && RP > 0 ? 1 : 0)>();
+    lds_barrier();  // and the readers of half u - 2 are done
+    if (pending) settle(h ^ 1, before);
+    if (h == 0) {
+      more = left > 0;
+      nlive = 0;
+      nn = fn;
+      nt = ft;
+      nlen = flen;
+      ntiles = ftiles;
+      if (more) {
+        locate(pages[par][wave][lane], ft, flen);
+        if (--left > 0) {
+          advance();
+          load_lds4(lookup(fn, ft, flen), pages_at + (par ^ 1) * kPagesBytes);
+        }
+      } else {
+        at = reinterpret_cast<const char*>(p.cache);
+      }
+      D::fetch_rotary(at, wave, lane, columns, rotary_at + (par ^ 1) * kRotaryBytes);
+    }
+    const bool here = of_half(live, h) != 0;
+    auto load = [&](int i) { D::fetch(i, h, at, wave, lane, columns, stage_at + after * kStageBytes); };
+    if (tid == 0) grown[after] = 0;
+    if (here && scoring) {
+      s = D::scores(stage[u] + (16 * tg + ln) * LP, rotary[par] + (h * kHalf + 16 * tg + ln) * RP, qf, ln, lg, load);
+      if (t * kTile + (h + 1) * kHalf > len - (p.Q - 1) || of_half(live, h) != ~0u) {
+        const int sees = len - sees_less;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tk = h * kHalf + 16 * tg + 4 * lg + i;
+          if (t * kTile + tk >= sees || !((live >> tk) & 1)) s[i] = -INFINITY;
+        }
+      }
+      float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      mx = max_halves(max_quarters(mx)) * p.scale2;
+      if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
+      if (__any(mx > m + 8.f)) {
+        if (lane == 0) grown[u] = 1;
+      }
+      weigh(h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D::kLat; ++i) load(i);
+    }
+    if (pending) D::values(stage[before], prob[h ^ 1], wave, ln, lg, acc);
+    pending = here;
+    if (h == 1 && (!more || nn != n)) {
+      // the piece's last half
+      lds_barrier();
+      if (pending) {
+        settle(1, u);
+        D::values(stage[u], prob[1], wave, ln, lg, acc);
+        pending = false;
+      }
+    }
+  };
+
+  wait_loads<0>();
+  for (;; par ^= 1) {
+    half(std::integral_constant<int, 0>{});
+    half(std::integral_constant<int, 1>{});
     if (!more || nn != n) {
       // ---- the end of a piece: tiles [begin, t] of sequence n
+      if (more && scoring) load_q(nn);
       l = sum_halves(sum_quarters(l));
       lds_barrier();
       const int ln = keep_here(lane & 15), lg = keep_here(lane >> 4);
@@ -470,9 +493,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       for (int j = 0; j < NB; ++j) {
         const int row = rb * MB + j * 16 + ln;
         if (row < p.rows) {
-          float sum = smax[0][j * 16 + ln];
-#pragma unroll
-          for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
+          const float sum = smax[0][j * 16 + ln] + smax[1][j * 16 + ln];
           const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
           const float lse2 = sum == 0.f ? -INFINITY : sfac[j * 16 + ln] + __log2f(sum);
 #pragma unroll
@@ -500,11 +521,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i][j] = f32x4{0, 0, 0, 0};
       }
+      wait_loads<0>();  // the queries are there, and no load to LDS outlives the workgroup
       if (!more) return;
       m = -INFINITY;
       l = 0.f;
       begin = nt;
-      if (scoring) load_q(nn);
     }
     n = nn;
     t = nt;

@@ -31,16 +31,15 @@ struct PrefillParams {
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
-// DK: D + R rounded up, EP: E rounded up, W: waves (32 queries each)
-template <int DK, int EP, int W>
+// DP, RP, EP: D, R and E rounded up to what the kernel is built for; W: waves
+// (32 queries each)
+template <int DP, int RP, int EP, int W>
 __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams p) {
-  constexpr int KC = (DK + 63) / 64 * 8;  // 16-byte chunks of a staged key row
-  constexpr int VC = EP / 8;              // and of a value row
-  constexpr int KS = DK / 16;
+  constexpr int KC = DP / 8, RC = RP / 8, VC = EP / 8;  // 16-byte chunks of a staged row
+  constexpr int KS = (DP + RP) / 16;
   constexpr int MT = EP / 32;
-  constexpr int kThreads = W * 64;
-  constexpr int kStage = kTile * (KC + VC) * 8;
-  __shared__ __attribute__((aligned(16))) __bf16 lds[2 * kStage];
+  constexpr int kKeyBytes = kTile * DP * 2, kRotBytes = kTile * RP * 2, kStage = kKeyBytes + kRotBytes + kTile * EP * 2;
+  __shared__ __attribute__((aligned(16))) char lds[2 * kStage];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 31, lh = lane >> 5;
@@ -92,7 +91,11 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
     for (int s = 0; s < KS; ++s) {
       const int c = 16 * s + 8 * lh;
       bf16x8 v = {};
-      if (c < p.D + p.R) v = *reinterpret_cast<const bf16x8*>(qp + c);
+      if (s < DP / 16) {
+        if (c < p.D) v = *reinterpret_cast<const bf16x8*>(qp + c);
+      } else {
+        if (c - DP < p.R) v = *reinterpret_cast<const bf16x8*>(qp + p.D + (c - DP));
+      }
       qf[s] = v;
     }
   }
@@ -110,62 +113,101 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
     for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
   float m = -INFINITY, l = 0.f;  // in units of scale2 s
 
-  const int DC = p.D / 8, RC = p.R / 8, EC = p.E / 8;
-  if (DC + RC < KC || EC < VC) {  // padding columns are zero from here on
-    for (int i = tid; i < 2 * kStage / 8; i += kThreads) reinterpret_cast<u32x4*>(lds)[i] = u32x4{0, 0, 0, 0};
-    __syncthreads();
-  }
-  const __bf16* kbase = p.k + k0 * p.ks[0] + h * p.ks[1];
-  const __bf16* rbase = p.kr + k0 * p.krs;
-  const __bf16* vbase = p.v + k0 * p.vs[0] + h * p.vs[1];
-
-  // stages tile j (keys 64 j ..): chunk c of key row r at position c ^ (r & 7),
-  // of value row r at c ^ f(r); rows behind the last key are zero
-  auto vswz = [](int r) { return VC >= 16 ? (r & 7) << 1 : ((r >> 1) & 3) << 1; };
-  auto stage = [&](int j, __bf16* buf) {
-    __bf16* kt = buf;
-    __bf16* vt = buf + kTile * KC * 8;
+  // Staged rows: chunk c of a key or value row r lies at c ^ 2 (r & 7) (of 8
+  // chunks: c ^ ((r >> 1) & 3) * 2), of a rotary row at c ^ (r / (rows in 256
+  // B)), so that the 16-byte operand reads and the transposed reads of values
+  // fall on distinct banks.  Each region is filled by loads of whole rows; a
+  // lane's rows in successive loads differ by a multiple of 8, so its chunk is
+  // the same.  Padding columns get copies of a row's last chunk: the queries
+  // are 0 there and the outputs not written.
+  struct Region {
+    const char* base;  // key 0
+    int64_t step;      // bytes from key to key
+    unsigned col;      // the lane's chunk
+    int row;           // and its row in the first load
+  };
+  auto swz = [](int r, int chunks) { return chunks >= 16 ? (r & 7) << 1 : ((r >> 1) & 3) << 1; };
+  auto region = [&](const __bf16* base, int64_t stride, int chunks, int have, bool rotary) {
+    Region g;
+    g.base = reinterpret_cast<const char*>(base);
+    g.step = stride * 2;
+    g.row = (wave * 64 + lane) / chunks;
+    const int pos = lane % chunks, c = rotary ? pos ^ (g.row / (16 / chunks) % chunks) : pos ^ swz(g.row, chunks);
+    g.col = (unsigned)(c < have ? c : have - 1) * 16;
+    return g;
+  };
+  const Region kreg = region(p.k + k0 * p.ks[0] + h * p.ks[1], p.ks[0], KC, p.D / 8, false);
+  const Region rreg = region(p.kr + k0 * p.krs, p.krs, RC > 0 ? RC : 8, p.R / 8, true);
+  const Region vreg = region(p.v + k0 * p.vs[0] + h * p.vs[1], p.vs[0], VC, p.E / 8, false);
+  const unsigned lds_at = lds_offset(lds) + wave * 1024;
+  // loads of region g for the tile at key j0, of whose rows ``rows`` are there
+  // (the others get the last one's bytes: their weights are 0)
+  auto fill = [&](const Region& g, int chunks, int j0, int rows, unsigned to) {
+    const int per = W * 64 / chunks;  // rows of the workgroup's loads
+    const char* base = g.base + j0 * g.step;
+    if (rows >= kTile) {
+      const unsigned off = (unsigned)g.row * (unsigned)g.step + g.col;
 #pragma unroll
-    for (int i = 0; i < kTile * KC / kThreads; ++i) {
-      const int c0 = (i * W + wave) * 64, c = c0 + lane;
-      const int r = c / KC, src = (c - r * KC) ^ (r & 7);
-      const int key = j * kTile + r;
-      const bool have = src < DC + RC;
-      const __bf16* g = src < DC ? kbase + key * p.ks[0] + src * 8 : rbase + key * p.krs + (src - DC) * 8;
-      if (have && key < lk) load_lds16(g, kt + c0 * 8);
-      if (have && key >= lk) reinterpret_cast<u32x4*>(kt)[c] = u32x4{0, 0, 0, 0};
-    }
+      for (int i = 0; i < kTile / per; ++i) load_lds16(base + i * per * g.step, off, to + i * W * 1024);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kTile * VC / kThreads; ++i) {
-      const int c0 = (i * W + wave) * 64, c = c0 + lane;
-      const int r = c / VC, src = (c - r * VC) ^ vswz(r);
-      const int key = j * kTile + r;
-      if (src < EC && key < lk) load_lds16(vbase + key * p.vs[0] + src * 8, vt + c0 * 8);
-      if (src < EC && key >= lk) reinterpret_cast<u32x4*>(vt)[c] = u32x4{0, 0, 0, 0};
+      for (int i = 0; i < kTile / per; ++i) {
+        const int r = g.row + i * per < rows ? g.row + i * per : rows - 1;
+        load_lds16(base, (unsigned)r * (unsigned)g.step + g.col, to + i * W * 1024);
+      }
     }
   };
+  auto stage = [&](int j) {
+    const unsigned to = lds_at + (j & 1) * kStage;
+    const int rows = lk - j * kTile;
+    fill(kreg, KC, j * kTile, rows, to);
+    if (RP > 0) fill(rreg, RC > 0 ? RC : 8, j * kTile, rows, to + kKeyBytes);
+    fill(vreg, VC, j * kTile, rows, to + kKeyBytes + kRotBytes);
+  };
+
+  // the lane's places in a stage: key operands (row ln of a 32-row block,
+  // chunk 2 k + lh) and transposed value reads (4 rows x 16 columns a group)
+  const int kat = ln * DP * 2 + ((lh ^ swz(ln, KC)) << 4), rat = kKeyBytes + ln * RP * 2;
+  const int rx = RC > 0 ? ln / (16 / (RC > 0 ? RC : 8)) % (RC > 0 ? RC : 8) : 0;
+  const int vrow = 4 * lh + ((lane & 15) >> 2), vcol = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  const int vat = kKeyBytes + kRotBytes + vrow * EP * 2 + (lane & 1) * 8;
 
   const int ntiles = (end + kTile - 1) / kTile;
-  if (ntiles > 0) stage(0, lds);
+  if (ntiles > 0) stage(0);
   for (int j = 0; j < ntiles; ++j) {
-    wait_loads();
-    __syncthreads();
-    if (j + 1 < ntiles) stage(j + 1, lds + ((j + 1) & 1) * kStage);
-    const __bf16* kt = lds + (j & 1) * kStage;
-    const __bf16* vt = kt + kTile * KC * 8;
+    wait_loads<0>();
+    lds_barrier();  // tile j is there, and the readers of tile j - 1 are done
+    if (j + 1 < ntiles) stage(j + 1);
+    const char* buf = lds + (j & 1) * kStage;
 
+    // ---- scores, operands read a group ahead
     f32x16 s[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+    {
+      constexpr int F = 2 * KS, G = 4;
+      bf16x8 kf[2][G];
+      auto read = [&](int g) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
+        for (int i = 0; i < G; ++i) {
+          const int f = g * G + i, k = f / 2, b = f % 2;
+          if (f >= F) continue;
+          const char* at = k < DP / 16 ? buf + (kat ^ (k % 8 * 32)) + k / 8 * 256 + b * 32 * DP * 2
+                                       : buf + rat + (((2 * (k - DP / 16) + lh) ^ rx) << 4) + b * 32 * RP * 2;
+          kf[g & 1][i] = *reinterpret_cast<const bf16x8*>(at);
+        }
+      };
+      read(0);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int r = 32 * b + ln;
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kt + (r * KC + ((2 * k + lh) ^ (r & 7))) * 8);
-        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k], s[b], 0, 0, 0);
+      for (int g = 0; g < F / G; ++g) {
+        if (g + 1 < F / G) read(g + 1);
+        hold_order();
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          s[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[g & 1][i], qf[(g * G + i) / 2], s[i & 1], 0, 0, 0);
+        hold_order();
       }
     }
     if (j * kTile + kTile > all_see || j * kTile + kTile > lk) {
@@ -182,16 +224,19 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-    mx = max_halves(mx);
-    const float mn = fmaxf(m, mx * p.scale2);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    if (__any(mn > m)) {
-      const float alpha = exp2_hw(m - base);
+    mx = max_halves(mx) * p.scale2;
+    // The maximum in use follows the true one only when that has grown by more
+    // than 8 (a factor of 256): the weights stay far inside the range and the
+    // output is seldom rescaled.
+    if (__any(mx > m + 8.f)) {
+      const float mn = mx > m + 8.f ? mx : m;
+      const float alpha = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
 #pragma unroll
       for (int i = 0; i < MT; ++i) acc[i] *= alpha;
       l *= alpha;
+      m = mn;
     }
-    m = mn;
+    const float base = m == -INFINITY ? 0.f : m;
     // weights: bf16 for the matrix unit (the values' own type), their sum fp32
     bf16x8 pf[2][2];
 #pragma unroll
@@ -202,19 +247,32 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
         l += e;
         pf[b][i >> 3][i & 7] = (__bf16)e;
       }
-    // step (b, u): tokens 32 b + 16 u + {4 lh .. + 3, 8 + 4 lh .. + 3}
+    // ---- step (b, u): keys 32 b + 16 u + {4 lh .. + 3, 8 + 4 lh .. + 3}
+    {
+      constexpr int F = 4 * MT, G = 2;
+      bf16x8 vf[2][G];
+      auto read = [&](int g) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int col = 32 * i + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-          const int r0 = 32 * b + 16 * u + 4 * lh + ((lane & 15) >> 2), r1 = r0 + 8;
-          const s16x4 lo = read_tr(vt + (r0 * VC + ((col >> 3) ^ vswz(r0))) * 8 + (col & 7));
-          const s16x4 hi = read_tr(vt + (r1 * VC + ((col >> 3) ^ vswz(r1))) * 8 + (col & 7));
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(join(lo, hi), pf[b][u], acc[i], 0, 0, 0);
+        for (int q = 0; q < G; ++q) {
+          const int f = g * G + q, bu = f / MT, i = f % MT;
+          // rows vrow + 16 bu and 8 further on: the same chunk
+          const char* at = buf + vat + (((4 * i + vcol) ^ swz(vrow, VC)) << 4) + bu * 16 * EP * 2;
+          vf[g & 1][q] = join(read_tr(at), read_tr(at + 8 * EP * 2));
         }
+      };
+      read(0);
+#pragma unroll
+      for (int g = 0; g < F / G; ++g) {
+        if (g + 1 < F / G) read(g + 1);
+        hold_order();
+#pragma unroll
+        for (int q = 0; q < G; ++q) {
+          const int f = g * G + q, bu = f / MT, i = f % MT;
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[g & 1][q], pf[bu >> 1][bu & 1], acc[i], 0, 0, 0);
+        }
+        hold_order();
+      }
+    }
   }
 
   l = sum_halves(l);
@@ -235,14 +293,19 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
   }
 }
 
-template <int DK, int EP>
+template <int DP, int RP, int EP>
 hipError_t launch(PrefillParams& p, hipStream_t stream) {
   constexpr int W = 4;
   p.tiles = (int)((p.T + 32 * W - 1) / (32 * W) + p.N);
   const int64_t items = (int64_t)p.tiles * p.H;
-  hipLaunchKernelGGL((latent_prefill_kernel<DK, EP, W>), dim3((unsigned)((items + 7) / 8 * 8)), dim3(W * 64), 0,
+  hipLaunchKernelGGL((latent_prefill_kernel<DP, RP, EP, W>), dim3((unsigned)((items + 7) / 8 * 8)), dim3(W * 64), 0,
                      stream, p);
   return hipGetLastError();
+}
+
+template <int DP, int EP>
+hipError_t launch_r(PrefillParams& p, hipStream_t stream) {
+  return p.R == 0 ? launch<DP, 0, EP>(p, stream) : (p.R <= 32 ? launch<DP, 32, EP>(p, stream) : launch<DP, 64, EP>(p, stream));
 }
 
 }  // namespace
@@ -272,10 +335,7 @@ hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t
   p.E = (int)a.E;
   p.causal = a.causal != 0;
   p.scale2 = a.scale * kLog2e;
-  const int64_t dk = a.D + a.R;
-  if (dk <= 96 && a.E <= 64) return launch<96, 64>(p, stream);
-  if (dk <= 128) return launch<128, 128>(p, stream);
-  return launch<192, 128>(p, stream);
+  return a.D <= 64 && a.E <= 64 ? launch_r<64, 64>(p, stream) : launch_r<128, 128>(p, stream);
 }
 
 }  // namespace kda
