@@ -49,6 +49,7 @@ struct DecodeParams {
   __bf16* out;
   float* lse;
   int N, Q, H, rows, row_blocks, groups;
+  int few;         // up to 256 sequences and 2^28 tokens each
   float scale2;    // scale log2 e
   float* part;     // [row_blocks][2 groups][MB][L] normalised outputs
   float* plse;     // [row_blocks][2 groups][MB] log2 of the sums
@@ -62,52 +63,86 @@ __device__ __forceinline__ int seq_tokens(const DecodeParams& p, int n) {
 }
 __device__ __forceinline__ int tiles_of(int tokens) { return (int)(((int64_t)tokens + kTile - 1) / kTile); }
 
-// Sum of the sequences' tiles, the same in all threads.
-__device__ int64_t total_tiles(const DecodeParams& p, int64_t* red) {
-  int64_t mine = 0;
-  for (int n = threadIdx.x; n < p.N; n += kThreads) mine += tiles_of(seq_tokens(p, n));
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) mine += __shfl_xor(mine, d, 64);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mine;
-  __syncthreads();
-  int64_t all = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) all += red[i];
-  return all;
-}
-
-// The sequence that holds tile x of the line, and the line position of its
-// first tile: each wave scans the lengths 64 at a time.
-__device__ void find_tile(const DecodeParams& p, int64_t x, int lane, int* seq, int64_t* first) {
-  int64_t base = 0;
-  for (int n0 = 0; n0 < p.N; n0 += 64) {
-    const int c = n0 + lane < p.N ? tiles_of(seq_tokens(p, n0 + lane)) : 0;
-    const int incl = wave_scan(c, lane);
-    const unsigned long long past = __ballot(base + incl > x);
-    if (past) {
-      const int i = __ffsll(past) - 1;
-      *seq = n0 + i;
-      *first = base + __shfl(incl - c, i, 64);
-      return;
-    }
-    base += __shfl(incl, 63, 64);
-  }
-  *seq = p.N;
-  *first = base;
-}
-
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t lane64(int64_t x, int src) {  // src is uniform
   const int lo = __builtin_amdgcn_readlane((int)x, src), hi = __builtin_amdgcn_readlane((int)(x >> 32), src);
   return ((int64_t)hi << 32) | (unsigned)lo;
 }
 
-// The kernel's arguments, read again where this is called: what only the ends
-// of pieces need does not occupy scalar registers in the tile loop.
-__device__ __forceinline__ const DecodeParams* cold_params() {
-  auto k = (const __attribute__((address_space(4))) DecodeParams*)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(k));
-  return (const DecodeParams*)k;
+// Share w of the line: its tiles and where they begin.
+struct Share {
+  int left;  // tiles, 0: no such share
+  int n, t;  // sequence and tile of the first one
+};
+
+// Shares are as equal as they can be and none is empty (there are fewer of
+// them where there are fewer tiles).
+__device__ __forceinline__ int64_t share_begin(const DecodeParams& p, int64_t total, int w, int* left) {
+  const int64_t shares = total < p.groups ? total : p.groups;
+  int64_t quot = 1, rem = 0;
+  if (total >= p.groups) {
+    quot = total <= 0xffffffffll ? (int64_t)((uint32_t)total / (uint32_t)p.groups) : total / p.groups;
+    rem = total - quot * p.groups;
+  }
+  *left = w < shares ? (int)(quot + (w < rem ? 1 : 0)) : 0;
+  return w * quot + (w < rem ? w : rem);
+}
+
+// Every wave scans the lengths by itself: one pass with four sequences a lane
+// where that holds them all (their lengths then go to LDS, too), else 64 at a
+// time, once for the sum and once for the place.
+__device__ __forceinline__ Share find_share(const DecodeParams& p, int w, int lane, int32_t* lens) {
+  Share s;
+  if (p.few) {
+    int c[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = 4 * lane + j;
+      const int tokens = n < p.N ? seq_tokens(p, n) : 0;
+      if (threadIdx.x < 64) lens[n] = tokens;
+      c[j] = tiles_of(tokens);
+      sum += c[j];
+    }
+    const int incl = wave_scan(sum, lane);
+    const int t0 = (int)share_begin(p, __builtin_amdgcn_readlane(incl, 63), w, &s.left);
+    const unsigned long long past = __ballot(incl > t0);
+    if (s.left == 0 || past == 0) {
+      s.left = 0;
+      return s;
+    }
+    const int i = __ffsll(past) - 1;
+    s.t = t0 - __builtin_amdgcn_readlane(incl - sum, i);
+    s.n = 4 * i;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int x = __builtin_amdgcn_readlane(c[j], i);
+      if (s.n == 4 * i + j && s.t >= x) {
+        s.t -= x;
+        ++s.n;
+      }
+    }
+    return s;
+  }
+  int64_t total = 0;
+  for (int n = lane; n < p.N; n += 64) total += tiles_of(seq_tokens(p, n));
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d, 64);
+  const int64_t t0 = share_begin(p, lane64(total, 0), w, &s.left);
+  int64_t base = 0;
+  for (int n0 = 0; s.left > 0 && n0 < p.N; n0 += 64) {
+    const int c = n0 + lane < p.N ? tiles_of(seq_tokens(p, n0 + lane)) : 0;
+    const int incl = wave_scan(c, lane);
+    const unsigned long long past = __ballot(base + incl > t0);
+    if (past) {
+      const int i = __ffsll(past) - 1;
+      s.n = n0 + i;
+      s.t = (int)(t0 - base) - __builtin_amdgcn_readlane(incl - c, i);
+      return s;
+    }
+    base += __builtin_amdgcn_readlane(incl, 63);
+  }
+  s.left = 0;
+  return s;
 }
 
 // LP, RP: L and R rounded up to what the kernel is built for; NB: blocks of 16
@@ -168,14 +203,12 @@ struct Decode {
   }
 
   // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i.
-  // Operands are read a group ahead of their products, and load(i),
-  // 0 <= i < kLat, is called along the way.
-  template <typename Load>
+  // Operands are read a group ahead of their products.
   static __device__ __forceinline__ f32x4 scores(const __bf16* lat_row, const __bf16* rot_row, const bf16x8 (&qf)[KS],
-                                                 int ln, int lg, const Load& load) {
+                                                 int ln, int lg) {
     const char *lat = reinterpret_cast<const char*>(lat_row), *rot = reinterpret_cast<const char*>(rot_row);
     const int x = (lg ^ ((ln & 7) << 1)) * 16, y = (lg ^ ((ln >> 1) & 7)) * 16;
-    constexpr int G = 6, NG = (KS + G - 1) / G, LG = (kLat + NG - 1) / NG;
+    constexpr int G = NB == 4 ? 4 : 6, NG = (KS + G - 1) / G;
     bf16x8 kf[2][G];
     auto read = [&](int g) {
 #pragma unroll
@@ -192,8 +225,6 @@ struct Decode {
     for (int g = 0; g < NG; ++g) {
       if (g + 1 < NG) read(g + 1);
       hold_order();
-#pragma unroll
-      for (int i = g * LG; i < kLat && i < (g + 1) * LG; ++i) load(i);
 #pragma unroll
       for (int i = 0; i < G; ++i)
         if (g * G + i < KS)
@@ -242,7 +273,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
   __shared__ int32_t pages[2][kWaves][64];  // page of token 64 t + lane of the tile fetched next
   __shared__ int grown[4];        // whether a row's maximum has grown much in half u, at u % 4
-  __shared__ int64_t red[kWaves];
+  __shared__ int32_t lens[256];            // the sequences' tokens (few)
+  __shared__ int64_t qat[2][MB];           // of a query row: its q and q_rope in a sequence's
+  __shared__ int32_t less[MB];             // and how many tokens less than the last one it sees
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, lg = lane >> 4;
@@ -251,22 +284,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
   const int rb = idx % p.row_blocks, w = (idx / p.row_blocks) * 8 + xcd;
 
-  const int64_t total = lane64(total_tiles(p, red), 0);
-  const int64_t shares = total < p.groups ? total : p.groups;  // none is empty
-  if (w >= shares) return;
-  const int64_t t0 = w * total / shares;
-  int left = uniform((int)((w + 1) * total / shares - t0));  // tiles of this share not fetched yet
-  int n = 0;
-  int64_t first = 0;
-  find_tile(p, t0, lane, &n, &first);
-  n = uniform(n);
-
+  const Share share = find_share(p, w, lane, lens);
+  if (share.left == 0) return;
+  if (tid < MB) {
+    // (rows behind the last get the first one's queries; they are not written)
+    const int row = rb * MB + tid < p.rows ? rb * MB + tid : 0, qi = row / p.H, qh = row - qi * p.H;
+    qat[0][tid] = qi * p.qs[1] + qh * p.qs[2];
+    qat[1][tid] = qi * p.qrs[1] + qh * p.qrs[2];
+    less[tid] = p.Q - 1 - qi;
+  }
   if (tid < 4) grown[tid] = 0;
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;                  // query rows this wave scores
   const int tg = (wave / NB) % TG;               // and tokens
-  const int qrow = rb * MB + rblock * 16 + ln;
-  const int sees_less = p.Q - 1 - (qrow < p.rows ? qrow / p.H : 0);  // this lane's row sees so many tokens less
+  __syncthreads();
+  const int sees_less = less[rblock * 16 + ln];
+  auto tokens_of = [&](int n) { return uniform(p.few ? lens[n] : seq_tokens(p, n)); };
 
   // where the page of token 64 t + lane of sequence s is, which has len tokens
   // (the last one's for lanes behind it), and that row's place; -1: no such row
@@ -282,26 +315,27 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   };
   bf16x8 qf[KS];
   auto load_q = [&](int s) {
-    const DecodeParams p = *cold_params();
-    const int row = keep_here(qrow), qi = row < p.rows ? row / p.H : 0, qh = row < p.rows ? row % p.H : 0;
-    const int lg = keep_here(lane >> 4);
-    const __bf16* qp = p.q + s * p.qs[0] + qi * p.qs[1] + qh * p.qs[2];
-    const __bf16* qrp = p.qr + s * p.qrs[0] + qi * p.qrs[1] + qh * p.qrs[2];
+    const __bf16* qp = p.q + s * p.qs[0] + qat[0][rblock * 16 + ln] + 8 * lg;
+    const __bf16* qrp = p.qr + s * p.qrs[0] + qat[1][rblock * 16 + ln] + 8 * lg;
+    if (p.L == LP && p.R == RP) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int c = 32 * k + 8 * lg;
-      bf16x8 x = {};
-      if (k < LP / 32) {
-        if (row < p.rows && c < p.L) x = *reinterpret_cast<const bf16x8*>(qp + c);
-      } else {
-        if (row < p.rows && c - LP < p.R) x = *reinterpret_cast<const bf16x8*>(qrp + (c - LP));
+      for (int k = 0; k < KS; ++k)
+        qf[k] = *reinterpret_cast<const bf16x8*>(k < LP / 32 ? qp + 32 * k : qrp + (32 * k - LP));
+    } else {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int c = 32 * k + 8 * lg;
+        bf16x8 x = {};
+        if (k < LP / 32 ? c < p.L : c - LP < p.R)
+          x = *reinterpret_cast<const bf16x8*>(k < LP / 32 ? qp + 32 * k : qrp + (32 * k - LP));
+        qf[k] = x;
       }
-      qf[k] = x;
     }
   };
 
   // the tile being computed: t of sequence n; the one fetched next: ft of sequence fn
-  int t = uniform((int)(t0 - first)), len = uniform(seq_tokens(p, n)), tiles = tiles_of(len), begin = t;
+  int n = uniform(share.n), t = uniform(share.t), left = uniform(share.left), len = tokens_of(n), tiles = tiles_of(len),
+      begin = t;
   const char* at;                  // rows of the tile fetched next
   unsigned long long live, nlive;  // which rows of the tile computed, and of that one, are there
   // Rows that are not there are fetched from the first one that is (their
@@ -334,7 +368,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   auto advance = [&]() {
     if (++ft < ftiles) return;
     ft = 0;
-    do flen = uniform(seq_tokens(p, ++fn));
+    do flen = tokens_of(++fn);
     while ((ftiles = tiles_of(flen)) == 0);
   };
   if (left > 0) {
@@ -431,10 +465,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       D::fetch_rotary(at, wave, lane, columns, rotary_at + (par ^ 1) * kRotaryBytes);
     }
     const bool here = of_half(live, h) != 0;
-    auto load = [&](int i) { D::fetch(i, h, at, wave, lane, columns, stage_at + after * kStageBytes); };
+    // (first of all: from here to the barrier two halves on is what a load has)
+#pragma unroll
+    for (int i = 0; i < D::kLat; ++i) D::fetch(i, h, at, wave, lane, columns, stage_at + after * kStageBytes);
     if (tid == 0) grown[after] = 0;
     if (here && scoring) {
-      s = D::scores(stage[u] + (16 * tg + ln) * LP, rotary[par] + (h * kHalf + 16 * tg + ln) * RP, qf, ln, lg, load);
+      s = D::scores(stage[u] + (16 * tg + ln) * LP, rotary[par] + (h * kHalf + 16 * tg + ln) * RP, qf, ln, lg);
       if (t * kTile + (h + 1) * kHalf > len - (p.Q - 1) || of_half(live, h) != ~0u) {
         const int sees = len - sees_less;
 #pragma unroll
@@ -450,9 +486,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (lane == 0) grown[u] = 1;
       }
       weigh(h);
-    } else {
-#pragma unroll
-      for (int i = 0; i < D::kLat; ++i) load(i);
     }
     if (pending) D::values(stage[before], prob[h ^ 1], wave, ln, lg, acc);
     pending = here;
@@ -482,44 +515,43 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (tg == 0) sfac[rblock * 16 + ln] = m;
       }
       lds_barrier();
-      const DecodeParams p = *cold_params();
       const bool whole = begin == 0 && t == tiles - 1;
-      const int slot = 2 * w + (begin > 0 ? 0 : 1);
+      const int slot = rb * 2 * p.groups + 2 * w + (begin > 0 ? 0 : 1);
       if (tid == 0 && rb == 0) {
         if (begin == 0) p.shared[2 * n] = w;
         if (t == tiles - 1) p.shared[2 * n + 1] = w;
       }
+      const int row0 = rb * MB + ln, col0 = wave * (MT * 16) + 4 * lg;
+      __bf16* out = p.out + ((int64_t)n * p.rows + row0) * p.L + col0;
+      float* part = p.part + ((int64_t)slot * MB + ln) * p.L + col0;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const int row = rb * MB + j * 16 + ln;
-        if (row < p.rows) {
-          const float sum = smax[0][j * 16 + ln] + smax[1][j * 16 + ln];
-          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-          const float lse2 = sum == 0.f ? -INFINITY : sfac[j * 16 + ln] + __log2f(sum);
+        const int row = row0 + j * 16;
+        const float sum = smax[0][j * 16 + ln] + smax[1][j * 16 + ln];
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const int col = wave * (MT * 16) + 16 * i + 4 * lg;
-            if (col < p.L) {
-              const f32x4 o = acc[i][j] * inv;
-              if (whole) {
-                const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-                *reinterpret_cast<bf16x4*>(p.out + ((int64_t)n * p.rows + row) * p.L + col) = ob;
-              } else {
-                *reinterpret_cast<f32x4*>(p.part + (((int64_t)rb * 2 * p.groups + slot) * MB + j * 16 + ln) * p.L +
-                                          col) = o;
-              }
-            }
-          }
-          if (wave == 0 && lg == 0) {
+        for (int i = 0; i < MT; ++i) {
+          if (row < p.rows && col0 + 16 * i < p.L) {
+            const f32x4 o = acc[i][j] * inv;
             if (whole) {
-              if (p.lse) p.lse[(int64_t)n * p.rows + row] = lse2 * kLn2;
+              const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+              *reinterpret_cast<bf16x4*>(out + 16 * i) = ob;
             } else {
-              p.plse[((int64_t)rb * 2 * p.groups + slot) * MB + j * 16 + ln] = lse2;
+              *reinterpret_cast<f32x4*>(part + 16 * i) = o;
             }
           }
+          acc[i][j] = f32x4{0, 0, 0, 0};
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][j] = f32x4{0, 0, 0, 0};
+        out += 16 * p.L;
+        part += 16 * p.L;
+      }
+      if (tid < MB && rb * MB + tid < p.rows) {
+        const float sum = smax[0][tid] + smax[1][tid];
+        const float lse2 = sum == 0.f ? -INFINITY : sfac[tid] + __log2f(sum);
+        if (!whole)
+          p.plse[(int64_t)slot * MB + tid] = lse2;
+        else if (p.lse)
+          p.lse[(int64_t)n * p.rows + rb * MB + tid] = lse2 * kLn2;
       }
       wait_loads<0>();  // the queries are there, and no load to LDS outlives the workgroup
       if (!more) return;
@@ -678,6 +710,7 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   p.rows = (int)(a.Q * a.H);
   p.row_blocks = s.row_blocks;
   p.groups = s.groups;
+  p.few = a.N <= 256 && a.max_pages <= ((int64_t)1 << 28) / a.page_size;
   p.scale2 = a.scale * kLog2e;
   p.part = static_cast<float*>(a.workspace);
   p.plse = p.part + part_rows(s) * a.L;
