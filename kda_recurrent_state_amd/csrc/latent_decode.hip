@@ -208,7 +208,7 @@ struct Decode {
                                                  int ln, int lg) {
     const char *lat = reinterpret_cast<const char*>(lat_row), *rot = reinterpret_cast<const char*>(rot_row);
     const int x = (lg ^ ((ln & 7) << 1)) * 16, y = (lg ^ ((ln >> 1) & 7)) * 16;
-    constexpr int G = NB == 4 ? 4 : 6, NG = (KS + G - 1) / G;
+    constexpr int G = NB == 4 ? 3 : 6, NG = (KS + G - 1) / G;
     bf16x8 kf[2][G];
     auto read = [&](int g) {
 #pragma unroll
@@ -268,11 +268,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG;
   __shared__ __attribute__((aligned(16))) __bf16 stage[kStages][D::kStage];
   __shared__ __attribute__((aligned(16))) __bf16 rotary[2][RP > 0 ? kTile * RP : 8];
-  __shared__ __attribute__((aligned(16))) __bf16 prob[2][MB * kHalf];
+  __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kHalf];
   __shared__ float smax[TG][MB];  // of a half; at a piece's end the sums
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
-  __shared__ int32_t pages[2][kWaves][64];  // page of token 64 t + lane of the tile fetched next
-  __shared__ int grown[4];        // whether a row's maximum has grown much in half u, at u % 4
+  __shared__ int32_t pages[2][kWaves][64];  // page of token 64 t + lane of the tile located next
+  __shared__ int grown[2];        // whether a row's maximum has grown much in half h
   __shared__ int32_t lens[256];            // the sequences' tokens (few)
   __shared__ int64_t qat[2][MB];           // of a query row: its q and q_rope in a sequence's
   __shared__ int32_t less[MB];             // and how many tokens less than the last one it sees
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     qat[1][tid] = qi * p.qrs[1] + qh * p.qrs[2];
     less[tid] = p.Q - 1 - qi;
   }
-  if (tid < 4) grown[tid] = 0;
+  if (tid < 2) grown[tid] = 0;
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;                  // query rows this wave scores
   const int tg = (wave / NB) % TG;               // and tokens
@@ -333,48 +333,70 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
   };
 
-  // the tile being computed: t of sequence n; the one fetched next: ft of sequence fn
-  int n = uniform(share.n), t = uniform(share.t), left = uniform(share.left), len = tokens_of(n), tiles = tiles_of(len),
-      begin = t;
-  const char* at;                  // rows of the tile fetched next
-  unsigned long long live, nlive;  // which rows of the tile computed, and of that one, are there
+  // The tiles in hand: the one computed, the next two, and the one after them,
+  // whose pages are being looked up.  ``left`` counts the share's tiles behind
+  // that one.
+  struct Tile {
+    int n, t, len;            // tile t of sequence n, which has len tokens
+    unsigned long long live;  // which rows are there
+  };
+  int left = uniform(share.left);
+  bool ahead = false;  // whether there is a tile behind the last one located
+  Tile cur, next, then, ask;
+  const char* at;      // rows of the last tile located (lane i: token i)
   // Rows that are not there are fetched from the first one that is (their
   // weights are 0), or, if there is none, from the cache's first (a half
   // without rows is not computed): every half has the same number of loads.
-  auto locate = [&](int page, int t, int len) {
-    int64_t row = place(page, t, len);
-    nlive = __ballot(row >= 0);
-    if (nlive != ~0ull) {
-      const int64_t some = nlive != 0 ? lane64(row, __ffsll(nlive) - 1) : 0;
+  auto locate = [&](int page, Tile& x) {
+    int64_t row = place(page, x.t, x.len);
+    x.live = __ballot(row >= 0);
+    if (x.live != ~0ull) {
+      const int64_t some = x.live != 0 ? lane64(row, __ffsll(x.live) - 1) : 0;
       row = row < 0 ? some : row;
     }
     at = reinterpret_cast<const char*>(p.cache + row);
   };
+  auto follow = [&](Tile& x) {  // the tile behind x
+    if (++x.t < tiles_of(x.len)) return;
+    x.t = 0;
+    do x.len = tokens_of(++x.n);
+    while (x.len == 0);
+  };
   const unsigned stage_at = lds_offset(stage), rotary_at = lds_offset(rotary), pages_at = lds_offset(pages[0][wave]);
   constexpr unsigned kStageBytes = D::kStage * 2, kRotaryBytes = sizeof(rotary[0]), kPagesBytes = sizeof(pages[0]);
   const typename D::Columns columns = D::columns(p, wave, lane);
-
-  auto of_half = [](unsigned long long x, int h) { return (unsigned)(x >> (h * 32)); };
-  locate(*lookup(n, t, len), t, len);
-  live = nlive;
-  D::fetch_rotary(at, wave, lane, columns, rotary_at);
+  auto fetch = [&](int h, int to) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < D::kLat; ++i) D::fetch(i, h, at, wave, lane, columns, stage_at + h * kStageBytes);
-  if (scoring) load_q(n);
-  --left;
-  int fn = n, ft = t, flen = len, ftiles = tiles;
-  auto advance = [&]() {
-    if (++ft < ftiles) return;
-    ft = 0;
-    do flen = tokens_of(++fn);
-    while ((ftiles = tiles_of(flen)) == 0);
+    for (int i = 0; i < D::kLat; ++i) D::fetch(i, h, at, wave, lane, columns, stage_at + to * kStageBytes);
   };
-  if (left > 0) {
-    advance();
-    load_lds4(lookup(fn, ft, flen), pages_at);
+
+  // three halves on their way: both of the first tile, one of the second
+  cur.n = uniform(share.n);
+  cur.t = uniform(share.t);
+  cur.len = tokens_of(cur.n);
+  const int page0 = *lookup(cur.n, cur.t, cur.len);
+  next = cur;
+  next.live = 0;
+  int page1 = -1;
+  if (--left > 0) {
+    follow(next);
+    page1 = *lookup(next.n, next.t, next.len);
   }
+  locate(page0, cur);
+  D::fetch_rotary(at, wave, lane, columns, rotary_at);
+  fetch(0, 0);
+  fetch(1, 1);
+  bool more = left > 0;  // whether ``next`` is a tile of the share
+  if (more) locate(page1, next);
+  fetch(0, 2);
+  then = ask = next;
+  if (more && --left > 0) {
+    follow(ask);
+    load_lds4(lookup(ask.n, ask.t, ask.len), pages_at + kPagesBytes);
+    ahead = true;
+  }
+  if (scoring) load_q(cur.n);
+  int begin = cur.t;
 
   float m = -INFINITY, l = 0.f;  // of row ln of the wave's block, over its tokens; units of scale2 s
   f32x4 acc[MT][NB];
@@ -383,40 +405,84 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  // The loop's unit is a half (32 tokens).  While half u is scored, the output
-  // product of half u - 1 follows without a barrier in between, so that one
-  // wave's products overlap the other wave's softmax on the same SIMD, and
-  // halves u + 1 and u + 2 are on their way.
-  f32x4 s = {0, 0, 0, 0};
-  float sum = 0.f;
-  bool pending = false, more = false;
-  int par = 0;  // of the tile: its stages are 2 par, 2 par + 1
-  int nn = n, nt = t, nlen = len, ntiles = tiles;
-
-  // Weights of the scores against the maximum in use, for the matrix unit in
-  // bf16, the values' own type; their sum stays in fp32.
-  auto weigh = [&](int h) {
-    const float base = m == -INFINITY ? 0.f : m;
-    bf16x4 pb;
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = exp2_hw(fmaf(s[i], p.scale2, -base));
-      sum += e;
-      pb[i] = (__bf16)e;
+  // The loop's unit is a half (32 tokens): half u = 2 par + h is computed while
+  // halves u + 1 and u + 2 are on their way and u + 3 is sent for.
+  int par = 0;
+  auto half = [&](auto hc) {
+    constexpr int h = decltype(hc)::value;
+    const int u = 2 * par + h, to = (u + 3) & 3;
+    // Half u (and with h == 0 its tile's rotary rows) has landed when at most
+    // the loads issued after it are under way: those of the two halves that
+    // follow and, with h == 1, the next tile's rotary rows.  Pages looked up a
+    // tile ago came before those.
+    wait_loads<2 * D::kLat + (h == 1 && RP > 0 ? 1 : 0)>();
+    lds_barrier();  // and the readers of half u - 1 are done
+    if (tid == 0) grown[h ^ 1] = 0;
+    if (h == 0) {
+      D::fetch_rotary(at, wave, lane, columns, rotary_at + (par ^ 1) * kRotaryBytes);
+      fetch(1, to);
+    } else {
+      // the tile after the next one: located, and sent for
+      then = ask;
+      then.live = 0;
+      if (ahead) {
+        locate(pages[par ^ 1][wave][lane], then);
+        ahead = false;
+        if (--left > 0) {
+          follow(ask);
+          load_lds4(lookup(ask.n, ask.t, ask.len), pages_at + par * kPagesBytes);
+          ahead = true;
+        }
+      } else {
+        at = reinterpret_cast<const char*>(p.cache);
+        then.n = -1;
+      }
+      fetch(0, to);
     }
-    const int tk = 16 * tg + 4 * lg;
-    *reinterpret_cast<bf16x4*>(prob[h] + (rblock * 16 + ln) * kHalf + (((tk >> 3) ^ ((ln >> 1) & 3)) << 3) +
-                               (tk & 7)) = pb;
-  };
-  // Half u - 1 (of parity h), whose weights all waves have written: takes its
-  // sums, after a new exchange of maxima if some row's has grown.  The maximum
-  // in use follows the true one only when that is larger by more than 8 (a
-  // factor of 256): the weights stay far inside the range, and most halves
-  // need neither the exchange nor a rescaling of the output.
-  auto settle = [&](int h, int u) {
-    float fac = 1.f;
-    if (grown[u]) {
+    if ((unsigned)(cur.live >> (h * 32)) == 0) return;
+
+    float sum = 0.f, fac = 1.f;
+    f32x4 s;
+    // Weights of the scores against the maximum in use, for the matrix unit in
+    // bf16, the values' own type; their sum stays in fp32.
+    auto weigh = [&]() {
+      const float base = m == -INFINITY ? 0.f : m;
+      bf16x4 pb;
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2_hw(fmaf(s[i], p.scale2, -base));
+        sum += e;
+        pb[i] = (__bf16)e;
+      }
+      const int tk = 16 * tg + 4 * lg;
+      *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kHalf + (((tk >> 3) ^ ((ln >> 1) & 3)) << 3) + (tk & 7)) =
+          pb;
+    };
+    if (scoring) {
+      s = D::scores(stage[u] + (16 * tg + ln) * LP, rotary[par] + (h * kHalf + 16 * tg + ln) * RP, qf, ln, lg);
+      if (cur.t * kTile + (h + 1) * kHalf > cur.len - (p.Q - 1) || (unsigned)(cur.live >> (h * 32)) != ~0u) {
+        const int sees = cur.len - sees_less;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tk = h * kHalf + 16 * tg + 4 * lg + i;
+          if (cur.t * kTile + tk >= sees || !((cur.live >> tk) & 1)) s[i] = -INFINITY;
+        }
+      }
+      float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      mx = max_halves(max_quarters(mx)) * p.scale2;
+      if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
+      // The maximum in use follows the true one only when that is larger by
+      // more than 8 (a factor of 256): the weights stay far inside the range,
+      // and most halves need neither an exchange of maxima between the waves
+      // nor a rescaling of the output.
+      if (__any(mx > m + 8.f)) {
+        if (lane == 0) grown[h] = 1;
+      }
+      weigh();
+    }
+    lds_barrier();
+    if (grown[h]) {
       if (scoring) {
         const float mx = fmaxf(smax[0][rblock * 16 + ln], smax[1][rblock * 16 + ln]);
         const float mn = mx > m + 8.f ? mx : m;
@@ -425,7 +491,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
       }
       lds_barrier();  // (all have read the maxima; the weights are written again)
-      if (scoring) weigh(h);
+      if (scoring) weigh();
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const float f = sfac[j * 16 + ln];
@@ -435,78 +501,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       lds_barrier();
     }
     l = l * fac + sum;
-  };
-
-  auto half = [&](auto hc) {
-    constexpr int h = decltype(hc)::value;
-    const int u = 2 * par + h, before = (u + 3) & 3, after = (u + 2) & 3;  // stages of halves u, u - 1, u + 2
-    // Half u has landed when at most the loads issued after it are under way:
-    // those of half u + 1, after the first half's with the next tile's rotary
-    // rows and pages.
-    wait_loads<D::kLat + (h == 1 && RP > 0 ? 1 : 0)>();
-    lds_barrier();  // and the readers of half u - 2 are done
-    if (pending) settle(h ^ 1, before);
-    if (h == 0) {
-      more = left > 0;
-      nlive = 0;
-      nn = fn;
-      nt = ft;
-      nlen = flen;
-      ntiles = ftiles;
-      if (more) {
-        locate(pages[par][wave][lane], ft, flen);
-        if (--left > 0) {
-          advance();
-          load_lds4(lookup(fn, ft, flen), pages_at + (par ^ 1) * kPagesBytes);
-        }
-      } else {
-        at = reinterpret_cast<const char*>(p.cache);
-      }
-      D::fetch_rotary(at, wave, lane, columns, rotary_at + (par ^ 1) * kRotaryBytes);
-    }
-    const bool here = of_half(live, h) != 0;
-    // (first of all: from here to the barrier two halves on is what a load has)
-#pragma unroll
-    for (int i = 0; i < D::kLat; ++i) D::fetch(i, h, at, wave, lane, columns, stage_at + after * kStageBytes);
-    if (tid == 0) grown[after] = 0;
-    if (here && scoring) {
-      s = D::scores(stage[u] + (16 * tg + ln) * LP, rotary[par] + (h * kHalf + 16 * tg + ln) * RP, qf, ln, lg);
-      if (t * kTile + (h + 1) * kHalf > len - (p.Q - 1) || of_half(live, h) != ~0u) {
-        const int sees = len - sees_less;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tk = h * kHalf + 16 * tg + 4 * lg + i;
-          if (t * kTile + tk >= sees || !((live >> tk) & 1)) s[i] = -INFINITY;
-        }
-      }
-      float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-      mx = max_halves(max_quarters(mx)) * p.scale2;
-      if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
-      if (__any(mx > m + 8.f)) {
-        if (lane == 0) grown[u] = 1;
-      }
-      weigh(h);
-    }
-    if (pending) D::values(stage[before], prob[h ^ 1], wave, ln, lg, acc);
-    pending = here;
-    if (h == 1 && (!more || nn != n)) {
-      // the piece's last half
-      lds_barrier();
-      if (pending) {
-        settle(1, u);
-        D::values(stage[u], prob[1], wave, ln, lg, acc);
-        pending = false;
-      }
-    }
+    D::values(stage[u], prob, wave, ln, lg, acc);
   };
 
   wait_loads<0>();
   for (;; par ^= 1) {
     half(std::integral_constant<int, 0>{});
     half(std::integral_constant<int, 1>{});
-    if (!more || nn != n) {
+    if (!more || next.n != cur.n) {
+      const int n = cur.n, t = cur.t, tiles = tiles_of(cur.len);
       // ---- the end of a piece: tiles [begin, t] of sequence n
-      if (more && scoring) load_q(nn);
+      if (more && scoring) load_q(next.n);
       l = sum_halves(sum_quarters(l));
       lds_barrier();
       const int ln = keep_here(lane & 15), lg = keep_here(lane >> 4);
@@ -557,13 +562,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       if (!more) return;
       m = -INFINITY;
       l = 0.f;
-      begin = nt;
+      begin = next.t;
     }
-    n = nn;
-    t = nt;
-    len = nlen;
-    tiles = ntiles;
-    live = nlive;
+    cur = next;
+    next = then;
+    more = next.n >= 0;
   }
 }
 
