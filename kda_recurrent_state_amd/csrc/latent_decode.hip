@@ -26,9 +26,7 @@ namespace {
 
 using namespace latent;
 
-constexpr int kTile = 64;      // tokens a tile of the line: two halves
-constexpr int kHalf = 32;      // tokens a stage
-constexpr int kStages = 4;
+constexpr int kTile = 64;      // tokens a tile
 constexpr int kThreads = 512;  // 8 waves
 constexpr int kWaves = kThreads / 64;
 
@@ -154,10 +152,11 @@ struct Decode {
   static constexpr int LC = LP / 8;               // 16-byte chunks of a staged latent row
   static constexpr int KS = DP / 32;              // contraction steps of the scores
   static constexpr int MT = LP / (16 * kWaves);   // 16-column blocks of the output a wave
-  static constexpr int TG = 2;                    // groups of 16 tokens of a half
+  static constexpr int TG = NB == 4 ? 2 : 4;      // groups of tokens of a tile
+  static constexpr int TB = kTile / 16 / TG;      // blocks of 16 tokens a group
   static constexpr int kScoring = NB * TG;        // waves that score (a row block and a group each)
-  static constexpr int kStage = kHalf * LP;       // elements of a stage
-  static constexpr int kRows = kHalf / kWaves;    // rows a wave fetches
+  static constexpr int kStage = kTile * LP;       // elements of a stage
+  static constexpr int kRows = kTile / kWaves;    // rows a wave fetches
 
   // Chunk c of latent row r is staged at position c ^ 2 (r & 7): the 8 rows x
   // 16 B of a score operand and the 4 rows x 32 B of a transposed value read
@@ -165,35 +164,32 @@ struct Decode {
   // them; their chunk c is at c ^ ((r >> 1) & 7).
 
   static constexpr int RI = 64 / LC;       // latent rows a load covers
-  static constexpr int kLat = kRows / RI;  // latent loads of a wave for a half
+  static constexpr int kLat = kRows / RI;  // latent loads of a wave for a tile
 
   // What a lane adds to its rows' addresses.  Padding columns (L < LP, R < RP)
   // get copies of a row's last chunk: the queries are 0 there and the outputs
   // not written.
   struct Columns {
-    unsigned lat[kLat], rot;
+    unsigned lat, last, rot;
   };
   static __device__ __forceinline__ Columns columns(const DecodeParams& p, int wave, unsigned lane) {
     Columns c;
-    const unsigned last = (unsigned)(p.L - 8) * 2;
-#pragma unroll
-    for (int i = 0; i < kLat; ++i) {
-      const unsigned off = (lane % LC * 16) ^ ((wave * kRows + i * RI + lane / LC) % 8 * 32);
-      c.lat[i] = off < last ? off : last;
-    }
+    c.lat = (lane % LC * 16) ^ (lane / LC % 8 * 32);
+    c.last = (unsigned)(p.L - 8) * 2;
     const unsigned r = wave * 8 + lane / 8, off = (lane % 8 ^ r / 2 % 8) * 16, end = (unsigned)(p.R - 8) * 2;
     c.rot = (RP > 0 && off < end ? off : end) + p.L * 2;
     return c;
   }
-  // Latent load i of half h of the tile whose rows lie at ``at`` (lane i:
-  // token i), to the stage at ``lds``.
-  static __device__ __forceinline__ void fetch(int i, int h, const char* at, int wave, int lane, const Columns& c,
+  // Latent load i of the tile whose rows lie at ``at`` (lane i: token i), to
+  // the stage at ``lds``.
+  static __device__ __forceinline__ void fetch(int i, const char* at, int wave, int lane, const Columns& c,
                                                unsigned lds) {
-    const int r = h * kHalf + wave * kRows + i * RI;
+    const int r = wave * kRows + i * RI;
+    const unsigned off = c.lat ^ (unsigned)(i * RI % 8 * 32), col = off < c.last ? off : c.last;
     if (RI == 1) {
-      load_lds16((const char*)lane64((int64_t)at, r), c.lat[i], lds + (wave * kRows + i) * LP * 2);
+      load_lds16((const char*)lane64((int64_t)at, r), col, lds + r * LP * 2);
     } else {
-      load_lds16((const char*)__shfl((int64_t)at, r + lane / LC, 64) + c.lat[i], lds + (wave * kRows + i * RI) * LP * 2);
+      load_lds16((const char*)__shfl((int64_t)at, r + lane / LC, 64) + col, lds + r * LP * 2);
     }
   }
   // The tile's rotary rows, 8 a wave.
@@ -202,61 +198,79 @@ struct Decode {
     if (RP > 0) load_lds16((const char*)__shfl((int64_t)at, wave * 8 + lane / 8, 64) + c.rot, lds + wave * 8 * RP * 2);
   }
 
-  // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i.
-  // Operands are read a group ahead of their products.
-  static __device__ __forceinline__ f32x4 scores(const __bf16* lat_row, const __bf16* rot_row, const bf16x8 (&qf)[KS],
-                                                 int ln, int lg) {
+  // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i
+  // of each block.  Operands are read a group ahead of their products, and
+  // load(i), 0 <= i < kLat, is called along the way: a wave stands still while
+  // the memory pipeline takes a load, so they are spread over its products.
+  template <typename Load>
+  static __device__ __forceinline__ void scores(const __bf16* lat_row, const __bf16* rot_row, const bf16x8 (&qf)[KS],
+                                                int ln, int lg, f32x4 (&s)[TB], const Load& load) {
     const char *lat = reinterpret_cast<const char*>(lat_row), *rot = reinterpret_cast<const char*>(rot_row);
     const int x = (lg ^ ((ln & 7) << 1)) * 16, y = (lg ^ ((ln >> 1) & 7)) * 16;
-    constexpr int G = NB == 4 ? 3 : 6, NG = (KS + G - 1) / G;
+    constexpr int F = KS * TB, G = NB == 4 ? 4 : 6, NG = (F + G - 1) / G, LG = (kLat + NG - 1) / NG;
     bf16x8 kf[2][G];
     auto read = [&](int g) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const int k = g * G + i;
-        if (k >= KS) continue;
-        const char* at = k < LP / 32 ? lat + (x ^ ((k & 3) * 64)) + (k >> 2) * 256 : rot + (y ^ ((k - LP / 32) * 64));
+        const int f = g * G + i, k = f / TB, j = f % TB;
+        if (f >= F) continue;
+        const char* at = k < LP / 32 ? lat + (x ^ ((k & 3) * 64)) + (k >> 2) * 256 + j * 16 * LP * 2
+                                     : rot + (y ^ ((k - LP / 32) * 64)) + j * 16 * RP * 2;
         kf[g & 1][i] = *reinterpret_cast<const bf16x8*>(at);
       }
     };
-    f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains of products
+    f32x4 part[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains of products
     read(0);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if (g + 1 < NG) read(g + 1);
       hold_order();
 #pragma unroll
-      for (int i = 0; i < G; ++i)
-        if (g * G + i < KS)
-          s[i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[g & 1][i], qf[g * G + i], s[i & 1], 0, 0, 0);
+      for (int i = g * LG; i < kLat && i < (g + 1) * LG; ++i) load(i);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int f = g * G + i;
+        if (f < F) part[f & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[g & 1][i], qf[f / TB], part[f & 1], 0, 0, 0);
+      }
       hold_order();
     }
-    return s[0] + s[1];
+    if (TB == 1) {
+      s[0] = part[0] + part[1];
+    } else {
+      s[0] = part[0];
+      s[TB - 1] = part[1];
+    }
   }
 
   // out^T[column][row] += rows^T P^T for the wave's columns, the operands read
   // one block of NB products ahead
-  static __device__ __forceinline__ void values(const __bf16* __restrict__ half, const __bf16* __restrict__ prob,
-                                                int wave, int ln, int lg, f32x4 (&acc)[MT][NB]) {
-    const int r0 = 8 * lg + (ln >> 2);  // rows r0 and r0 + 4
+  static __device__ __forceinline__ void values(const __bf16* tile, const __bf16* prob, int wave, int ln, int lg,
+                                                f32x4 (&acc)[MT][NB]) {
+    const int r0 = 8 * lg + (ln >> 2);  // rows r0 and r0 + 4 of each 32
     const int c0 = wave * (MT * 2) + ((ln & 3) >> 1);
-    const char* rows = reinterpret_cast<const char*>(half + r0 * LP) + (ln & 1) * 8;
+    const char* rows = reinterpret_cast<const char*>(tile + r0 * LP) + (ln & 1) * 8;
+    constexpr int B = kTile / 32 * MT;
     bf16x8 pf[NB], vf[2];
-    auto read = [&](int i) {
-      const int x = ((c0 + 2 * i) ^ ((r0 & 7) << 1)) * 16;
-      vf[i & 1] = join(read_tr(rows + x), read_tr(rows + (x ^ 128) + 4 * LP * 2));
-    };
+    auto weights = [&](int k) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-      pf[j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kHalf + ((lg ^ ((ln >> 1) & 3)) << 3));
+      for (int j = 0; j < NB; ++j)
+        pf[j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kTile + (((4 * k + lg) ^ (ln & 7)) << 3));
+    };
+    auto read = [&](int b) {
+      const int k = b / MT, i = b % MT;
+      const int x = ((c0 + 2 * i) ^ ((r0 & 7) << 1)) * 16;
+      vf[b & 1] = join(read_tr(rows + x + k * 32 * LP * 2), read_tr(rows + (x ^ 128) + (k * 32 + 4) * LP * 2));
+    };
+    weights(0);
     read(0);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (i + 1 < MT) read(i + 1);
+    for (int b = 0; b < B; ++b) {
+      if (b == MT) weights(1);
+      if (b + 1 < B) read(b + 1);
       hold_order();
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[i & 1], pf[j], acc[i][j], 0, 0, 0);
+        acc[b % MT][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[b & 1], pf[j], acc[b % MT][j], 0, 0, 0);
       hold_order();
     }
   }
@@ -265,14 +279,14 @@ struct Decode {
 template <int LP, int RP, int NB>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_decode_kernel(DecodeParams p) {
   using D = Decode<LP, RP, NB>;
-  constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG;
-  __shared__ __attribute__((aligned(16))) __bf16 stage[kStages][D::kStage];
+  constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG, TB = D::TB;
+  __shared__ __attribute__((aligned(16))) __bf16 stage[2][D::kStage];
   __shared__ __attribute__((aligned(16))) __bf16 rotary[2][RP > 0 ? kTile * RP : 8];
-  __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kHalf];
-  __shared__ float smax[TG][MB];  // of a half; at a piece's end the sums
+  __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kTile];
+  __shared__ float smax[TG][MB];  // of a tile; at a piece's end the sums
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
   __shared__ int32_t pages[2][kWaves][64];  // page of token 64 t + lane of the tile located next
-  __shared__ int grown[2];        // whether a row's maximum has grown much in half h
+  __shared__ int grown[2];        // whether a row's maximum has grown much in this tile
   __shared__ int32_t lens[256];            // the sequences' tokens (few)
   __shared__ int64_t qat[2][MB];           // of a query row: its q and q_rope in a sequence's
   __shared__ int32_t less[MB];             // and how many tokens less than the last one it sees
@@ -315,8 +329,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   };
   bf16x8 qf[KS];
   auto load_q = [&](int s) {
-    const __bf16* qp = p.q + s * p.qs[0] + qat[0][rblock * 16 + ln] + 8 * lg;
-    const __bf16* qrp = p.qr + s * p.qrs[0] + qat[1][rblock * 16 + ln] + 8 * lg;
+    const int row = keep_here(rblock * 16 + ln), lg = keep_here(lane >> 4);
+    const __bf16* qp = p.q + s * p.qs[0] + qat[0][row] + 8 * lg;
+    const __bf16* qrp = p.qr + s * p.qrs[0] + qat[1][row] + 8 * lg;
     if (p.L == LP && p.R == RP) {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -333,20 +348,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
   };
 
-  // The tiles in hand: the one computed, the next two, and the one after them,
+  // The tiles in hand: the one computed, the next one, and the one after it,
   // whose pages are being looked up.  ``left`` counts the share's tiles behind
-  // that one.
+  // the one computed.
   struct Tile {
     int n, t, len;            // tile t of sequence n, which has len tokens
     unsigned long long live;  // which rows are there
   };
-  int left = uniform(share.left);
-  bool ahead = false;  // whether there is a tile behind the last one located
-  Tile cur, next, then, ask;
+  int left = uniform(share.left) - 1;
+  Tile cur, next, ask;
   const char* at;      // rows of the last tile located (lane i: token i)
   // Rows that are not there are fetched from the first one that is (their
-  // weights are 0), or, if there is none, from the cache's first (a half
-  // without rows is not computed): every half has the same number of loads.
+  // weights are 0); a tile without any is not fetched and not computed.
   auto locate = [&](int page, Tile& x) {
     int64_t row = place(page, x.t, x.len);
     x.live = __ballot(row >= 0);
@@ -365,35 +378,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const unsigned stage_at = lds_offset(stage), rotary_at = lds_offset(rotary), pages_at = lds_offset(pages[0][wave]);
   constexpr unsigned kStageBytes = D::kStage * 2, kRotaryBytes = sizeof(rotary[0]), kPagesBytes = sizeof(pages[0]);
   const typename D::Columns columns = D::columns(p, wave, lane);
-  auto fetch = [&](int h, int to) {
-#pragma unroll
-    for (int i = 0; i < D::kLat; ++i) D::fetch(i, h, at, wave, lane, columns, stage_at + to * kStageBytes);
-  };
-
-  // three halves on their way: both of the first tile, one of the second
+  auto fetch = [&](int i, int to) { D::fetch(i, at, wave, lane, columns, stage_at + to * kStageBytes); };
   cur.n = uniform(share.n);
   cur.t = uniform(share.t);
   cur.len = tokens_of(cur.n);
-  const int page0 = *lookup(cur.n, cur.t, cur.len);
-  next = cur;
-  next.live = 0;
-  int page1 = -1;
-  if (--left > 0) {
-    follow(next);
-    page1 = *lookup(next.n, next.t, next.len);
-  }
-  locate(page0, cur);
+  locate(*lookup(cur.n, cur.t, cur.len), cur);
   D::fetch_rotary(at, wave, lane, columns, rotary_at);
-  fetch(0, 0);
-  fetch(1, 1);
-  bool more = left > 0;  // whether ``next`` is a tile of the share
-  if (more) locate(page1, next);
-  fetch(0, 2);
-  then = ask = next;
-  if (more && --left > 0) {
+#pragma unroll
+  for (int i = 0; i < D::kLat; ++i) fetch(i, 0);
+  next = ask = cur;
+  if (left > 0) {
     follow(ask);
-    load_lds4(lookup(ask.n, ask.t, ask.len), pages_at + kPagesBytes);
-    ahead = true;
+    load_lds4(lookup(ask.n, ask.t, ask.len), pages_at);
   }
   if (scoring) load_q(cur.n);
   int begin = cur.t;
@@ -405,109 +401,103 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  // The loop's unit is a half (32 tokens): half u = 2 par + h is computed while
-  // halves u + 1 and u + 2 are on their way and u + 3 is sent for.
-  int par = 0;
-  auto half = [&](auto hc) {
-    constexpr int h = decltype(hc)::value;
-    const int u = 2 * par + h, to = (u + 3) & 3;
-    // Half u (and with h == 0 its tile's rotary rows) has landed when at most
-    // the loads issued after it are under way: those of the two halves that
-    // follow and, with h == 1, the next tile's rotary rows.  Pages looked up a
-    // tile ago came before those.
-    wait_loads<2 * D::kLat + (h == 1 && RP > 0 ? 1 : 0)>();
-    lds_barrier();  // and the readers of half u - 1 are done
-    if (tid == 0) grown[h ^ 1] = 0;
-    if (h == 0) {
-      D::fetch_rotary(at, wave, lane, columns, rotary_at + (par ^ 1) * kRotaryBytes);
-      fetch(1, to);
-    } else {
-      // the tile after the next one: located, and sent for
-      then = ask;
-      then.live = 0;
-      if (ahead) {
-        locate(pages[par ^ 1][wave][lane], then);
-        ahead = false;
-        if (--left > 0) {
-          follow(ask);
-          load_lds4(lookup(ask.n, ask.t, ask.len), pages_at + par * kPagesBytes);
-          ahead = true;
-        }
-      } else {
-        at = reinterpret_cast<const char*>(p.cache);
-        then.n = -1;
+  for (int par = 0;; par ^= 1) {
+    wait_loads<0>();
+    lds_barrier();  // this tile has landed, and the readers of the one before are done
+    const bool more = left > 0;
+    if (more) {
+      next = ask;
+      locate(pages[par][wave][lane], next);
+      if (--left > 0) {
+        follow(ask);
+        load_lds4(lookup(ask.n, ask.t, ask.len), pages_at + (par ^ 1) * kPagesBytes);
       }
-      fetch(0, to);
     }
-    if ((unsigned)(cur.live >> (h * 32)) == 0) return;
-
-    float sum = 0.f, fac = 1.f;
-    f32x4 s;
-    // Weights of the scores against the maximum in use, for the matrix unit in
-    // bf16, the values' own type; their sum stays in fp32.
-    auto weigh = [&]() {
-      const float base = m == -INFINITY ? 0.f : m;
-      bf16x4 pb;
-      sum = 0.f;
+    if (tid == 0) grown[par ^ 1] = 0;
+    const bool fetches = more && next.live != 0;
+    if (fetches) D::fetch_rotary(at, wave, lane, columns, rotary_at + (par ^ 1) * kRotaryBytes);
+    if (fetches && !(scoring && cur.live)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = exp2_hw(fmaf(s[i], p.scale2, -base));
-        sum += e;
-        pb[i] = (__bf16)e;
-      }
-      const int tk = 16 * tg + 4 * lg;
-      *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kHalf + (((tk >> 3) ^ ((ln >> 1) & 3)) << 3) + (tk & 7)) =
-          pb;
-    };
-    if (scoring) {
-      s = D::scores(stage[u] + (16 * tg + ln) * LP, rotary[par] + (h * kHalf + 16 * tg + ln) * RP, qf, ln, lg);
-      if (cur.t * kTile + (h + 1) * kHalf > cur.len - (p.Q - 1) || (unsigned)(cur.live >> (h * 32)) != ~0u) {
-        const int sees = cur.len - sees_less;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tk = h * kHalf + 16 * tg + 4 * lg + i;
-          if (cur.t * kTile + tk >= sees || !((cur.live >> tk) & 1)) s[i] = -INFINITY;
-        }
-      }
-      float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-      mx = max_halves(max_quarters(mx)) * p.scale2;
-      if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
-      // The maximum in use follows the true one only when that is larger by
-      // more than 8 (a factor of 256): the weights stay far inside the range,
-      // and most halves need neither an exchange of maxima between the waves
-      // nor a rescaling of the output.
-      if (__any(mx > m + 8.f)) {
-        if (lane == 0) grown[h] = 1;
-      }
-      weigh();
+      for (int i = 0; i < D::kLat; ++i) fetch(i, par ^ 1);
     }
-    lds_barrier();
-    if (grown[h]) {
+    if (cur.live) {
+      float sum = 0.f, fac = 1.f;
+      f32x4 s[TB];
+      // Weights of the scores against the maximum in use, for the matrix unit
+      // in bf16, the values' own type; their sum stays in fp32.
+      auto weigh = [&]() {
+        const float base = m == -INFINITY ? 0.f : m;
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+          bf16x4 pb;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
+            sum += e;
+            pb[i] = (__bf16)e;
+          }
+          const int tk = 16 * (TB * tg + j) + 4 * lg;
+          *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+        }
+      };
       if (scoring) {
-        const float mx = fmaxf(smax[0][rblock * 16 + ln], smax[1][rblock * 16 + ln]);
-        const float mn = mx > m + 8.f ? mx : m;
-        fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
-        m = mn;
-        if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
-      }
-      lds_barrier();  // (all have read the maxima; the weights are written again)
-      if (scoring) weigh();
+        D::scores(stage[par] + (16 * TB * tg + ln) * LP, rotary[par] + (16 * TB * tg + ln) * RP, qf, ln, lg, s,
+                  [&](int i) {
+                    if (fetches) fetch(i, par ^ 1);
+                  });
+        if (cur.t * kTile + kTile > cur.len - (p.Q - 1) || cur.live != ~0ull) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const float f = sfac[j * 16 + ln];
+          for (int j = 0; j < TB; ++j) {
+            // of the lane's four tokens: how many are seen, and which are there
+            const int at4 = 16 * (TB * tg + j) + 4 * lg, sees = cur.len - sees_less - cur.t * kTile - at4;
+            const unsigned there = (unsigned)(cur.live >> at4);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][j] *= f;
+            for (int i = 0; i < 4; ++i)
+              if (i >= sees || !(there >> i & 1)) s[j][i] = -INFINITY;
+          }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
+        mx = max_halves(max_quarters(mx)) * p.scale2;
+        if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
+        // The maximum in use follows the true one only when that is larger by
+        // more than 8 (a factor of 256): the weights stay far inside the range,
+        // and most tiles need neither an exchange of maxima between the waves
+        // nor a rescaling of the output.
+        if (__any(mx > m + 8.f)) {
+          if (lane == 0) grown[par] = 1;
+        }
+        weigh();
       }
       lds_barrier();
+      if (grown[par]) {
+        if (scoring) {
+          float mx = smax[0][rblock * 16 + ln];
+#pragma unroll
+          for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
+          const float mn = mx > m + 8.f ? mx : m;
+          fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
+          m = mn;
+          if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
+        }
+        lds_barrier();  // (all have read the maxima; the weights are written again)
+        if (scoring) weigh();
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const float f = sfac[j * 16 + ln];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[i][j] *= f;
+        }
+        lds_barrier();
+      }
+      l = l * fac + sum;
+      D::values(stage[par], prob, wave, ln, lg, acc);
     }
-    l = l * fac + sum;
-    D::values(stage[u], prob, wave, ln, lg, acc);
-  };
 
-  wait_loads<0>();
-  for (;; par ^= 1) {
-    half(std::integral_constant<int, 0>{});
-    half(std::integral_constant<int, 1>{});
     if (!more || next.n != cur.n) {
       const int n = cur.n, t = cur.t, tiles = tiles_of(cur.len);
       // ---- the end of a piece: tiles [begin, t] of sequence n
@@ -532,7 +522,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int row = row0 + j * 16;
-        const float sum = smax[0][j * 16 + ln] + smax[1][j * 16 + ln];
+        float sum = smax[0][j * 16 + ln];
+#pragma unroll
+        for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -550,13 +542,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         out += 16 * p.L;
         part += 16 * p.L;
       }
-      if (tid < MB && rb * MB + tid < p.rows) {
-        const float sum = smax[0][tid] + smax[1][tid];
-        const float lse2 = sum == 0.f ? -INFINITY : sfac[tid] + __log2f(sum);
+      const int r = keep_here(tid);
+      if (r < MB && rb * MB + r < p.rows) {
+        float sum = smax[0][r];
+#pragma unroll
+        for (int g = 1; g < TG; ++g) sum += smax[g][r];
+        const float lse2 = sum == 0.f ? -INFINITY : sfac[r] + __log2f(sum);
         if (!whole)
-          p.plse[(int64_t)slot * MB + tid] = lse2;
+          p.plse[(int64_t)slot * MB + r] = lse2;
         else if (p.lse)
-          p.lse[(int64_t)n * p.rows + rb * MB + tid] = lse2 * kLn2;
+          p.lse[(int64_t)n * p.rows + rb * MB + r] = lse2 * kLn2;
       }
       wait_loads<0>();  // the queries are there, and no load to LDS outlives the workgroup
       if (!more) return;
@@ -565,8 +560,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       begin = next.t;
     }
     cur = next;
-    next = then;
-    more = next.n >= 0;
   }
 }
 
