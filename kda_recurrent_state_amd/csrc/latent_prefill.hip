@@ -44,30 +44,55 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 31, lh = lane >> 5;
 
-  // items of one head are neighbours and run on one XCD (its L2 holds the
-  // head's keys and values), the longest first
-  const int64_t items = (int64_t)p.tiles * p.H, per = (items + 7) / 8;
-  const int64_t item = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= per || item >= items) return;
-  const int h = (int)(item / p.tiles);
-  int x = p.tiles - 1 - (int)(item % p.tiles);
+  // Work items, the longest first.  A head's items run on one XCD, whose L2
+  // then holds its keys and values: heads are dealt to the XCDs where they come
+  // out even, else the list of (head, tile) is cut into eight parts.
+  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  int h, x;
+  if ((p.H & 7) == 0) {
+    const int heads = p.H >> 3;
+    h = xcd * heads + idx % heads;
+    x = idx / heads;
+  } else {
+    const int64_t items = (int64_t)p.tiles * p.H, per = (items + 7) / 8, item = xcd * per + idx;
+    if (idx >= per || item >= items) return;
+    h = (int)(item / p.tiles);
+    x = (int)(item % p.tiles);
+  }
 
-  // query tile x of the batch: sequence n, queries 32 W t ..
+  // Query tile x: sequence n, queries 32 W t ..  Up to 64 sequences are taken
+  // in the order of their keys, most first; of a sequence the last tile, which
+  // sees most keys, comes first.
   int n = -1, t = 0;
   int64_t q0 = 0, q1 = 0;
   for (int n0 = 0; n0 < p.N; n0 += 64) {
     int64_t a = 0, b = 0;
-    if (n0 + lane < p.N) {
-      a = clamp64(p.cu_q[n0 + lane], 0, p.T);
-      b = clamp64(p.cu_q[n0 + lane + 1], a, p.T);
+    int mine = n0 + lane;
+    if (mine < p.N) {
+      a = clamp64(p.cu_q[mine], 0, p.T);
+      b = clamp64(p.cu_q[mine + 1], a, p.T);
     }
-    const int c = (int)((b - a + 32 * W - 1) / (32 * W));
+    int c = (int)((b - a + 32 * W - 1) / (32 * W));
+    if (p.N <= 64 && p.N > 1) {
+      // c of the sequence of this rank, which is put in ``mine``
+      const int keys = lane < p.N ? (int)((unsigned)p.cu_k[lane + 1] - (unsigned)p.cu_k[lane]) : 0;
+      int rank = 0;
+      for (int j = 0; j < p.N; ++j) {
+        const int other = __builtin_amdgcn_readlane(keys, j);
+        rank += other > keys || (other == keys && j < lane) ? 1 : 0;
+      }
+      rank = lane < p.N ? rank : lane;  // (a permutation of the lanes)
+      mine = __builtin_amdgcn_ds_permute(rank * 4, lane);
+      c = __shfl(c, mine, 64);
+      a = __shfl(a, mine, 64);
+      b = __shfl(b, mine, 64);
+    }
     const int incl = wave_scan(c, lane);
     const unsigned long long past = __ballot(incl > x);
     if (past) {
       const int i = __ffsll(past) - 1;
-      n = n0 + i;
-      t = x - __shfl(incl - c, i, 64);
+      n = __shfl(mine, i, 64);
+      t = __shfl(incl, i, 64) - 1 - x;
       q0 = __shfl(a, i, 64);
       q1 = __shfl(b, i, 64);
       break;
@@ -104,6 +129,9 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
   const int qlast = qfirst + 32 * W < lq ? qfirst + 32 * W : lq;
   int end = p.causal ? lk - (lq - qlast) : lk;
   end = end < 0 ? 0 : end;
+  // that the wave's last query sees (none: a wave without queries)
+  const int wlast = qfirst + wave * 32 + 32 < lq ? qfirst + wave * 32 + 32 : lq;
+  const int wend = qfirst + wave * 32 >= lq ? 0 : (p.causal ? lk - (lq - wlast) : lk);
   const int all_see = p.causal ? lk - (lq - 1 - (qfirst + wave * 32)) : lk;  // the wave's first query
 
   f32x16 acc[MT];
@@ -178,6 +206,7 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
     wait_loads<0>();
     lds_barrier();  // tile j is there, and the readers of tile j - 1 are done
     if (j + 1 < ntiles) stage(j + 1);
+    if (j * kTile >= wend) continue;
     const char* buf = lds + (j & 1) * kStage;
 
     // ---- scores, operands read a group ahead
