@@ -34,7 +34,10 @@ struct Stores {
   int n;
 };
 
-__device__ __forceinline__ int64_t used_pages(int64_t len, int64_t page) { return len <= 0 ? 0 : (len + page - 1) / page; }
+// (lengths are below 2^31 and page sizes at most 2^30: 32-bit arithmetic)
+__device__ __forceinline__ int64_t used_pages(int64_t len, int64_t page) {
+  return len <= 0 ? 0 : (int64_t)(((uint32_t)len + (uint32_t)page - 1) / (uint32_t)page);
+}
 
 // inclusive prefix sum over the workgroup; tmp holds one value a wave
 __device__ __forceinline__ int block_scan(int x, int* tmp, int* total) {
@@ -54,6 +57,10 @@ __device__ __forceinline__ int block_scan(int x, int* tmp, int* total) {
   }
   *total = all;
   return x + before;
+}
+
+__device__ __forceinline__ int pages_needed(int share, int64_t len, int64_t page, int64_t used) {
+  return share ? ((uint32_t)len % (uint32_t)page != 0 ? 1 : 0) : (int)used;
 }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -98,6 +105,7 @@ struct ForkPlan {
   int32_t* free;   // the free pages taken, in order
 };
 
+// Many entries: a workgroup each.
 template <typename IdxT>
 __global__ __launch_bounds__(kThreads) void fork_check_kernel(Pool p, const IdxT* src, const IdxT* dst, int share,
                                                               ForkPlan w) {
@@ -121,13 +129,76 @@ __global__ __launch_bounds__(kThreads) void fork_check_kernel(Pool p, const IdxT
     ok = __syncthreads_or(bad) == 0;
   }
   if (threadIdx.x == 0) {
-    w.need[i] = !ok ? -1 : (share ? (len % p.page_size != 0 ? 1 : 0) : (int32_t)used);
+    w.need[i] = !ok ? -1 : pages_needed(share, len, p.page_size, used);
     w.used[i] = (int32_t)used;
   }
 }
 
-__global__ __launch_bounds__(kPlanThreads) void fork_plan_kernel(Pool p, int64_t M, int32_t* status, ForkPlan w) {
+constexpr int kFew = 128;                         // entries the plan checks itself
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kEach = kFew / kPlanWaves;          // of which a wave takes up to so many
+
+// The same checks for up to kFew entries by the planning workgroup (a launch
+// less): thread i fetches entry i, then a wave checks the pages of kEach
+// entries at once, so that their loads overlap.
+template <typename IdxT>
+__device__ void fork_check_few(const Pool& p, const IdxT* src, const IdxT* dst, int M, int share, const ForkPlan& w,
+                               int64_t (*entry)[kFew]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t *es = entry[0], *ed = entry[1], *eu = entry[2];  // slots, and pages of the parent (0 where the entry is bad)
+  int need = -1;
+  if (tid < M) {
+    const int64_t s = (int64_t)src[tid], d = (int64_t)dst[tid];
+    int64_t used = 0;
+    if (s >= 0 && s < p.num_seqs && d >= 0 && d < p.num_seqs && s != d) {
+      const int64_t len = p.lengths[s], pages = used_pages(len, p.page_size);
+      if (len >= 0 && p.lengths[d] == 0 && pages <= p.max_pages) {
+        used = pages;
+        need = pages_needed(share, len, p.page_size, used);
+      }
+    }
+    es[tid] = s;
+    ed[tid] = d;
+    eu[tid] = used;
+    w.need[tid] = need;
+    w.used[tid] = (int32_t)used;
+  }
+  __syncthreads();
+  int32_t page[kEach];
+  bool bad[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = wave + k * kPlanWaves;
+    page[k] = -1;
+    bad[k] = false;
+    if (i < M && lane < eu[i]) page[k] = (p.table + es[i] * p.table_stride)[lane];
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = wave + k * kPlanWaves;
+    if (i < M && lane < eu[i])
+      bad[k] = page[k] < 0 || page[k] >= p.num_pages || p.refs[page[k]] <= 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = wave + k * kPlanWaves;
+    if (i >= M) continue;
+    for (int64_t j = lane + 64; j < eu[i]; j += 64) {
+      const int64_t pg = (p.table + es[i] * p.table_stride)[j];
+      bad[k] |= pg < 0 || pg >= p.num_pages || p.refs[pg] <= 0;
+    }
+    for (int j = lane; j < i; j += 64) bad[k] |= ed[j] == ed[i];  // the slot is another entry's
+    if (__ballot(bad[k]) != 0 && lane == 0) w.need[i] = -1;
+  }
+  __syncthreads();  // (the entries are read back by other threads)
+}
+
+template <typename IdxT>
+__global__ __launch_bounds__(kPlanThreads) void fork_plan_kernel(Pool p, const IdxT* src, const IdxT* dst, int64_t M,
+                                                                 int share, int32_t* status, ForkPlan w) {
   __shared__ int tmp[kPlanThreads / 64];
+  __shared__ int64_t entry[3][kFew];
+  if (M <= kFew) fork_check_few(p, src, dst, (int)M, share, w, entry);
   // pages the entries ask for, in order (64-bit totals: M max_pages may pass 32 bits)
   int64_t asked = 0;
   for (int64_t i0 = 0; i0 < M; i0 += kPlanThreads) {
@@ -228,34 +299,81 @@ struct CompactPlan {
   int32_t* count;  // [2] moves, live pages
 };
 
+// One workgroup.  A wave looks at 64 pages with one load and one ballot and
+// holds the ballots of up to kChunks of them, chunk c's in lane c; up to
+// kPlanThreads kChunks pages (32768) are loaded once, more of them in as many
+// steps as it takes, three times over.  (8192 pages: 10 us; one page a thread
+// and step took 14 us.)
+constexpr int kChunks = 32;
+
 __global__ __launch_bounds__(kPlanThreads) void compact_plan_kernel(Pool p, CompactPlan w, int32_t* live_out) {
   __shared__ int tmp[kPlanThreads / 64];
-  int live = 0;
-  for (int64_t i = threadIdx.x; i < p.num_pages; i += kPlanThreads) live += p.refs[i] > 0;
-  int all = 0;
-  block_scan(live, tmp, &all);
-  live = all;
-  int gaps = 0, moves = 0;  // free pages before the live count, live ones behind it: as many
-  for (int64_t i0 = 0; i0 < p.num_pages; i0 += kPlanThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool in = i < p.num_pages, taken = in && p.refs[i] > 0;
-    const int gap = in && i < live && !taken, move = i >= live && taken;
-    if (i0 < live) {
-      const int at = gaps + block_scan(gap, tmp, &all) - 1;
-      if (gap) w.to[at] = (int32_t)i;
-      gaps += all;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // chunks a wave looks at in a step: few pages are spread over all waves
+  const int64_t need = (p.num_pages + kPlanThreads - 1) / kPlanThreads;
+  const int chunks = need < kChunks ? (int)need : kChunks;
+  const int64_t step = (int64_t)kPlanThreads * chunks;
+  const bool once = p.num_pages <= step;
+  unsigned long long taken = 0;  // lane c: pages in use of the wave's chunk c in this step
+  auto look = [&](int64_t i0) {
+    const int64_t first = i0 + (int64_t)wave * chunks * 64 + lane;
+    taken = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 8) {
+      int32_t ref[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int64_t i = first + (c0 + c) * 64;
+        ref[c] = c0 + c < chunks && i < p.num_pages ? p.refs[i] : 0;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const unsigned long long m = __ballot(ref[c] > 0);
+        if (lane == c0 + c) taken = m;
+      }
     }
-    if (i0 + kPlanThreads > live) {
-      const int at = moves + block_scan(move, tmp, &all) - 1;
-      if (move) w.from[at] = (int32_t)i;
-      if (in && i >= live) w.rank[i] = move ? at : -1;
-      moves += all;
+  };
+  int all = 0;
+  int64_t live = 0, kept = 0;  // pages in use; those of them that stay
+  for (int64_t i0 = 0; i0 < p.num_pages; i0 += step) {
+    look(i0);
+    block_scan(__popcll(taken), tmp, &all);
+    live += all;
+  }
+  for (int64_t i0 = 0; i0 < live; i0 += step) {
+    if (!once) look(i0);
+    const int64_t below = live - (i0 + ((int64_t)wave * chunks + lane) * 64);  // of the lane's pages
+    const unsigned long long in = below >= 64 ? ~0ull : (below > 0 ? (1ull << below) - 1 : 0);
+    block_scan(__popcll(taken & in), tmp, &all);
+    kept += all;
+  }
+  const int moves = (int)(live - kept);
+  int before = 0;  // pages in use before this step
+  for (int64_t i0 = 0; i0 < p.num_pages; i0 += step) {
+    if (!once) look(i0);
+    const int n = __popcll(taken);
+    const int first = before + block_scan(n, tmp, &all) - n;  // and before the lane's pages
+    before += all;
+    for (int c = 0; c < chunks; ++c) {
+      const int64_t i = i0 + ((int64_t)wave * chunks + c) * 64 + lane;
+      if (i - lane >= p.num_pages) break;
+      const unsigned lo = __builtin_amdgcn_readlane((unsigned)taken, c);
+      const unsigned hi = __builtin_amdgcn_readlane((unsigned)(taken >> 32), c);
+      // pages in use before page i
+      const int rank = __builtin_amdgcn_readlane(first, c) + __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
+      if (i >= p.num_pages) continue;
+      const bool used = ((lane < 32 ? lo >> lane : hi >> (lane - 32)) & 1) != 0;
+      if (i < live) {
+        if (!used) w.to[i - rank] = (int32_t)i;
+      } else {
+        if (used) w.from[rank - kept] = (int32_t)i;
+        w.rank[i] = used ? rank - (int)kept : -1;
+      }
     }
   }
   if (threadIdx.x == 0) {
     w.count[0] = moves;
-    w.count[1] = live;
-    if (live_out) *live_out = live;
+    w.count[1] = (int32_t)live;
+    if (live_out) *live_out = (int32_t)live;
   }
 }
 
@@ -350,11 +468,14 @@ hipError_t fork_typed(const kda_page_pool_t& a, const kda_page_store_t* stores, 
                       hipStream_t stream) {
   const Pool p = pool_of(a);
   const IdxT *s = static_cast<const IdxT*>(src), *d = static_cast<const IdxT*>(dst);
-  hipLaunchKernelGGL((fork_check_kernel<IdxT>), dim3((unsigned)M), dim3(kThreads), 0, stream, p, s, d, share ? 1 : 0,
-                     w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, M, status, w);
+  hipError_t e = hipSuccess;
+  if (M > kFew) {
+    hipLaunchKernelGGL((fork_check_kernel<IdxT>), dim3((unsigned)M), dim3(kThreads), 0, stream, p, s, d, share ? 1 : 0,
+                       w);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((fork_plan_kernel<IdxT>), dim3(1), dim3(kPlanThreads), 0, stream, p, s, d, M, share ? 1 : 0,
+                     status, w);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int width = width_of(stores, num_stores);
   int64_t at = 0, tables = M;

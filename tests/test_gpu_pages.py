@@ -173,7 +173,8 @@ def test_fork_and_compact_many_layers(many):
 
 @pytest.mark.parametrize("seqs,per,pages,page,live", [(1, 1, 1, 1, 1), (1, 1, 1, 1, 0), (8, 4, 40, 16, 4),
                                                       (33, 7, 300, 5, 20), (300, 12, 5000, 8, 150), (9, 5, 1500, 3, 9),
-                                                      (64, 8, 70, 4, 64)])
+                                                      (64, 8, 70, 4, 64), (150, 300, 33000, 2, 110),
+                                                      (150, 300, 70000, 2, 150)])
 def test_compact(seqs, per, pages, page, live):
     import kda_recurrent_state_amd as kda
     pool = _pool(7, seqs, per, pages, page, live)
