@@ -392,6 +392,9 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  *  causal          -- nonzero: query i of a sequence with Lq queries and Lk
  *                     keys sees keys j < Lk - (Lq - 1 - i), so its queries are
  *                     the last Lq of Lk positions; zero: it sees all Lk keys.
+ *  workspace       -- device scratch, 16-byte aligned, of at least
+ *                     kda_latent_prefill_workspace_size(T, S, N, H, E) bytes
+ *                     (may be NULL when that size is 0).
  * For query i and head h of a sequence, over the keys j it sees:
  *   s_j = scale (q_i[:D] . k_j + q_i[D:] . k_rope_j)
  *   out_i = sum_j exp(s_j - lse_i) v_j,   lse_i = log sum_j exp(s_j)
@@ -421,14 +424,21 @@ typedef struct {
   float* lse;
   float scale;
   int causal;
+  void* workspace;
+  size_t workspace_bytes;
 } kda_latent_prefill_args_t;
+
+/* Bytes of device workspace kda_latent_prefill needs for these sizes: 0 unless
+ * there are few queries and many keys, which are then split. */
+size_t kda_latent_prefill_workspace_size(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E);
 
 /*
  * kda_latent_prefill -- see kda_latent_prefill_args_t.  Aliasing (checked on
- * the host, KDA_E_ALIAS): out and lse overlap neither each other nor any
- * input.  T == 0 or N == 0 enqueues nothing.
+ * the host, KDA_E_ALIAS): out, lse and the workspace overlap neither each
+ * other nor any input.  Calls that can run at the same time need workspaces of
+ * their own.  T == 0 or N == 0 enqueues nothing.
  * Errors: KDA_E_NULL, KDA_E_DTYPE, KDA_E_SHAPE, KDA_E_LAYOUT (alignment or
- * strides), KDA_E_UNSUPPORTED, KDA_E_ALIAS, KDA_E_HIP.
+ * strides), KDA_E_UNSUPPORTED, KDA_E_WORKSPACE, KDA_E_ALIAS, KDA_E_HIP.
  */
 kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* args, void* stream);
 

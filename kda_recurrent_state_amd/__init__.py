@@ -24,12 +24,12 @@ from .api import (KDAStateCopy, cache_descriptor, checkpoint_offsets, int8_store
                   kda_ckpt_dequantize_gather,
                   kda_ckpt_quantize_scatter, kda_recurrent_decode, kda_state_gather, kda_state_scatter)
 from .latent import (kda_latent_decode, kda_latent_decode_workspace_size, kda_latent_prefill,  # noqa: F401
-                     kda_page_compact, kda_page_fork, kda_page_free)
+                     kda_latent_prefill_workspace_size, kda_page_compact, kda_page_fork, kda_page_free)
 
 __all__ = ["kda_state_gather", "kda_state_scatter", "kda_chunk_prefill", "kda_chunk_prefill_workspace_size",
            "kda_chunk_prefill_noalloc",
            "kda_recurrent_decode", "kda_ckpt_quantize_scatter", "kda_ckpt_dequantize_gather",
            "int8_store_descriptor",
-           "kda_latent_prefill", "kda_latent_decode", "kda_latent_decode_workspace_size",
-           "kda_page_fork", "kda_page_compact", "kda_page_free",
+           "kda_latent_prefill", "kda_latent_prefill_workspace_size", "kda_latent_decode",
+           "kda_latent_decode_workspace_size", "kda_page_fork", "kda_page_compact", "kda_page_free",
            "KDAStateCopy", "KDAError", "load_library", "cache_descriptor", "checkpoint_offsets"]

@@ -16,7 +16,8 @@ STATUS_NAMES = {0: "KDA_OK", 1: "KDA_E_NULL", 2: "KDA_E_DTYPE", 3: "KDA_E_SHAPE"
 EXPORTED = ("kda_state_gather", "kda_state_scatter", "kda_chunk_prefill", "kda_chunk_prefill_workspace_size",
             "kda_chunk_prefill_noalloc",
             "kda_recurrent_decode", "kda_ckpt_quantize_scatter", "kda_ckpt_dequantize_gather",
-            "kda_latent_prefill", "kda_latent_decode", "kda_latent_decode_workspace_size",
+            "kda_latent_prefill", "kda_latent_prefill_workspace_size", "kda_latent_decode",
+            "kda_latent_decode_workspace_size",
             "kda_page_fork", "kda_page_fork_workspace_size", "kda_page_compact", "kda_page_compact_workspace_size",
             "kda_page_free",
             "kda_status_string", "kda_last_error_detail")
@@ -66,7 +67,8 @@ class LatentPrefillArgs(ctypes.Structure):
                 ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64 * 2),
                 ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
-                ("scale", ctypes.c_float), ("causal", ctypes.c_int)]
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class LatentDecodeArgs(ctypes.Structure):
@@ -135,6 +137,8 @@ def load_library(path: str = LIB_PATH):
     lib.kda_latent_prefill.restype = ctypes.c_int
     lib.kda_latent_decode.argtypes = [ctypes.POINTER(LatentDecodeArgs), vp]
     lib.kda_latent_decode.restype = ctypes.c_int
+    lib.kda_latent_prefill_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    lib.kda_latent_prefill_workspace_size.restype = ctypes.c_size_t
     lib.kda_latent_decode_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.kda_latent_decode_workspace_size.restype = ctypes.c_size_t
     pool, stores = ctypes.POINTER(PagePool), ctypes.POINTER(PageStore)

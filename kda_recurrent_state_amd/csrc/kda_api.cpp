@@ -329,7 +329,7 @@ kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
   if (a->dtype != KDA_BF16) return KDA_E_DTYPE;
   if (!dim8(a->D, 8, 128) || !dim8(a->R, 0, 64) || !dim8(a->E, 8, 128)) return KDA_E_UNSUPPORTED;
   if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
-  if (a->T > 0x7fffffff || a->S > 0x7fffffff || a->H > 65536) return KDA_E_UNSUPPORTED;
+  if (a->T > 0x7fffffff || a->S > 0x7fffffff || a->N > 0x7fffffff || a->H > 65535) return KDA_E_UNSUPPORTED;
   // one workgroup for each 32 queries of a head at least: the grid stays in 31 bits
   if ((a->T / 32 + a->N + 1) > (int64_t)0x7fffff00 / a->H) return KDA_E_UNSUPPORTED;
   if (a->T == 0 || a->N == 0) return KDA_OK;
@@ -348,15 +348,20 @@ kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
   if (a->S > 1 && (a->k_stride[0] > far || a->v_stride[0] > far || (a->R > 0 && a->k_rope_stride > far)))
     return KDA_E_UNSUPPORTED;
   if (a->S == 0) kn = vn = rn = 0;
+  const size_t need = kda::latent_prefill_workspace_bytes(a->T, a->S, a->N, a->H, a->E);
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return KDA_E_WORKSPACE;
+  if (need > 0 && !aligned(a->workspace, 16)) return KDA_E_LAYOUT;
   const Span ins[6] = {{a->q, qn * 2},
                        {a->k, kn * 2},
                        {a->R > 0 ? a->k_rope : nullptr, rn * 2},
                        {a->v, vn * 2},
                        {a->cu_seqlens_q, (a->N + 1) * 4},
                        {a->cu_seqlens_k, (a->N + 1) * 4}};
-  const Span outs[2] = {{a->out, a->T * a->H * a->E * 2}, {a->lse, a->T * a->H * 4}};
-  const int same[2] = {-1, -1};
-  return alias_error(outs, same, 2, ins, 6) ? KDA_E_ALIAS : KDA_OK;
+  const Span outs[3] = {{a->out, a->T * a->H * a->E * 2},
+                        {a->lse, a->T * a->H * 4},
+                        {need > 0 ? a->workspace : nullptr, (int64_t)need}};
+  const int same[3] = {-1, -1, -1};
+  return alias_error(outs, same, 3, ins, 6) ? KDA_E_ALIAS : KDA_OK;
 }
 
 kda_status_t check_latent_decode(const kda_latent_decode_args_t* a) {
@@ -443,6 +448,13 @@ bool stores_alias(const kda_page_store_t* s, int64_t n, int64_t num_pages, const
 }  // namespace
 
 extern "C" {
+
+size_t kda_latent_prefill_workspace_size(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E) {
+  if (T <= 0 || S < 0 || N <= 0 || H <= 0 || E <= 0 || T > 0x7fffffff || S > 0x7fffffff || N > 0x7fffffff ||
+      H > 65536 || E > 128)
+    return 0;
+  return kda::latent_prefill_workspace_bytes(T, S, N, H, E);
+}
 
 kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* a, void* stream) {
   const kda_status_t st = check_latent_prefill(a);

@@ -115,6 +115,15 @@ __device__ __forceinline__ float sum_quarters(float x) {
   return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
 }
 
+// The value of the first active lane, the same in all and known to be.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The value of lane ``src`` (uniform).
+__device__ __forceinline__ int64_t lane64(int64_t x, int src) {
+  const int lo = __builtin_amdgcn_readlane((int)x, src), hi = __builtin_amdgcn_readlane((int)(x >> 32), src);
+  return ((int64_t)hi << 32) | (unsigned)lo;
+}
+
 // inclusive prefix sum over the wave's lanes
 __device__ __forceinline__ int wave_scan(int x, int lane) {
 #pragma unroll

@@ -61,12 +61,6 @@ __device__ __forceinline__ int seq_tokens(const DecodeParams& p, int n) {
 }
 __device__ __forceinline__ int tiles_of(int tokens) { return (int)(((int64_t)tokens + kTile - 1) / kTile); }
 
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t lane64(int64_t x, int src) {  // src is uniform
-  const int lo = __builtin_amdgcn_readlane((int)x, src), hi = __builtin_amdgcn_readlane((int)(x >> 32), src);
-  return ((int64_t)hi << 32) | (unsigned)lo;
-}
-
 // Share w of the line: its tiles and where they begin.
 struct Share {
   int left;  // tiles, 0: no such share

@@ -15,7 +15,13 @@ namespace {
 
 using namespace latent;
 
-constexpr int kTile = 64;  // keys a tile
+constexpr int kTile = 64;       // keys a tile
+constexpr int kWaves = 4;       // 32 queries each
+constexpr int kQueries = 32 * kWaves;
+// Key tiles a piece has at least where a workgroup's keys are split: 16 take
+// about 20 us, twice what joining the pieces costs.
+constexpr int kPiece = 16;
+constexpr int kMostSplits = 32;
 
 struct PrefillParams {
   const __bf16 *q, *k, *kr, *v;
@@ -26,43 +32,25 @@ struct PrefillParams {
   int64_t T, S;
   int N, H, D, R, E, causal;
   int tiles;       // upper bound of the query tiles of a head
+  int splits;      // pieces the keys of a query tile are cut into at most
   float scale2;    // scale log2 e
+  float* part;     // [splits][T][H][E] normalised outputs of pieces
+  float* plse;     // [splits][T][H] log2 of their sums
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
-// DP, RP, EP: D, R and E rounded up to what the kernel is built for; W: waves
-// (32 queries each)
-template <int DP, int RP, int EP, int W>
-__global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams p) {
-  constexpr int KC = DP / 8, RC = RP / 8, VC = EP / 8;  // 16-byte chunks of a staged row
-  constexpr int KS = (DP + RP) / 16;
-  constexpr int MT = EP / 32;
-  constexpr int kKeyBytes = kTile * DP * 2, kRotBytes = kTile * RP * 2, kStage = kKeyBytes + kRotBytes + kTile * EP * 2;
-  __shared__ __attribute__((aligned(16))) char lds[2 * kStage];
+// A query tile: queries qfirst .. of a sequence with lq queries from q0 and lk
+// keys from k0, and the keys that the tile's last query sees.
+struct QueryTile {
+  int64_t q0, k0;
+  int qfirst, lq, lk, end;
+};
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ln = lane & 31, lh = lane >> 5;
-
-  // Work items, the longest first.  A head's items run on one XCD, whose L2
-  // then holds its keys and values: heads are dealt to the XCDs where they come
-  // out even, else the list of (head, tile) is cut into eight parts.
-  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  int h, x;
-  if ((p.H & 7) == 0) {
-    const int heads = p.H >> 3;
-    h = xcd * heads + idx % heads;
-    x = idx / heads;
-  } else {
-    const int64_t items = (int64_t)p.tiles * p.H, per = (items + 7) / 8, item = xcd * per + idx;
-    if (idx >= per || item >= items) return;
-    h = (int)(item / p.tiles);
-    x = (int)(item % p.tiles);
-  }
-
-  // Query tile x: sequence n, queries 32 W t ..  Up to 64 sequences are taken
-  // in the order of their keys, most first; of a sequence the last tile, which
-  // sees most keys, comes first.
+// Query tile x of the batch; false if there are fewer.  Up to 64 sequences are
+// taken in the order of their keys, most first; of a sequence the last tile,
+// which sees most keys, comes first.
+__device__ __forceinline__ bool find_tile(const PrefillParams& p, int x, int lane, QueryTile* out) {
   int n = -1, t = 0;
   int64_t q0 = 0, q1 = 0;
   for (int n0 = 0; n0 < p.N; n0 += 64) {
@@ -72,7 +60,7 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
       a = clamp64(p.cu_q[mine], 0, p.T);
       b = clamp64(p.cu_q[mine + 1], a, p.T);
     }
-    int c = (int)((b - a + 32 * W - 1) / (32 * W));
+    int c = (int)((b - a + kQueries - 1) / kQueries);
     if (p.N <= 64 && p.N > 1) {
       // c of the sequence of this rank, which is put in ``mine``
       const int keys = lane < p.N ? (int)((unsigned)p.cu_k[lane + 1] - (unsigned)p.cu_k[lane]) : 0;
@@ -91,22 +79,71 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
     const unsigned long long past = __ballot(incl > x);
     if (past) {
       const int i = __ffsll(past) - 1;
-      n = __shfl(mine, i, 64);
-      t = __shfl(incl, i, 64) - 1 - x;
-      q0 = __shfl(a, i, 64);
-      q1 = __shfl(b, i, 64);
+      n = __builtin_amdgcn_readlane(mine, i);
+      t = __builtin_amdgcn_readlane(incl, i) - 1 - x;
+      q0 = lane64(a, i);
+      q1 = lane64(b, i);
       break;
     }
-    x -= __shfl(incl, 63, 64);
+    x -= __builtin_amdgcn_readlane(incl, 63);
   }
-  if (n < 0) return;
-  n = __builtin_amdgcn_readfirstlane(n);
-  t = __builtin_amdgcn_readfirstlane(t);
-  const int lq = __builtin_amdgcn_readfirstlane((int)(q1 - q0));
-  const int64_t k0 = clamp64(p.cu_k[n], 0, p.S);
-  const int lk = __builtin_amdgcn_readfirstlane((int)(clamp64(p.cu_k[n + 1], k0, p.S) - k0));
+  if (n < 0) return false;
+  out->q0 = q0;
+  out->qfirst = t * kQueries;
+  const int lq = (int)(q1 - q0);
+  out->k0 = lane64(clamp64(p.cu_k[n], 0, p.S), 0);
+  const int lk = uniform((int)(clamp64(p.cu_k[n + 1], out->k0, p.S) - out->k0));
+  const int last = out->qfirst + kQueries < lq ? out->qfirst + kQueries : lq;
+  const int end = p.causal ? lk - (lq - last) : lk;
+  out->lq = lq;
+  out->lk = lk;
+  out->end = end < 0 ? 0 : end;
+  return true;
+}
 
-  const int qfirst = t * 32 * W;
+// Key tiles of a piece of a query tile that sees ``ntiles`` of them.
+__device__ __forceinline__ int piece_tiles(const PrefillParams& p, int ntiles) {
+  const int per = (ntiles + p.splits - 1) / p.splits;
+  return per < kPiece ? kPiece : per;
+}
+
+// DP, RP, EP: D, R and E rounded up to what the kernel is built for
+template <int DP, int RP, int EP>
+__global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(PrefillParams p) {
+  constexpr int W = kWaves;
+  constexpr int KC = DP / 8, RC = RP / 8, VC = EP / 8;  // 16-byte chunks of a staged row
+  constexpr int KS = (DP + RP) / 16;
+  constexpr int MT = EP / 32;
+  constexpr int kKeyBytes = kTile * DP * 2, kRotBytes = kTile * RP * 2, kStage = kKeyBytes + kRotBytes + kTile * EP * 2;
+  __shared__ __attribute__((aligned(16))) char lds[2 * kStage];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ln = lane & 31, lh = lane >> 5;
+
+  // Work items, the longest first.  A head's items run on one XCD, whose L2
+  // then holds its keys and values: heads are dealt to the XCDs where they come
+  // out even, else the list of (head, tile) is cut into eight parts.
+  const int xcd = blockIdx.x & 7, idx = (blockIdx.x >> 3) / p.splits, piece = (blockIdx.x >> 3) % p.splits;
+  int h, x;
+  if ((p.H & 7) == 0) {
+    const int heads = p.H >> 3;
+    h = xcd * heads + idx % heads;
+    x = idx / heads;
+  } else {
+    const int64_t items = (int64_t)p.tiles * p.H, per = (items + 7) / 8, item = xcd * per + idx;
+    if (idx >= per || item >= items) return;
+    h = (int)(item / p.tiles);
+    x = (int)(item % p.tiles);
+  }
+  QueryTile tile;
+  if (!find_tile(p, x, lane, &tile)) return;
+  const int64_t q0 = tile.q0, k0 = tile.k0;
+  const int lq = tile.lq, lk = tile.lk, qfirst = tile.qfirst;
+  // key tiles [first, last) of this piece
+  const int ntiles = (tile.end + kTile - 1) / kTile, per_piece = piece_tiles(p, ntiles);
+  const int first = piece * per_piece, last = first + per_piece < ntiles ? first + per_piece : ntiles;
+  if (piece > 0 && first >= ntiles) return;
+
   const int qi = qfirst + wave * 32 + ln;  // this lane's query
   const int64_t qrow = q0 + (qi < lq ? qi : lq - 1);
   bf16x8 qf[KS];
@@ -124,12 +161,9 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
       qf[s] = v;
     }
   }
-  // keys that this lane's query sees, and that the workgroup's last one sees
+  // keys that this lane's query sees, and that the wave's last one sees (none:
+  // a wave without queries)
   const int sees = p.causal ? lk - (lq - 1 - qi) : lk;
-  const int qlast = qfirst + 32 * W < lq ? qfirst + 32 * W : lq;
-  int end = p.causal ? lk - (lq - qlast) : lk;
-  end = end < 0 ? 0 : end;
-  // that the wave's last query sees (none: a wave without queries)
   const int wlast = qfirst + wave * 32 + 32 < lq ? qfirst + wave * 32 + 32 : lq;
   const int wend = qfirst + wave * 32 >= lq ? 0 : (p.causal ? lk - (lq - wlast) : lk);
   const int all_see = p.causal ? lk - (lq - 1 - (qfirst + wave * 32)) : lk;  // the wave's first query
@@ -200,12 +234,11 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
   const int vrow = 4 * lh + ((lane & 15) >> 2), vcol = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const int vat = kKeyBytes + kRotBytes + vrow * EP * 2 + (lane & 1) * 8;
 
-  const int ntiles = (end + kTile - 1) / kTile;
-  if (ntiles > 0) stage(0);
-  for (int j = 0; j < ntiles; ++j) {
+  if (first < last) stage(first);
+  for (int j = first; j < last; ++j) {
     wait_loads<0>();
     lds_barrier();  // tile j is there, and the readers of tile j - 1 are done
-    if (j + 1 < ntiles) stage(j + 1);
+    if (j + 1 < last) stage(j + 1);
     if (j * kTile >= wend) continue;
     const char* buf = lds + (j & 1) * kStage;
 
@@ -306,8 +339,11 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
 
   l = sum_halves(l);
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  if (qi < lq) {
-    __bf16* op = p.out + ((q0 + qi) * p.H + h) * p.E;
+  if (qi >= lq) return;
+  const int64_t row = (q0 + qi) * p.H + h;
+  const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
+  if (per_piece >= ntiles) {  // all of the keys
+    __bf16* op = p.out + row * p.E;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -318,26 +354,89 @@ __global__ __launch_bounds__(W * 64, 2) void latent_prefill_kernel(PrefillParams
                           (__bf16)(acc[i][4 * g + 2] * inv), (__bf16)(acc[i][4 * g + 3] * inv)};
         *reinterpret_cast<bf16x4*>(op + col) = o;
       }
-    if (p.lse && lh == 0) p.lse[(q0 + qi) * p.H + h] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    if (p.lse && lh == 0) p.lse[row] = lse2 * kLn2;
+  } else {
+    const int64_t slot = piece * p.T * p.H + row;
+    float* op = p.part + slot * p.E;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int col = 32 * i + 8 * g + 4 * lh;
+        if (col >= p.E) continue;
+        *reinterpret_cast<f32x4*>(op + col) = f32x4{acc[i][4 * g] * inv, acc[i][4 * g + 1] * inv,
+                                                    acc[i][4 * g + 2] * inv, acc[i][4 * g + 3] * inv};
+      }
+    if (lh == 0) p.plse[slot] = lse2;
   }
 }
 
+// Joins the pieces of a query tile: half a wave a row, 4 columns a lane.
+// Grid: (query tiles, heads).
+__global__ __launch_bounds__(256) void latent_pieces_kernel(PrefillParams p) {
+  const int lane = threadIdx.x & 63, half = threadIdx.x >> 5, c = (threadIdx.x & 31) * 4, h = blockIdx.y;
+  QueryTile tile;
+  if (!find_tile(p, blockIdx.x, lane, &tile)) return;
+  const int ntiles = (tile.end + kTile - 1) / kTile, per = piece_tiles(p, ntiles);
+  if (per >= ntiles) return;
+  const int pieces = (ntiles + per - 1) / per;
+  const int64_t step = p.T * p.H;
+  for (int i = half; i < kQueries && tile.qfirst + i < tile.lq; i += 8) {
+    const int64_t row = (tile.q0 + tile.qfirst + i) * p.H + h;
+    float top = -INFINITY, sum = 0.f;
+    for (int s = 0; s < pieces; ++s) top = fmaxf(top, p.plse[s * step + row]);
+    const float base = top == -INFINITY ? 0.f : top;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < pieces; ++s) {
+      const float f = exp2_hw(p.plse[s * step + row] - base);
+      sum += f;
+      if (c < p.E) o += f * *reinterpret_cast<const f32x4*>(p.part + (s * step + row) * p.E + c);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    if (c < p.E) {
+      const bf16x4 ob = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
+      *reinterpret_cast<bf16x4*>(p.out + row * p.E + c) = ob;
+    }
+    if (p.lse && c == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+  }
+}
+
+// Query tiles of a head at most, and the pieces their keys are cut into.  With
+// 512 workgroups (two a CU) or more, every workgroup takes all keys of its
+// tile; with fewer, the keys are split so that there are about as many.
+void prefill_shape(int64_t T, int64_t S, int64_t N, int64_t H, int64_t* tiles, int64_t* splits) {
+  *tiles = (T + (kQueries - 1) * N) / kQueries;
+  const int64_t items = *tiles * H, room = items > 0 ? 512 / items : 1;
+  const int64_t longest = ((S + kTile - 1) / kTile + kPiece - 1) / kPiece;  // pieces of the longest sequence
+  int64_t s = room < longest ? room : longest;
+  s = s < kMostSplits ? s : kMostSplits;
+  *splits = s < 1 ? 1 : s;
+}
+
 template <int DP, int RP, int EP>
-hipError_t launch(PrefillParams& p, hipStream_t stream) {
-  constexpr int W = 4;
-  p.tiles = (int)((p.T + 32 * W - 1) / (32 * W) + p.N);
-  const int64_t items = (int64_t)p.tiles * p.H;
-  hipLaunchKernelGGL((latent_prefill_kernel<DP, RP, EP, W>), dim3((unsigned)((items + 7) / 8 * 8)), dim3(W * 64), 0,
-                     stream, p);
+hipError_t launch(const PrefillParams& p, hipStream_t stream) {
+  const int64_t blocks = ((int64_t)p.tiles * p.H + 7) / 8 * 8 * p.splits;
+  hipLaunchKernelGGL((latent_prefill_kernel<DP, RP, EP>), dim3((unsigned)blocks), dim3(kQueries * 2), 0, stream, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(latent_pieces_kernel, dim3((unsigned)p.tiles, (unsigned)p.H), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
 template <int DP, int EP>
-hipError_t launch_r(PrefillParams& p, hipStream_t stream) {
-  return p.R == 0 ? launch<DP, 0, EP>(p, stream) : (p.R <= 32 ? launch<DP, 32, EP>(p, stream) : launch<DP, 64, EP>(p, stream));
+hipError_t launch_r(const PrefillParams& p, hipStream_t stream) {
+  if (p.R == 0) return launch<DP, 0, EP>(p, stream);
+  return p.R <= 32 ? launch<DP, 32, EP>(p, stream) : launch<DP, 64, EP>(p, stream);
 }
 
 }  // namespace
+
+size_t latent_prefill_workspace_bytes(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E) {
+  int64_t tiles, splits;
+  prefill_shape(T, S, N, H, &tiles, &splits);
+  return splits == 1 ? 0 : (size_t)(splits * T * H * (E + 1)) * 4;
+}
 
 hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t stream) {
   PrefillParams p;
@@ -364,6 +463,12 @@ hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t
   p.E = (int)a.E;
   p.causal = a.causal != 0;
   p.scale2 = a.scale * kLog2e;
+  int64_t tiles, splits;
+  prefill_shape(a.T, a.S, a.N, a.H, &tiles, &splits);
+  p.tiles = (int)tiles;
+  p.splits = (int)splits;
+  p.part = static_cast<float*>(a.workspace);
+  p.plse = splits > 1 ? p.part + splits * a.T * a.H * a.E : nullptr;
   return a.D <= 64 && a.E <= 64 ? launch_r<64, 64>(p, stream) : launch_r<128, 128>(p, stream);
 }
 

@@ -76,7 +76,8 @@ def _call(what: str, dev: torch.device, stream, made: list, entry, *args) -> Non
 def kda_latent_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                        k_rope: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                       scale: Optional[float] = None, causal: bool = True, with_lse: bool = False, stream=None):
+                       scale: Optional[float] = None, causal: bool = True, with_lse: bool = False,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
     """Latent attention in the expanded form over a packed batch.
 
     q: [T,H,D+R]; k: [S,H,D]; v: [S,H,E]; k_rope: [S,R], the rotary part of the
@@ -86,13 +87,14 @@ def kda_latent_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seq
     of the keys (default: the same).  With ``causal``, a sequence's queries are
     the last of its key positions.  ``scale`` defaults to (D+R)^-1/2.
     Returns (out [T,H,E], lse [T,H] fp32 or None); a query that sees no key
-    gets 0 and -inf.
+    gets 0 and -inf.  Few queries over many keys take a workspace, from PyTorch
+    unless one is given (:func:`kda_latent_prefill_workspace_size` bytes).
     """
     what = "kda_latent_prefill"
     lib = _lib.load_library()
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens
-    dev = _device(q, k, v, cu_seqlens, k_rope, cu_seqlens_k, out, lse)
+    dev = _device(q, k, v, cu_seqlens, k_rope, cu_seqlens_k, out, lse, workspace)
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or (k_rope is not None and k_rope.dim() != 2):
         raise KDAError(what, 3, "q, k, v must be 3-D and k_rope 2-D")
     (T, H, DR), (S, Hk, D), (Sv, Hv, E) = q.shape, k.shape, v.shape
@@ -117,12 +119,17 @@ def kda_latent_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seq
     out = _out(what, "out", out, (T, H, E), torch.bfloat16, dev, made)
     if lse is not None or with_lse:
         lse = _out(what, "lse", lse, (T, H), torch.float32, dev, made)
+    ws = _workspace(workspace, lib.kda_latent_prefill_workspace_size(T, S, N, H, E), dev, made)
     a = LatentPrefillArgs(T, S, N, H, D, R, E, KDA_BF16, q.data_ptr(), q.stride()[:2], k.data_ptr(), k.stride()[:2],
                           *rope, v.data_ptr(), v.stride()[:2], cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr(),
                           out.data_ptr(), None if lse is None else lse.data_ptr(),
-                          DR ** -0.5 if scale is None else scale, 1 if causal else 0)
+                          DR ** -0.5 if scale is None else scale, 1 if causal else 0, *ws)
     _call(what, dev, stream, made, lib.kda_latent_prefill, a)
     return out, lse
+
+
+def kda_latent_prefill_workspace_size(T: int, S: int, N: int, H: int, E: int) -> int:
+    return int(_lib.load_library().kda_latent_prefill_workspace_size(T, S, N, H, E))
 
 
 def kda_latent_decode_workspace_size(N: int, Q: int, H: int, L: int) -> int:

@@ -73,6 +73,95 @@ def test_prefill_dims(H, D, R, E):
     _check_prefill(x, lq, lk, True, _prefill(x, lq, lk, True))
 
 
+@pytest.mark.parametrize("lq,past,H,causal", [([1], [5000], 3, True), ([130], [4000], 8, True),
+                                              ([70, 3], [2200, 9000], 2, True), ([200], [2100], 5, False),
+                                              ([40, 0, 1], [0, 6000, 3000], 16, True), ([2300], [0], 1, True)])
+def test_prefill_few_queries_over_many_keys(lq, past, H, causal):
+    """The keys are split over workgroups and the pieces joined; a workspace of
+    the caller's that holds NaN gives the same."""
+    import kda_recurrent_state_amd as kda
+    lk = [a + b for a, b in zip(lq, past)]
+    need = kda.kda_latent_prefill_workspace_size(sum(lq), sum(lk), len(lq), H, 80)
+    assert need > 0
+    x = _prefill_inputs(lq, lk, H, 96, 32, 80)
+    got = _prefill(x, lq, lk, causal)
+    _check_prefill(x, lq, lk, causal, got)
+    ws = torch.full((need // 4,), math.nan, device="cuda")
+    again = _prefill(x, lq, lk, causal, workspace=ws)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_prefill_split_keys_leave_other_rows():
+    """Rows of q outside the sequences, with the keys split."""
+    import kda_recurrent_state_amd as kda
+    x = _prefill_inputs([50], [5000], 2, 64, 0, 64)
+    cu_q, cu_k = [5, 5, 41], [100, 100, 4900]
+    out = torch.full((50, 2, 64), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((50, 2), 7.0, device="cuda")
+    kda.kda_latent_prefill(x["q"], x["k"], x["v"], _i32(cu_q), cu_seqlens_k=_i32(cu_k), out=out, lse=lse)
+    want = ref.prefill(x["q"], x["k"], x["v"], None, cu_q, cu_k, 64 ** -0.5, True)
+    ref.check(out[5:41], lse[5:41], [w[5:41] for w in want], "rows")
+    assert (out[:5] == 7).all() and (out[41:] == 7).all() and (lse[:5] == 7).all() and (lse[41:] == 7).all()
+
+
+def test_prefill_graph_follows_offsets():
+    """A captured call whose offsets change between replays, keys split."""
+    x = _prefill_inputs([60], [6000], 4, 64, 32, 64)
+    import kda_recurrent_state_amd as kda
+    cu_q, cu_k = _i32([0, 60, 60]), _i32([0, 6000, 6000])
+    out, lse = torch.zeros(60, 4, 64, dtype=BF16, device="cuda"), torch.zeros(60, 4, device="cuda")
+    ws = torch.empty(kda.kda_latent_prefill_workspace_size(60, 6000, 2, 4, 64), dtype=torch.uint8, device="cuda")
+    call = lambda o, s, w: kda.kda_latent_prefill(x["q"], x["k"], x["v"], cu_q, k_rope=x["k_rope"],  # noqa: E731
+                                                  cu_seqlens_k=cu_k, out=o, lse=s, workspace=w)
+    call(out, lse, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out, lse, ws)
+    for a, b in (([0, 60, 60], [0, 6000, 6000]), ([0, 1, 60], [0, 4000, 6000]), ([0, 30, 60], [0, 10, 5000])):
+        cu_q.copy_(_i32(a))
+        cu_k.copy_(_i32(b))
+        g.replay()
+        torch.cuda.synchronize()
+        eager = call(torch.zeros_like(out), torch.zeros_like(lse), None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+        ref.check(out, lse, ref.prefill(x["q"], x["k"], x["v"], x["k_rope"], a, b, 96 ** -0.5, True), "graph %s" % a)
+
+
+def test_nothing_to_do_and_empty_sides():
+    import kda_recurrent_state_amd as kda
+    z = lambda *s: torch.zeros(*s, dtype=BF16, device="cuda")  # noqa: E731
+    out, lse = kda.kda_latent_prefill(z(0, 2, 64), z(5, 2, 64), z(5, 2, 64), _i32([0, 0]), cu_seqlens_k=_i32([0, 5]),
+                                      with_lse=True)
+    assert out.shape == (0, 2, 64) and lse.shape == (0, 2)
+    out, lse = kda.kda_latent_prefill(z(3, 2, 64), z(0, 2, 64), z(0, 2, 64), _i32([0, 3]), cu_seqlens_k=_i32([0, 0]),
+                                      with_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    out, lse = kda.kda_latent_decode(z(2, 16, 64), torch.zeros(0, 3, dtype=torch.int32, device="cuda"), _i32([]),
+                                     z(0, 4, 64), scale=1.0, with_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+def test_calls_on_two_streams_at_once():
+    """Decode and split prefill of different inputs under way together: each
+    call has a workspace of its own."""
+    a = _decode_inputs([3000, 40, 900], 2, 32, 512, 64, 64, seed=21)
+    b = _decode_inputs([100, 5000], 1, 64, 256, 32, 16, seed=22)
+    c = _prefill_inputs([33], [7000], 4, 128, 64, 128, seed=23)
+    alone = [_decode(a), _decode(b), _prefill(c, [33], [7000])]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = [_decode(a, stream=streams[0]), _decode(b, stream=streams[1]),
+               _prefill(c, [33], [7000], stream=streams[2])]
+        torch.cuda.synchronize()
+        for x, y in zip(alone, got):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 def test_prefill_rows_that_see_nothing():
     # more queries than keys: the first ones see none; and a sequence without keys
     lq, lk = [100, 40, 70], [30, 0, 70]

@@ -43,8 +43,8 @@ def _prefill(**kw):
     (dict(R=-8), SHAPE), (dict(E=0), SHAPE), (dict(N=0), SHAPE),
     (dict(dtype=0), DTYPE), (dict(dtype=7), DTYPE),
     (dict(D=12), UNSUPPORTED), (dict(D=136), UNSUPPORTED), (dict(R=4), UNSUPPORTED), (dict(R=72), UNSUPPORTED),
-    (dict(E=20), UNSUPPORTED), (dict(E=136), UNSUPPORTED), (dict(H=65537), UNSUPPORTED),
-    (dict(T=1 << 31), UNSUPPORTED), (dict(T=1 << 30, H=65536), UNSUPPORTED),
+    (dict(E=20), UNSUPPORTED), (dict(E=136), UNSUPPORTED), (dict(H=65536), UNSUPPORTED),
+    (dict(T=1 << 31), UNSUPPORTED), (dict(T=1 << 30, H=65535), UNSUPPORTED),
     (dict(scale=0.0), UNSUPPORTED), (dict(scale=-1.0), UNSUPPORTED), (dict(scale=math.inf), UNSUPPORTED),
     (dict(scale=math.nan), UNSUPPORTED),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(k_rope=None), NULL), (dict(out=None), NULL),
@@ -53,11 +53,23 @@ def _prefill(**kw):
     (dict(v_stride=(48, 20)), LAYOUT), (dict(k_rope_stride=12), LAYOUT), (dict(k_stride=(1 << 50, 16)), LAYOUT),
     (dict(q=0x10008), LAYOUT), (dict(k=0x20002), LAYOUT), (dict(v=0x40008), LAYOUT), (dict(k_rope=0x30008), LAYOUT),
     (dict(out=0x70004), LAYOUT),
+    (dict(S=1 << 16, H=1), WORKSPACE), (dict(S=1 << 16, H=1, workspace=0x10000000, workspace_bytes=64), WORKSPACE),
+    (dict(S=1 << 16, H=1, workspace=0x10000008, workspace_bytes=1 << 30), LAYOUT),
+    (dict(S=1 << 16, H=1, workspace=0x20000, workspace_bytes=1 << 30), ALIAS),
+    (dict(k_stride=((1 << 24) + 8, 16)), UNSUPPORTED), (dict(v_stride=((1 << 24) + 8, 24)), UNSUPPORTED),
+    (dict(k_rope_stride=(1 << 24) + 8), UNSUPPORTED),
     (dict(out=0x10000), ALIAS), (dict(out=0x20000 + 16), ALIAS), (dict(out=0x30000), ALIAS), (dict(out=0x40000), ALIAS),
     (dict(out=0x50000), ALIAS), (dict(out=0x60000), ALIAS), (dict(lse=0x70000 + 8), ALIAS), (dict(lse=0x10000), ALIAS),
 ])
 def test_prefill_refusals(lib, kw, status):
     assert lib.kda_latent_prefill(ctypes.byref(_prefill(**kw)), None) == status
+
+
+def test_prefill_workspace_is_for_few_queries_and_many_keys(lib):
+    size = lib.kda_latent_prefill_workspace_size
+    assert size(0, 100, 1, 8, 128) == 0 and size(100, 100, 1, 8, 136) == 0
+    assert size(100, 1024, 1, 8, 128) == 0 and size(1 << 16, 1 << 16, 1, 8, 128) == 0
+    assert size(100, 1 << 16, 1, 8, 128) > 0
 
 
 def test_prefill_nothing_to_do(lib):
