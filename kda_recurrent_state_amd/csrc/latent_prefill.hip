@@ -18,9 +18,10 @@ using namespace latent;
 constexpr int kTile = 64;       // keys a tile
 constexpr int kWaves = 4;       // 32 queries each
 constexpr int kQueries = 32 * kWaves;
-// Key tiles a piece has at least where a workgroup's keys are split: 16 take
-// about 20 us, twice what joining the pieces costs.
-constexpr int kPiece = 16;
+// Key tiles a piece has at least where a workgroup's keys are split: 8 take
+// about 12 us, joining two pieces 8 (128 queries over 1024 keys, 16 heads: 22 us
+// in two pieces, 27 in one; over 4096: 28 us in eight, 95 in one).
+constexpr int kPiece = 8;
 constexpr int kMostSplits = 32;
 
 struct PrefillParams {
@@ -371,35 +372,38 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
   }
 }
 
-// Joins the pieces of a query tile: half a wave a row, 4 columns a lane.
-// Grid: (query tiles, heads).
+// Joins the pieces of a query tile: half a wave a row, 4 columns a lane, 8
+// rows a workgroup (a workgroup a tile takes 30 us, one row after the other).
+// Grid: (query tiles x their rows / 8, heads).
+constexpr int kJoinRows = 8;
 __global__ __launch_bounds__(256) void latent_pieces_kernel(PrefillParams p) {
   const int lane = threadIdx.x & 63, half = threadIdx.x >> 5, c = (threadIdx.x & 31) * 4, h = blockIdx.y;
   QueryTile tile;
-  if (!find_tile(p, blockIdx.x, lane, &tile)) return;
+  if (!find_tile(p, blockIdx.x / (kQueries / kJoinRows), lane, &tile)) return;
   const int ntiles = (tile.end + kTile - 1) / kTile, per = piece_tiles(p, ntiles);
   if (per >= ntiles) return;
   const int pieces = (ntiles + per - 1) / per;
   const int64_t step = p.T * p.H;
-  for (int i = half; i < kQueries && tile.qfirst + i < tile.lq; i += 8) {
-    const int64_t row = (tile.q0 + tile.qfirst + i) * p.H + h;
-    float top = -INFINITY, sum = 0.f;
-    for (int s = 0; s < pieces; ++s) top = fmaxf(top, p.plse[s * step + row]);
-    const float base = top == -INFINITY ? 0.f : top;
-    f32x4 o = {0, 0, 0, 0};
+  const int i = tile.qfirst + blockIdx.x % (kQueries / kJoinRows) * kJoinRows + half;
+  if (i >= tile.lq) return;
+  const int64_t row = (tile.q0 + i) * p.H + h;
+  float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
-    for (int s = 0; s < pieces; ++s) {
-      const float f = exp2_hw(p.plse[s * step + row] - base);
-      sum += f;
-      if (c < p.E) o += f * *reinterpret_cast<const f32x4*>(p.part + (s * step + row) * p.E + c);
-    }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    if (c < p.E) {
-      const bf16x4 ob = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
-      *reinterpret_cast<bf16x4*>(p.out + row * p.E + c) = ob;
-    }
-    if (p.lse && c == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+  for (int s = 0; s < pieces; ++s) top = fmaxf(top, p.plse[s * step + row]);
+  const float base = top == -INFINITY ? 0.f : top;
+  f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < pieces; ++s) {
+    const float f = exp2_hw(p.plse[s * step + row] - base);
+    sum += f;
+    if (c < p.E) o += f * *reinterpret_cast<const f32x4*>(p.part + (s * step + row) * p.E + c);
   }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  if (c < p.E) {
+    const bf16x4 ob = {(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
+    *reinterpret_cast<bf16x4*>(p.out + row * p.E + c) = ob;
+  }
+  if (p.lse && c == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 // Query tiles of a head at most, and the pieces their keys are cut into.  With
@@ -420,7 +424,8 @@ hipError_t launch(const PrefillParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((latent_prefill_kernel<DP, RP, EP>), dim3((unsigned)blocks), dim3(kQueries * 2), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(latent_pieces_kernel, dim3((unsigned)p.tiles, (unsigned)p.H), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(latent_pieces_kernel, dim3((unsigned)p.tiles * (kQueries / kJoinRows), (unsigned)p.H), dim3(256),
+                     0, stream, p);
   return hipGetLastError();
 }
 

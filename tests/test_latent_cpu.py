@@ -68,7 +68,7 @@ def test_prefill_refusals(lib, kw, status):
 def test_prefill_workspace_is_for_few_queries_and_many_keys(lib):
     size = lib.kda_latent_prefill_workspace_size
     assert size(0, 100, 1, 8, 128) == 0 and size(100, 100, 1, 8, 136) == 0
-    assert size(100, 1024, 1, 8, 128) == 0 and size(1 << 16, 1 << 16, 1, 8, 128) == 0
+    assert size(100, 512, 1, 8, 128) == 0 and size(1 << 16, 1 << 16, 1, 8, 128) == 0
     assert size(100, 1 << 16, 1, 8, 128) > 0
 
 
