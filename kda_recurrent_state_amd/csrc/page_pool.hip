@@ -267,7 +267,8 @@ __global__ __launch_bounds__(kThreads) void fork_apply_kernel(Pool p, const IdxT
       }
       to[j] = pg;
     }
-    if (threadIdx.x == 0) p.lengths[d] = p.lengths[s];
+    // (the slot of an empty parent may be another entry's child by now)
+    if (threadIdx.x == 0) p.lengths[d] = used > 0 ? p.lengths[s] : 0;
     return;
   }
   const int64_t total = (int64_t)*w.count * st.per_page;

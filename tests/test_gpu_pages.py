@@ -127,6 +127,21 @@ def test_fork_bad_entries_and_full_pool():
     assert s.tolist() == [2, 2, 2, 2]
 
 
+@pytest.mark.parametrize("entries", [7, 160])
+@pytest.mark.parametrize("share", [True, False])
+def test_fork_of_an_empty_slot_that_becomes_a_child(entries, share):
+    """Every entry sees the pool as it was: a child of a slot that is empty before the call is empty, also where that
+    slot is another entry's child."""
+    pool = _pool(9, 400, 5, 1200, 8, 30, shared=0)
+    full = [s for s in range(400) if pool[1][s] > 0]
+    empty = [s for s in range(400) if pool[1][s] == 0][:2 * entries]
+    a, b = empty[:entries], empty[entries:]
+    src, dst = [full[i % len(full)] for i in range(entries)] + a, a + b
+    order = [i // 2 + entries * (i % 2) for i in range(2 * entries)]
+    status = _check_fork(pool, 8, [src[i] for i in order], [dst[i] for i in order], share, caches=[_caches(1200, 8)[0]])
+    assert not status.any()
+
+
 def test_fork_of_state_rows_matches_gather_and_scatter():
     """Recurrent states (page size 1, one row a slot, rows with a gap): a fork
     without sharing equals gathering the parents' rows and scattering them."""
