@@ -370,7 +370,7 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  * head from one latent vector a token, over a packed batch.  All pointers are
  * device pointers; every tensor's last dim is dense and its other dims have
  * the element strides given.
- *  T, S, N, H      -- query tokens, key tokens, sequences, heads.
+ *  T, S, N, H      -- query tokens, key tokens, sequences, heads (H <= 65535).
  *  D, R, E         -- key dim per head (8..128), rotary key dim shared by the
  *                     heads (0..64), value dim (8..128); multiples of 8.
  *  dtype           -- of q, k, k_rope, v and out: KDA_BF16.
@@ -398,8 +398,9 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  * For query i and head h of a sequence, over the keys j it sees:
  *   s_j = scale (q_i[:D] . k_j + q_i[D:] . k_rope_j)
  *   out_i = sum_j exp(s_j - lse_i) v_j,   lse_i = log sum_j exp(s_j)
- * A query that sees no key gets out 0 and lse -inf.  Rows of q that belong to
- * no sequence have their out and lse rows left as they were.
+ * A query that sees no key (or only keys whose score is -inf) gets out 0 and
+ * lse -inf.  Rows of q that belong to no sequence have their out and lse rows
+ * left as they were.
  * Precision: products of bf16 operands with fp32 sums; scores, the running
  * maximum and sum and the output accumulate in fp32; the softmax weights are
  * rounded to bf16 as operands of the second product.
@@ -446,7 +447,8 @@ kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* args, void* str
  * Arguments of kda_latent_decode: Q new tokens for each of N sequences against
  * a paged cache of latent rows, in the absorbed form (the key up-projection
  * folded into q, the value up-projection applied to out by the caller).
- *  N, Q, H         -- sequences, new tokens a sequence (>= 1), heads; Q * H <= 1024.
+ *  N, Q, H         -- sequences (<= 65535), new tokens a sequence (>= 1), heads;
+ *                     Q * H <= 1024.
  *  L, R            -- latent dim (8..512), rotary key dim (0..64); multiples of 8.
  *  dtype           -- of the cache, q, q_rope and out: KDA_BF16.
  *  cache           -- [num_pages, page_size, L+R], dense inner dims, page_stride
@@ -468,10 +470,10 @@ kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* args, void* str
  *   s_j = scale (q . row_j[:L] + q_rope . row_j[L:]),  out = sum_j softmax(s)_j row_j[:L]
  * A query that sees no row gets out 0 and lse -inf.  Rows whose page_table
  * entry lies outside [0, num_pages) are not seen; lengths are clamped to
- * [0, max_pages * page_size] (which may not exceed 2^30).  Rows of a page
- * behind a sequence's length are not read.  The result does not depend on the
- * order of workgroups; how a sequence is split depends on the whole batch's
- * lengths, so its rounding may change with its neighbours' lengths.
+ * [0, max_pages * page_size] (which may not exceed 2^30, nor 2^40 / N).
+ * Rows of a page behind a sequence's length are not read.  The result does not
+ * depend on the order of workgroups; how a sequence is split depends on the
+ * whole batch's lengths, so its rounding may change with its neighbours'.
  * Precision as kda_latent_prefill; partial results of split sequences are fp32.
  * A non-finite row a later query of the same call sees can reach its earlier
  * queries, as in kda_latent_prefill.
@@ -558,7 +560,7 @@ typedef struct {
  *    every store's copies are done.
  * Unserved entries change nothing.  All entries see the pool as it was before
  * the call.
- *  src, dst  -- [num_forks] int32 or int64 device arrays.
+ *  src, dst  -- [num_forks] int32 or int64 device arrays; num_forks <= 65536.
  *  stores    -- host array of num_stores stores (0 .. 4096; NULL with 0).
  *  status    -- [num_forks] int32 device output.
  *  workspace -- device scratch (4-byte aligned) of

@@ -375,6 +375,8 @@ kda_status_t check_latent_decode(const kda_latent_decode_args_t* a) {
   if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
   const int64_t most = (int64_t)1 << 30, row = a->L + a->R;
   if (a->page_size > most || a->max_pages > most / a->page_size || a->num_pages > 0x7fffffff) return KDA_E_UNSUPPORTED;
+  // (a workgroup's tiles are counted in 31 bits)
+  if (a->N > 1 && a->max_pages * a->page_size > ((int64_t)1 << 40) / a->N) return KDA_E_UNSUPPORTED;
   if (a->N > 1 && a->table_stride < a->max_pages) return KDA_E_OVERLAP;
   if (a->page_stride < a->page_size * row) return KDA_E_OVERLAP;
   if (a->page_stride % 8 != 0) return KDA_E_LAYOUT;
@@ -487,7 +489,7 @@ kda_status_t kda_page_fork(const kda_page_pool_t* pool, const kda_page_store_t* 
   if ((st = check_stores(stores, num_stores, pool->num_pages)) != KDA_OK) return st;
   if (it != KDA_I32 && it != KDA_I64) return KDA_E_DTYPE;
   if (num_forks < 0) return KDA_E_SHAPE;
-  if (num_forks > ((int64_t)1 << 24)) return KDA_E_UNSUPPORTED;
+  if (num_forks > ((int64_t)1 << 16)) return KDA_E_UNSUPPORTED;  // (each entry's dst is compared with those before it)
   if (num_forks == 0) return KDA_OK;
   if (!src || !dst || !status) return KDA_E_NULL;
   const size_t need = kda::page_fork_workspace_bytes(num_forks, pool->max_pages, pool->num_pages, share != 0);

@@ -95,6 +95,7 @@ def _decode(lib, **kw):
     (dict(Q=1025, H=1), UNSUPPORTED), (dict(Q=33, H=32), UNSUPPORTED), (dict(N=65536), UNSUPPORTED),
     (dict(scale=0.0), UNSUPPORTED), (dict(scale=math.nan), UNSUPPORTED),
     (dict(max_pages=1 << 27, table_stride=1 << 27), UNSUPPORTED), (dict(page_size=1 << 31), UNSUPPORTED),
+    (dict(N=65535, max_pages=1 << 21, table_stride=1 << 21), UNSUPPORTED),
     (dict(table_stride=3), OVERLAP), (dict(page_stride=16 * 80 - 8), OVERLAP), (dict(page_stride=16 * 80 + 4), LAYOUT),
     (dict(page_stride=1 << 45), SHAPE),
     (dict(cache=None), NULL), (dict(page_table=None), NULL), (dict(lengths=None), NULL), (dict(q=None), NULL),
@@ -155,7 +156,7 @@ def test_pool_refusals(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(it=3), DTYPE), (dict(m=-1), SHAPE), (dict(m=(1 << 24) + 1), UNSUPPORTED), (dict(src=None), NULL),
+    (dict(it=3), DTYPE), (dict(m=-1), SHAPE), (dict(m=(1 << 24) + 1), UNSUPPORTED), (dict(m=(1 << 16) + 1), UNSUPPORTED), (dict(src=None), NULL),
     (dict(dst=None), NULL), (dict(status=None), NULL), (dict(ws=None), WORKSPACE), (dict(wb=8), WORKSPACE),
     (dict(ws=0x70002), LAYOUT),
     (dict(stores=((None, 256, 256),)), NULL), (dict(stores=((0x1000000, 255, 256),)), OVERLAP),
