@@ -176,32 +176,35 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
     for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
   float m = -INFINITY, l = 0.f;  // in units of scale2 s
 
-  // Staged rows: chunk c of a key or value row r lies at c ^ 2 (r & 7) (of 8
-  // chunks: c ^ ((r >> 1) & 3) * 2), of a rotary row at c ^ (r / (rows in 256
-  // B)), so that the 16-byte operand reads and the transposed reads of values
-  // fall on distinct banks.  Each region is filled by loads of whole rows; a
-  // lane's rows in successive loads differ by a multiple of 8, so its chunk is
-  // the same.  Padding columns get copies of a row's last chunk: the queries
-  // are 0 there and the outputs not written.
+  // Staged rows: chunk c of a key or rotary row r lies at c ^ (r / (rows in 256
+  // B)), of a value row at c ^ 4 (r & 3) (of 8 chunks: c ^ 4 ((r >> 1) & 1)).
+  // The 16 lanes of a cycle of a 16-byte operand read have 16 rows of the two
+  // halves, the 32 of a transposed 8-byte read four rows of four chunks, and
+  // these fall on distinct banks (two lanes on each: 1253 -> %s us for 16384
+  // tokens, 16 heads).  Each region is filled by loads of whole rows; a lane's
+  // rows in successive loads differ by a multiple of 16, so its chunk is the
+  // same.  Padding columns get copies of a row's last chunk: the queries are 0
+  // there and the outputs not written.
   struct Region {
     const char* base;  // key 0
     int64_t step;      // bytes from key to key
     unsigned col;      // the lane's chunk
     int row;           // and its row in the first load
   };
-  auto swz = [](int r, int chunks) { return chunks >= 16 ? (r & 7) << 1 : ((r >> 1) & 3) << 1; };
-  auto region = [&](const __bf16* base, int64_t stride, int chunks, int have, bool rotary) {
+  auto kswz = [](int r, int chunks) { return r / (16 / chunks) % chunks; };
+  auto vswz = [](int r, int chunks) { return chunks >= 16 ? (r & 3) << 2 : (r & 2) << 1; };
+  auto region = [&](const __bf16* base, int64_t stride, int chunks, int have, bool values) {
     Region g;
     g.base = reinterpret_cast<const char*>(base);
     g.step = stride * 2;
     g.row = (wave * 64 + lane) / chunks;
-    const int pos = lane % chunks, c = rotary ? pos ^ (g.row / (16 / chunks) % chunks) : pos ^ swz(g.row, chunks);
+    const int pos = lane % chunks, c = pos ^ (values ? vswz(g.row, chunks) : kswz(g.row, chunks));
     g.col = (unsigned)(c < have ? c : have - 1) * 16;
     return g;
   };
   const Region kreg = region(p.k + k0 * p.ks[0] + h * p.ks[1], p.ks[0], KC, p.D / 8, false);
-  const Region rreg = region(p.kr + k0 * p.krs, p.krs, RC > 0 ? RC : 8, p.R / 8, true);
-  const Region vreg = region(p.v + k0 * p.vs[0] + h * p.vs[1], p.vs[0], VC, p.E / 8, false);
+  const Region rreg = region(p.kr + k0 * p.krs, p.krs, RC > 0 ? RC : 8, p.R / 8, false);
+  const Region vreg = region(p.v + k0 * p.vs[0] + h * p.vs[1], p.vs[0], VC, p.E / 8, true);
   const unsigned lds_at = lds_offset(lds) + wave * 1024;
   // loads of region g for the tile at key j0, of whose rows ``rows`` are there
   // (the others get the last one's bytes: their weights are 0)
@@ -230,8 +233,8 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
 
   // the lane's places in a stage: key operands (row ln of a 32-row block,
   // chunk 2 k + lh) and transposed value reads (4 rows x 16 columns a group)
-  const int kat = ln * DP * 2 + ((lh ^ swz(ln, KC)) << 4), rat = kKeyBytes + ln * RP * 2;
-  const int rx = RC > 0 ? ln / (16 / (RC > 0 ? RC : 8)) % (RC > 0 ? RC : 8) : 0;
+  const int kat = ln * DP * 2 + ((lh ^ kswz(ln, KC)) << 4), rat = kKeyBytes + ln * RP * 2;
+  const int rx = kswz(ln, RC > 0 ? RC : 8);
   const int vrow = 4 * lh + ((lane & 15) >> 2), vcol = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const int vat = kKeyBytes + kRotBytes + vrow * EP * 2 + (lane & 1) * 8;
 
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
         for (int q = 0; q < G; ++q) {
           const int f = g * G + q, bu = f / MT, i = f % MT;
           // rows vrow + 16 bu and 8 further on: the same chunk
-          const char* at = buf + vat + (((4 * i + vcol) ^ swz(vrow, VC)) << 4) + bu * 16 * EP * 2;
+          const char* at = buf + vat + (((4 * i + vcol) ^ vswz(vrow, VC)) << 4) + bu * 16 * EP * 2;
           vf[g & 1][q] = join(read_tr(at), read_tr(at + 8 * EP * 2));
         }
       };
