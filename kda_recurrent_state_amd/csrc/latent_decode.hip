@@ -568,6 +568,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 // sequences).
 __global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, int MB, int parts) {
   __shared__ f32x4 osum[kWaves][2][64];
+  __shared__ float wtop[kWaves], wsum[kWaves];
   const int n = blockIdx.y, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int row = blockIdx.x * (kWaves / parts) + wave / parts, part = wave % parts, c = lane * 8;
   const bool have = row < p.rows;
@@ -584,35 +585,66 @@ __global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, i
   // share w0 holds the sequence's beginning (slot 2 w0 + 1), the later ones
   // begin in mid-sequence (slot 2 w)
   auto slot = [&](int w) { return at + (int64_t)(2 * w + (w == w0 ? 1 : 0)) * MB; };
-  float top = -INFINITY, sum = 0.f, base = 0.f;
+  // one pass with a running maximum, four pieces' loads at once
+  float top = -INFINITY, sum = 0.f;
   f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   if (have) {
-    for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.plse[slot(w)]);
+    for (int first = w0 + part; first <= w1; first += 4 * parts) {
+      float e[4];
+      f32x4 x[4][2];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    base = top == -INFINITY ? 0.f : top;
-    for (int w = w0 + lane; w <= w1; w += 64) sum += exp2_hw(p.plse[slot(w)] - base);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    if (c < p.L) {
-#pragma unroll 4
-      for (int w = w0 + part; w <= w1; w += parts) {
+      for (int u = 0; u < 4; ++u) {
+        const int w = first + u * parts;
+        e[u] = -INFINITY;
+        x[u][0] = x[u][1] = f32x4{0, 0, 0, 0};
+        if (w > w1) continue;
         const int64_t s = slot(w);
-        const float f = exp2_hw(p.plse[s] - base);
-        o[0] += f * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
-        o[1] += f * *reinterpret_cast<const f32x4*>(p.part + s * p.L + c + 4);
+        e[u] = p.plse[s];
+        if (c < p.L) {
+          x[u][0] = *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
+          x[u][1] = *reinterpret_cast<const f32x4*>(p.part + s * p.L + c + 4);
+        }
       }
+      float mx = top;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mx = fmaxf(mx, e[u]);
+      const float base = mx == -INFINITY ? 0.f : mx, old = exp2_hw(top - base);
+      sum *= old;
+      o[0] *= old;
+      o[1] *= old;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = exp2_hw(e[u] - base);
+        sum += f;
+        o[0] += f * x[u][0];
+        o[1] += f * x[u][1];
+      }
+      top = mx;
     }
   }
   if (parts > 1) {  // (uniform over the workgroup)
     osum[wave][0][lane] = o[0];
     osum[wave][1][lane] = o[1];
+    if (lane == 0) {
+      wtop[wave] = top;
+      wsum[wave] = sum;
+    }
     __syncthreads();
-    if (part == 0)
+    if (part == 0) {
+      float mx = top;
+      for (int i = 1; i < parts; ++i) mx = fmaxf(mx, wtop[wave + i]);
+      const float base = mx == -INFINITY ? 0.f : mx, own = exp2_hw(top - base);
+      sum *= own;
+      o[0] *= own;
+      o[1] *= own;
       for (int i = 1; i < parts; ++i) {
-        o[0] += osum[wave + i][0][lane];
-        o[1] += osum[wave + i][1][lane];
+        const float f = exp2_hw(wtop[wave + i] - base);
+        sum += f * wsum[wave + i];
+        o[0] += f * osum[wave + i][0][lane];
+        o[1] += f * osum[wave + i][1][lane];
       }
+      top = mx;
+    }
   }
   if (part != 0 || !have) return;
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
