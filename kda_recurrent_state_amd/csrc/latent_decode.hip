@@ -8,6 +8,25 @@
 // over the rows its token sees, so the same row is key and value: it is read
 // once from HBM, staged in LDS, and serves both products from there.
 //
+// Bound.  A row is 2 (L + R) bytes and 2 (2 L + R) flop a query row: with 64
+// query rows about 120 flop a byte, below the 270 at which this chip's copies
+// (5 TB/s) and matrix products (1350 TFLOP/s) balance.  64 query rows over 200
+// ragged sequences (L = 512, R = 64, 414 MB): 127-145 us, join included, where a
+// copy's rate gives 84; 128 rows over 64 x 16000 tokens: 366-380 us, 740
+// TFLOP/s, where the bytes give 236 and the products 206.  What the kernel
+// adds are the phases of a tile that do not overlap in a workgroup (scores,
+// weights, output, two barriers) and, with 128 rows, the second row block's
+// reads of the same rows from L2.
+//
+// Tile.  64 tokens in two stages of 72 KB fill the LDS, so a CU has one
+// workgroup of 8 waves.  For the scores a wave takes a block of 16 query rows
+// and a group of the tokens, for the output all rows and an eighth of the
+// columns, so the weights go through LDS and the output stays in registers (64
+// a lane at 64 rows).  Tiles of 32 tokens in four stages took 134 / 397 us
+// where these then took 134 / 394; 4 waves of 512 registers 136 / 414 where 8
+// took 143 / 400, and with 128 rows a workgroup 742 (the registers did not hold
+// output, queries and scores).
+//
 // Work split.  The batch's rows, cut into tiles of 64 tokens, form one long
 // line of tiles (sequence after sequence); workgroup w of G takes an equal
 // share of that line, whatever the lengths are.  A share may end one
@@ -47,7 +66,6 @@ struct DecodeParams {
   __bf16* out;
   float* lse;
   int N, Q, H, rows, row_blocks, groups;
-  int few;         // up to 256 sequences and 2^28 tokens each
   float scale2;    // scale log2 e
   float* part;     // [row_blocks][2 groups][MB][L] normalised outputs
   float* plse;     // [row_blocks][2 groups][MB] log2 of the sums
@@ -80,41 +98,10 @@ __device__ __forceinline__ int64_t share_begin(const DecodeParams& p, int64_t to
   return w * quot + (w < rem ? w : rem);
 }
 
-// Every wave scans the lengths by itself: one pass with four sequences a lane
-// where that holds them all (their lengths then go to LDS, too), else 64 at a
-// time, once for the sum and once for the place.
-__device__ __forceinline__ Share find_share(const DecodeParams& p, int w, int lane, int32_t* lens) {
+// Every wave scans the lengths by itself, 64 at a time, once for the sum and
+// once for the place.
+__device__ __forceinline__ Share find_share(const DecodeParams& p, int w, int lane) {
   Share s;
-  if (p.few) {
-    int c[4], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = 4 * lane + j;
-      const int tokens = n < p.N ? seq_tokens(p, n) : 0;
-      if (threadIdx.x < 64) lens[n] = tokens;
-      c[j] = tiles_of(tokens);
-      sum += c[j];
-    }
-    const int incl = wave_scan(sum, lane);
-    const int t0 = (int)share_begin(p, __builtin_amdgcn_readlane(incl, 63), w, &s.left);
-    const unsigned long long past = __ballot(incl > t0);
-    if (s.left == 0 || past == 0) {
-      s.left = 0;
-      return s;
-    }
-    const int i = __ffsll(past) - 1;
-    s.t = t0 - __builtin_amdgcn_readlane(incl - sum, i);
-    s.n = 4 * i;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const int x = __builtin_amdgcn_readlane(c[j], i);
-      if (s.n == 4 * i + j && s.t >= x) {
-        s.t -= x;
-        ++s.n;
-      }
-    }
-    return s;
-  }
   int64_t total = 0;
   for (int n = lane; n < p.N; n += 64) total += tiles_of(seq_tokens(p, n));
 #pragma unroll
@@ -286,7 +273,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
   __shared__ int32_t pages[2][kWaves][64];  // page of token 64 t + lane of the tile located next
   __shared__ int grown[2];        // whether a row's maximum has grown much in this tile
-  __shared__ int32_t lens[256];            // the sequences' tokens (few)
   __shared__ int64_t qat[2][MB];           // of a query row: its q and q_rope in a sequence's
   __shared__ int32_t less[MB];             // and how many tokens less than the last one it sees
 
@@ -297,7 +283,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
   const int rb = idx % p.row_blocks, w = (idx / p.row_blocks) * 8 + xcd;
 
-  const Share share = find_share(p, w, lane, lens);
+  const Share share = find_share(p, w, lane);
   if (share.left == 0) return;
   if (tid < MB) {
     // (rows behind the last get the first one's queries; they are not written)
@@ -312,7 +298,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const int tg = (wave / NB) % TG;               // and tokens
   __syncthreads();
   const int sees_less = less[rblock * 16 + ln];
-  auto tokens_of = [&](int n) { return uniform(p.few ? lens[n] : seq_tokens(p, n)); };
+  auto tokens_of = [&](int n) { return uniform(seq_tokens(p, n)); };
 
   // where the page of token 64 t + lane of sequence s is, which has len tokens
   // (the last one's for lanes behind it), and that row's place; -1: no such row
@@ -565,7 +551,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 // Joins the pieces of a sequence that several workgroups share, and writes
 // the outputs of empty sequences.  A wave takes one query row (8 columns a
 // lane) and every ``parts``-th piece; grid: (groups of 8 / parts rows,
-// sequences).
+// sequences).  HBM-bound where there are many rows: 46 MB of pieces of 200
+// sequences x 64 rows in 11.5 us, 51 MB in 13 us; a pass for the maxima before
+// one for the outputs took 13 and 17.5.
 __global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, int MB, int parts) {
   __shared__ f32x4 osum[kWaves][2][64];
   __shared__ float wtop[kWaves], wsum[kWaves];
@@ -662,9 +650,9 @@ struct Shape {
   int nb, row_blocks, groups;
 };
 
-// Query rows a workgroup (16, 32 or 64) and shares of the line: one
-// workgroup fits a CU (LDS), 256 in all; the shares are a multiple of 8, one
-// set an XCD.
+// Query rows a workgroup (16, 32 or 64: 16 rows of 200 ragged sequences take 98
+// us in workgroups of 16 and 112 of 64) and shares of the line: one workgroup
+// fits a CU (LDS), 256 in all; the shares are a multiple of 8, one set an XCD.
 Shape decode_shape(int64_t Q, int64_t H) {
   Shape s;
   const int64_t rows = Q * H;
@@ -737,7 +725,6 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   p.rows = (int)(a.Q * a.H);
   p.row_blocks = s.row_blocks;
   p.groups = s.groups;
-  p.few = a.N <= 256 && a.max_pages <= ((int64_t)1 << 28) / a.page_size;
   p.scale2 = a.scale * kLog2e;
   p.part = static_cast<float*>(a.workspace);
   p.plse = p.part + part_rows(s) * a.L;
@@ -745,7 +732,8 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   hipError_t e = a.L <= 128 ? launch_r<128>(p, s.nb, stream)
                             : (a.L <= 256 ? launch_r<256>(p, s.nb, stream) : launch_r<512>(p, s.nb, stream));
   if (e != hipSuccess) return e;
-  // few rows: more waves share a row's pieces
+  // few rows: more waves share a row's pieces (one sequence of 4000 tokens, 32
+  // rows: 19.5 us, a wave a row 31)
   int parts = kWaves;
   while (parts > 1 && (int64_t)p.rows * p.N * parts > 2048 * kWaves) parts >>= 1;
   const int per = kWaves / parts;
