@@ -28,8 +28,11 @@ constexpr float kLn2 = 0.693147180559945309417f;
 __device__ __forceinline__ unsigned lds_offset(const void* lds) {
   return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)lds;
 }
-__device__ __forceinline__ void load_lds16(const char* base, unsigned offset, unsigned lds) {  // base is uniform
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(lds)
+// base is uniform.  (A memory instruction may read a scalar register five wait
+// states after a vector instruction, such as a read of one lane, has written it;
+// the compiler does not count them for assembly.)
+__device__ __forceinline__ void load_lds16(const char* base, unsigned offset, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(lds)
                : "memory");
 }
 __device__ __forceinline__ void load_lds16(const char* lane_address, unsigned lds) {
