@@ -83,6 +83,7 @@ __device__ __forceinline__ int tiles_of(int tokens) { return (int)(((int64_t)tok
 struct Share {
   int left;  // tiles, 0: no such share
   int n, t;  // sequence and tile of the first one
+  int len;   // and that sequence's tokens
 };
 
 // Shares are as equal as they can be and none is empty (there are fewer of
@@ -109,13 +110,14 @@ __device__ __forceinline__ Share find_share(const DecodeParams& p, int w, int la
   const int64_t t0 = share_begin(p, lane64(total, 0), w, &s.left);
   int64_t base = 0;
   for (int n0 = 0; s.left > 0 && n0 < p.N; n0 += 64) {
-    const int c = n0 + lane < p.N ? tiles_of(seq_tokens(p, n0 + lane)) : 0;
+    const int tokens = n0 + lane < p.N ? seq_tokens(p, n0 + lane) : 0, c = tiles_of(tokens);
     const int incl = wave_scan(c, lane);
     const unsigned long long past = __ballot(base + incl > t0);
     if (past) {
       const int i = __ffsll(past) - 1;
       s.n = n0 + i;
       s.t = (int)(t0 - base) - __builtin_amdgcn_readlane(incl - c, i);
+      s.len = __builtin_amdgcn_readlane(tokens, i);
       return s;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
@@ -283,8 +285,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
   const int rb = idx % p.row_blocks, w = (idx / p.row_blocks) * 8 + xcd;
 
-  const Share share = find_share(p, w, lane);
-  if (share.left == 0) return;
   if (tid < MB) {
     // (rows behind the last get the first one's queries; they are not written)
     const int row = rb * MB + tid < p.rows ? rb * MB + tid : 0, qi = row / p.H, qh = row - qi * p.H;
@@ -293,6 +293,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     less[tid] = p.Q - 1 - qi;
   }
   if (tid < 2) grown[tid] = 0;
+  const Share share = find_share(p, w, lane);
+  if (share.left == 0) return;
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;                  // query rows this wave scores
   const int tg = (wave / NB) % TG;               // and tokens
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   auto fetch = [&](int i, int to) { D::fetch(i, at, wave, lane, columns, stage_at + to * kStageBytes); };
   cur.n = uniform(share.n);
   cur.t = uniform(share.t);
-  cur.len = tokens_of(cur.n);
+  cur.len = uniform(share.len);
   locate(*lookup(cur.n, cur.t, cur.len), cur);
   D::fetch_rotary(at, wave, lane, columns, rotary_at);
 #pragma unroll
