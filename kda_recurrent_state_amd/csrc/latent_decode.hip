@@ -12,7 +12,7 @@
 // query rows about 120 flop a byte, below the 270 at which this chip's copies
 // (5 TB/s) and matrix products (1350 TFLOP/s) balance.  64 query rows over 200
 // ragged sequences (L = 512, R = 64, 414 MB): 127-145 us, join included, where a
-// copy's rate gives 84; 128 rows over 64 x 16000 tokens: 366-380 us, 740
+// copy's rate gives 84; 128 rows over 64 x 16000 tokens: 366-384 us, 740
 // TFLOP/s, where the bytes give 236 and the products 206.  What the kernel
 // adds are the phases of a tile that do not overlap in a workgroup (scores,
 // weights, output, two barriers) and, with 128 rows, the second row block's
