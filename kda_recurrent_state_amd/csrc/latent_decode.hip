@@ -35,8 +35,6 @@
 // outputs with their log-sum, and the join kernel weighs them.  Both kernels
 // derive the shares from the lengths on the device, so a captured call
 // follows its lengths.
-#include <type_traits>
-
 #include "internal.h"
 #include "latent_common.h"
 
