@@ -384,8 +384,10 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  *                     dim); the token strides of k, k_rope and v are at most 2^24.
  *  cu_seqlens_q    -- [N+1] int32 offsets of the sequences' queries in q.
  *  cu_seqlens_k    -- [N+1] int32 offsets of their keys in k, k_rope and v.
- *                     Both non-decreasing (not checked; the kernel clamps, so
- *                     bad offsets cannot address outside the tensors).
+ *                     Both non-decreasing (not checked: the kernel clamps them
+ *                     to the tensors and raises a query offset to the largest
+ *                     before it, so bad offsets address nothing outside and no
+ *                     query belongs to two sequences).
  *  out             -- [T, H, E] contiguous, 8-byte aligned.
  *  lse             -- [T, H] fp32, or NULL.
  *  scale           -- factor of the scores, positive and finite.

@@ -67,13 +67,27 @@ struct QueryTile {
 __device__ __forceinline__ bool find_tile(const PrefillParams& p, int x, int lane, QueryTile* out) {
   int n = -1, t = 0;
   int64_t q0 = 0, q1 = 0;
+  int64_t behind = 0;  // the largest offset before these sequences
   for (int n0 = 0; n0 < p.N; n0 += 64) {
-    int64_t a = 0, b = 0;
+    int64_t a = p.T, b = p.T;
     int mine = n0 + lane;
     if (mine < p.N) {
       a = clamp64(p.cu_q[mine], 0, p.T);
-      b = clamp64(p.cu_q[mine + 1], a, p.T);
+      b = clamp64(p.cu_q[mine + 1], 0, p.T);
     }
+    // An offset below one before it is raised to that one, so that no two
+    // sequences have a query in common: they would write the same rows.
+    if (__any(b < a || a < behind)) {
+      int top = (int)(a < behind ? behind : a);
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(top, d, 64);
+        if (lane >= d && y > top) top = y;
+      }
+      a = top;
+      if (b < a) b = a;
+    }
+    behind = lane64(b, 63);
     int c = (int)((b - a + kQueries - 1) / kQueries);
     if (p.N <= 64 && p.N > 1) {
       // c of the sequence of this rank, which is put in ``mine``

@@ -231,6 +231,35 @@ def test_prefill_bad_offsets_stay_inside():
     ref.check(out[:50], None, want, "clamped")
 
 
+@pytest.mark.parametrize("cu_q", [[0, 50, 20, 90], [10, 5, 80, 80, 30, 90], [-4, 40, 400, 0, 90], [90, 0, 90],
+                                  [0] + [30, 10] * 40 + [70, 60, 90], [(37 * i) % 91 for i in range(150)]])
+def test_prefill_query_offsets_that_fall(cu_q):
+    """A query offset below one before it is raised to it: no row has two
+    writers, whatever the offsets, and rows of no sequence stay as they were."""
+    import kda_recurrent_state_amd as kda
+    x = _prefill_inputs([90], [90], 2, 64, 32, 64)
+    cu_k = [(29 * i) % 60 + (40 if i % 2 else 0) for i in range(len(cu_q))]
+    sound, k_ranges = [], []
+    for i, c in enumerate(cu_q):
+        sound.append(max([min(max(c, 0), 90)] + sound[-1:]))
+        k0, k1 = min(cu_k[i], 90), min(cu_k[min(i + 1, len(cu_k) - 1)], 90)
+        k_ranges.append((k0, max(k0, k1)))
+    out = torch.full((90, 2, 64), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((90, 2), 7.0, device="cuda")
+    kda.kda_latent_prefill(x["q"], x["k"], x["v"], _i32(cu_q), k_rope=x["k_rope"], cu_seqlens_k=_i32(cu_k), out=out,
+                           lse=lse)
+    torch.cuda.synchronize()
+    seen = torch.zeros(90, dtype=torch.bool)
+    for a, b, (c, d) in zip(sound, sound[1:], k_ranges):
+        if a == b:
+            continue
+        seen[a:b] = True
+        want = ref.prefill(x["q"][a:b], x["k"][c:d], x["v"][c:d], x["k_rope"][c:d], [0, b - a], [0, d - c], 96 ** -0.5,
+                           True)
+        ref.check(out[a:b], lse[a:b], want, "rows %d to %d" % (a, b))
+    assert (out[~seen.cuda()] == 7).all() and (lse[~seen.cuda()] == 7).all()
+
+
 def test_prefill_many_sequences():
     # more sequences than one scan step of a wave, most of them tiny
     lq = [(7 * i) % 5 for i in range(150)] + [140, 1]
