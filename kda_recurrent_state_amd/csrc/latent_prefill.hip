@@ -212,12 +212,14 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
   // these fall on distinct banks (two lanes on each: 1275 -> 1263 us for 16384
   // tokens, 16 heads).  Each region is filled by loads of whole rows; a lane's
   // rows in successive loads differ by a multiple of 16, so its chunk is the
-  // same.  Padding columns get copies of a row's last chunk: the queries are 0
-  // there and the outputs not written.
+  // same.  Padding columns (D < DP, R < RP) of keys stay 0 from the start, as
+  // the queries are there: anything else times 0 could be NaN.  Those of values
+  // get copies of a row's last chunk and end in outputs that are not written.
   struct Region {
     const char* base;  // key 0
     int64_t step;      // bytes from key to key
     unsigned col;      // the lane's chunk
+    bool there;        // whether a row has it (else the lane is off)
     int row;           // and its row in the first load
   };
   auto kswz = [](int r, int chunks) { return r / (16 / chunks) % chunks; };
@@ -229,6 +231,7 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
     g.row = (wave * 64 + lane) / chunks;
     const int pos = lane % chunks, c = pos ^ (values ? vswz(g.row, chunks) : kswz(g.row, chunks));
     g.col = (unsigned)(c < have ? c : have - 1) * 16;
+    g.there = values || c < have;
     return g;
   };
   const Region kreg = region(p.k + k0 * p.ks[0] + h * p.ks[1], p.ks[0], KC, p.D / 8, false);
@@ -240,6 +243,7 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
   auto fill = [&](const Region& g, int chunks, int j0, int rows, unsigned to) {
     const int per = W * 64 / chunks;  // rows of the workgroup's loads
     const char* base = g.base + j0 * g.step;
+    if (!g.there) return;
     if (rows >= kTile) {
       const unsigned off = (unsigned)g.row * (unsigned)g.step + g.col;
 #pragma unroll
@@ -267,6 +271,12 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
   const int vrow = 4 * lh + ((lane & 15) >> 2), vcol = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const int vat = kKeyBytes + kRotBytes + vrow * EP * 2 + (lane & 1) * 8;
 
+  if (p.D < DP || p.R < RP) {
+    for (int i = tid * 16; i < kKeyBytes + kRotBytes; i += W * 64 * 16)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) *reinterpret_cast<u32x4*>(lds + b * kStage + i) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+  }
   if (first < last) stage(first);
   for (int j = first; j < last; ++j) {
     wait_loads<0>();

@@ -260,6 +260,27 @@ def test_prefill_query_offsets_that_fall(cu_q):
     assert (out[~seen.cuda()] == 7).all() and (lse[~seen.cuda()] == 7).all()
 
 
+@pytest.mark.parametrize("D,R,E", [(96, 32, 80), (64, 0, 128), (64, 32, 128), (120, 56, 24), (8, 8, 8), (64, 16, 64),
+                                   (40, 0, 64), (128, 64, 128)])
+@pytest.mark.parametrize("lq,past", [([70, 5, 130], [0, 85, 3]), ([40], [3000])])
+def test_prefill_keys_with_infinite_components(D, R, E, lq, past):
+    """A score bias in the last column of the keys (and of the rotary keys):
+    -inf takes a key out, at every width; queries of which no key is left get 0
+    and -inf."""
+    lk = [a + b for a, b in zip(lq, past)]
+    x = _prefill_inputs(lq, lk, 2, D, R, E)
+    gen = torch.Generator().manual_seed(31)
+    S = sum(lk)
+    out = torch.rand(S, generator=gen) < 0.3
+    out[:3] = True
+    x["q"][..., D - 1] = 1
+    x["k"][..., D - 1] = torch.where(out, -math.inf, 0.25).to(BF16).cuda()[:, None]
+    if R:
+        x["q"][..., D + R - 1] = 1
+        x["k_rope"][..., R - 1] = torch.where(torch.rand(S, generator=gen) < 0.2, -math.inf, 0.0).to(BF16).cuda()
+    _check_prefill(x, lq, lk, True, _prefill(x, lq, lk, True))
+
+
 def test_prefill_many_sequences():
     # more sequences than one scan step of a wave, most of them tiny
     lq = [(7 * i) % 5 for i in range(150)] + [140, 1]
