@@ -385,6 +385,36 @@ def test_decode_rows_behind_the_length_may_be_anything():
     ref.check(*_decode(x), want, "behind")
 
 
+@pytest.mark.parametrize("L,R", [(512, 56), (136, 24), (504, 56), (256, 32), (8, 8), (128, 8), (512, 64)])
+@pytest.mark.parametrize("Q,H", [(1, 5), (2, 20), (1, 64)])
+def test_decode_rotary_keys_with_infinite_components(L, R, Q, H):
+    """A score bias in the last rotary column: -inf takes a row out, at every
+    width; a sequence of which no row is left gets 0 and -inf."""
+    lens = [300, 2, 70, 129]
+    x = _decode_inputs(lens, Q, H, L, R, 16)
+    gen = torch.Generator().manual_seed(33)
+    x["q_rope"][..., R - 1] = 1
+    x["cache"][..., L + R - 1] = torch.where(torch.rand(x["cache"].shape[:2], generator=gen) < 0.3, -math.inf, 0.5).to(BF16)
+    x["cache"][x["table"][2, :5].long(), :, L + R - 1] = -math.inf
+    out, lse = _decode(x)
+    _check_decode(x, (out, lse))
+    assert (out[2] == 0).all() and (lse[2] == -math.inf).all()
+
+
+@pytest.mark.parametrize("L,R", [(384, 0), (136, 0), (504, 56), (40, 8), (264, 64)])
+def test_decode_latents_with_infinite_components(L, R):
+    """-inf in a latent row's last value, which the queries take as it is: the
+    row has weight 0, and the other columns of the output do not see it."""
+    x = _decode_inputs([200, 65, 3], 1, 6, L, R, 64)
+    gen = torch.Generator().manual_seed(34)
+    x["q"][..., L - 1] = 1
+    bad = torch.rand(x["cache"].shape[:2], generator=gen) < 0.3
+    x["cache"][..., L - 1] = torch.where(bad, -math.inf, 0.5).to(BF16)
+    out, lse = _decode(x)
+    want = ref.decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], 0.07)
+    ref.check(out[..., :L - 1], lse, [want[0][..., :L - 1], want[1], want[2][..., :L - 1]], "latent bias")
+
+
 def test_decode_strides():
     """q as the transposed result of a product by head, q_rope as the end of a
     joint projection, pages with a gap, rows of a wider table, 3-D q."""
