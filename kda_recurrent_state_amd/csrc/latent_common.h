@@ -84,6 +84,21 @@ __device__ __forceinline__ bf16x8 join(const s16x4& lo, const s16x4& hi) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The softmax weights are 2^fma(s, scale2, -base): base is a rounded product
+// (the maximum in use, s scale2 of some s), the fused operation's is not, and
+// their difference is the same factor of all weights.  It is at most 2^16 up to
+// |base| = kFar, but past the range of fp32 from 2^31 on, where the scores stand
+// that were masked by the type's lowest value.  Rows out there (the maximum is
+// finite) take their scores relative to the maximum, both products rounded, and
+// the base 0, so that the maximum's own weight is 1.
+constexpr float kFar = 268435456.f;  // 2^28: half a step is 16
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && m != -INFINITY; }
+__device__ __forceinline__ float from_far(float s, float scale2, float m) {
+#pragma clang fp contract(off)
+  const float x = s * scale2;
+  return (x - m) / scale2;
+}
+
 // The scheduler moves nothing across this.  By itself it puts each LDS read
 // right before the product that needs it and waits for it, so the product
 // loops read the next operands between two of these.

@@ -204,6 +204,7 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
   float m = -INFINITY, l = 0.f;  // in units of scale2 s
+  bool far = false;              // whether a query of the wave is_far
 
   // Staged rows: chunk c of a key or rotary row r lies at c ^ (r / (rows in 256
   // B)), of a value row at c ^ 4 (r & 3) (of 8 chunks: c ^ 4 ((r >> 1) & 1)).
@@ -333,15 +334,24 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
     // The maximum in use follows the true one only when that has grown by more
     // than 8 (a factor of 256): the weights stay far inside the range and the
     // output is seldom rescaled.
-    if (__any(mx > m + 8.f)) {
+    float base = m;
+    if (__any(mx > m + 8.f) || far) {
       const float mn = mx > m + 8.f ? mx : m;
       const float alpha = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
 #pragma unroll
       for (int i = 0; i < MT; ++i) acc[i] *= alpha;
       l *= alpha;
-      m = mn;
+      base = m = mn;
+      far = __any(is_far(m));
+      if (far && is_far(m)) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[b][i] = from_far(s[b][i], p.scale2, m);
+        base = 0.f;
+      }
     }
-    const float base = m == -INFINITY ? 0.f : m;
+    base = base == -INFINITY ? 0.f : base;
     // weights: bf16 for the matrix unit (the values' own type), their sum fp32
     bf16x8 pf[2][2];
 #pragma unroll

@@ -20,7 +20,21 @@ def attend(q, keys, values, sees, scale):
     return p @ v, lse, p @ v.abs()
 
 
-def prefill(q, k, v, k_rope, cu_q, cu_k, scale, causal):
+def attend_far(q, keys, values, sees, scale):
+    """As attend, for scores whose step in fp64 is above 1: lse is the maximum
+    there and exp(s - lse) no weight, so the maximum is subtracted and the
+    weights are divided by their sum."""
+    if sees.dim() == 1:
+        sees = torch.arange(keys.shape[0])[None, :] < sees[:, None]
+    s = ((q @ keys.T) * scale).masked_fill(~sees, -math.inf)
+    top = s.amax(-1)
+    p = torch.exp(s - torch.where(torch.isinf(top), 0.0, top)[:, None])
+    total = p.sum(-1)
+    p = p / total.clamp(min=1e-300)[:, None]
+    return p @ values, top + total.log(), p @ values.abs()
+
+
+def prefill(q, k, v, k_rope, cu_q, cu_k, scale, causal, attend=attend):
     T, H, _ = q.shape
     out = torch.zeros(T, H, v.shape[2], dtype=torch.float64)
     mag = torch.zeros_like(out)
@@ -43,7 +57,7 @@ def prefill(q, k, v, k_rope, cu_q, cu_k, scale, causal):
     return out, lse, mag
 
 
-def decode(cache, table, lengths, q, q_rope, scale):
+def decode(cache, table, lengths, q, q_rope, scale, attend=attend):
     """q [N, Q, H, L]"""
     N, Q, H, L = q.shape
     pages, page, _ = cache.shape

@@ -281,6 +281,37 @@ def test_prefill_keys_with_infinite_components(D, R, E, lq, past):
     _check_prefill(x, lq, lk, True, _prefill(x, lq, lk, True))
 
 
+@pytest.mark.parametrize("low", [torch.finfo(BF16).min, -1e30, 1e30])
+@pytest.mark.parametrize("lq,past,H", [([70, 5, 130], [0, 85, 3], 2)])
+def test_prefill_scores_of_the_types_range(lq, past, H, low):
+    """A mask of the type's lowest value as a score bias.  Where nothing but
+    such keys is seen, their scores are equal (the rest of the sum is below
+    half a step) and the output is the mean of their values."""
+    lk = [a + b for a, b in zip(lq, past)]
+    x = _prefill_inputs(lq, lk, H, 128, 64, 128)
+    gen = torch.Generator().manual_seed(32)
+    masked = torch.rand(sum(lk), generator=gen) < 0.5
+    masked[:40] = True
+    masked[-sum(lk) // 3:] = True
+    x["q"][..., 127] = 1
+    x["q"][:, 0, 127] = 0   # a head without the bias
+    x["k"][..., 127] = torch.where(masked, low, 0.0).to(BF16).cuda()[:, None]
+    if past[0]:
+        x["k"][..., 127] = low   # all of them
+    out, lse = _prefill(x, lq, lk, True)
+    want = ref.prefill(x["q"], x["k"], x["v"], x["k_rope"], _cu(lq), _cu(lk), 192 ** -0.5, True, ref.attend_far)
+    ref.check(out, None, want, "range")
+    _check_lse_range(lse, want[1])
+
+
+def _check_lse_range(lse, want):
+    """Near scores of 1e30 and more lse is held relatively: the factor to base 2
+    and back is rounded six times (the scale, its product with log2 e, log2 e,
+    the score's product, ln 2 and its product), each by 2^-24 at most."""
+    got = lse.cpu().double().reshape(want.shape)
+    assert ((got - want).abs() <= torch.where(want.abs() < 1e6, torch.full_like(want, 1e-4), want.abs() * 2.0 ** -21)).all()
+
+
 def test_prefill_many_sequences():
     # more sequences than one scan step of a wave, most of them tiny
     lq = [(7 * i) % 5 for i in range(150)] + [140, 1]
