@@ -395,6 +395,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   int begin = cur.t;
 
   float m = -INFINITY, l = 0.f;  // of row ln of the wave's block, over its tokens; units of scale2 s
+  bool far = false;              // whether one of the wave's rows is_far
   f32x4 acc[MT][NB];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -425,8 +426,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       f32x4 s[TB];
       // Weights of the scores against the maximum in use, for the matrix unit
       // in bf16, the values' own type; their sum stays in fp32.
-      auto weigh = [&]() {
-        const float base = m == -INFINITY ? 0.f : m;
+      auto weigh = [&](float base) {
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < TB; ++j) {
@@ -467,11 +467,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         // The maximum in use follows the true one only when that is larger by
         // more than 8 (a factor of 256): the weights stay far inside the range,
         // and most tiles need neither an exchange of maxima between the waves
-        // nor a rescaling of the output.
-        if (__any(mx > m + 8.f)) {
+        // nor a rescaling of the output.  (Rows that are far go the same way.)
+        if (__any(mx > m + 8.f) || far) {
           if (lane == 0) grown[par] = 1;
         }
-        weigh();
+        weigh(m == -INFINITY ? 0.f : m);
       }
       lds_barrier();
       if (grown[par]) {
@@ -485,7 +485,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
           if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
         }
         lds_barrier();  // (all have read the maxima; the weights are written again)
-        if (scoring) weigh();
+        if (scoring) {
+          float base = m == -INFINITY ? 0.f : m;
+          far = __any(is_far(m));
+          if (far && is_far(m)) {
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[j][i] = from_far(s[j][i], p.scale2, m);
+            base = 0.f;
+          }
+          weigh(base);
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           const float f = sfac[j * 16 + ln];
@@ -556,6 +567,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       wait_loads<0>();  // the queries are there, and no load to LDS outlives the workgroup
       if (!more) return;
       m = -INFINITY;
+      far = false;
       l = 0.f;
       begin = next.t;
     }

@@ -446,6 +446,25 @@ def test_decode_latents_with_infinite_components(L, R):
     ref.check(out[..., :L - 1], lse, [want[0][..., :L - 1], want[1], want[2][..., :L - 1]], "latent bias")
 
 
+@pytest.mark.parametrize("low", [torch.finfo(BF16).min, -1e30, 1e30])
+@pytest.mark.parametrize("Q,H", [(1, 3), (2, 32)])
+@pytest.mark.parametrize("lens", [[64, 40, 9, 17]])
+def test_decode_scores_of_the_types_range(lens, Q, H, low):
+    """As test_prefill_scores_of_the_types_range: rows masked by the type's
+    lowest value, all of a sequence's or some."""
+    x = _decode_inputs(lens, Q, H, 512, 64, 16)
+    gen = torch.Generator().manual_seed(35)
+    x["q_rope"][..., 63] = 1
+    x["q_rope"][:, :, 0, 63] = 0   # a head without the bias
+    x["cache"][..., 575] = torch.where(torch.rand(x["cache"].shape[:2], generator=gen) < 0.5, low, 0.0).to(BF16)
+    for n in (0, 3):
+        x["cache"][x["table"][n, :-(-lens[n] // 16)].long(), :, 575] = low
+    out, lse = _decode(x)
+    want = ref.decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], 0.07, ref.attend_far)
+    ref.check(out, None, want, "range")
+    _check_lse_range(lse, want[1])
+
+
 def test_decode_strides():
     """q as the transposed result of a product by head, q_rope as the end of a
     joint projection, pages with a gap, rows of a wider table, 3-D q."""
