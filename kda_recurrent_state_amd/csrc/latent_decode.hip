@@ -32,7 +32,8 @@
 // share of that line, whatever the lengths are.  A share may end one
 // sequence, hold several and begin another.  A piece that is a whole sequence
 // is written as output; the others go to the workspace as normalised fp32
-// outputs with their log-sum, and the join kernel weighs them.  Both kernels
+// outputs with their maximum and sum (one number for both would lose the sum of
+// scores that are large), and the join kernel weighs them.  Both kernels
 // derive the shares from the lengths on the device, so a captured call
 // follows its lengths.
 #include "internal.h"
@@ -66,7 +67,7 @@ struct DecodeParams {
   int N, Q, H, rows, row_blocks, groups;
   float scale2;    // scale log2 e
   float* part;     // [row_blocks][2 groups][MB][L] normalised outputs
-  float* plse;     // [row_blocks][2 groups][MB] log2 of the sums
+  float2* psum;    // [row_blocks][2 groups][MB] the maxima and the sums against them
   int32_t* shared; // [N][2] first and last share of a sequence
 };
 
@@ -558,11 +559,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         float sum = smax[0][r];
 #pragma unroll
         for (int g = 1; g < TG; ++g) sum += smax[g][r];
-        const float lse2 = sum == 0.f ? -INFINITY : sfac[r] + __log2f(sum);
         if (!whole)
-          p.plse[(int64_t)slot * MB + r] = lse2;
+          p.psum[(int64_t)slot * MB + r] = make_float2(sfac[r], sum);
         else if (p.lse)
-          p.lse[(int64_t)n * p.rows + rb * MB + r] = lse2 * kLn2;
+          p.lse[(int64_t)n * p.rows + rb * MB + r] = sum == 0.f ? -INFINITY : (sfac[r] + __log2f(sum)) * kLn2;
       }
       wait_loads<0>();  // the queries are there, and no load to LDS outlives the workgroup
       if (!more) return;
@@ -605,16 +605,19 @@ __global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, i
   f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   if (have) {
     for (int first = w0 + part; first <= w1; first += 4 * parts) {
-      float e[4];
+      float e[4], l[4];
       f32x4 x[4][2];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int w = first + u * parts;
         e[u] = -INFINITY;
+        l[u] = 0.f;
         x[u][0] = x[u][1] = f32x4{0, 0, 0, 0};
         if (w > w1) continue;
         const int64_t s = slot(w);
-        e[u] = p.plse[s];
+        const float2 ml = p.psum[s];
+        e[u] = ml.x;
+        l[u] = ml.y;
         if (c < p.L) {
           x[u][0] = *reinterpret_cast<const f32x4*>(p.part + s * p.L + c);
           x[u][1] = *reinterpret_cast<const f32x4*>(p.part + s * p.L + c + 4);
@@ -629,7 +632,7 @@ __global__ __launch_bounds__(kThreads) void latent_join_kernel(DecodeParams p, i
       o[1] *= old;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float f = exp2_hw(e[u] - base);
+        const float f = exp2_hw(e[u] - base) * l[u];
         sum += f;
         o[0] += f * x[u][0];
         o[1] += f * x[u][1];
@@ -717,7 +720,7 @@ hipError_t launch_r(const DecodeParams& p, int nb, hipStream_t stream) {
 }  // namespace
 
 size_t latent_decode_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L) {
-  return (size_t)(part_rows(decode_shape(Q, H)) * (L + 1) + 2 * N) * 4;
+  return (size_t)(part_rows(decode_shape(Q, H)) * (L + 2) + 2 * N) * 4;
 }
 
 hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t stream) {
@@ -755,8 +758,8 @@ hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t s
   p.groups = s.groups;
   p.scale2 = a.scale * kLog2e;
   p.part = static_cast<float*>(a.workspace);
-  p.plse = p.part + part_rows(s) * a.L;
-  p.shared = reinterpret_cast<int32_t*>(p.plse + part_rows(s));
+  p.psum = reinterpret_cast<float2*>(p.part + part_rows(s) * a.L);
+  p.shared = reinterpret_cast<int32_t*>(p.psum + part_rows(s));
   hipError_t e = a.L <= 128 ? launch_r<128>(p, s.nb, stream)
                             : (a.L <= 256 ? launch_r<256>(p, s.nb, stream) : launch_r<512>(p, s.nb, stream));
   if (e != hipSuccess) return e;

@@ -448,10 +448,11 @@ def test_decode_latents_with_infinite_components(L, R):
 
 @pytest.mark.parametrize("low", [torch.finfo(BF16).min, -1e30, 1e30])
 @pytest.mark.parametrize("Q,H", [(1, 3), (2, 32)])
-@pytest.mark.parametrize("lens", [[64, 40, 9, 17]])
+@pytest.mark.parametrize("lens", [[64, 40, 9, 17], [130, 300, 70, 2000]])
 def test_decode_scores_of_the_types_range(lens, Q, H, low):
     """As test_prefill_scores_of_the_types_range: rows masked by the type's
-    lowest value, all of a sequence's or some."""
+    lowest value, all of a sequence's or some; longer sequences are in pieces of
+    unequal length."""
     x = _decode_inputs(lens, Q, H, 512, 64, 16)
     gen = torch.Generator().manual_seed(35)
     x["q_rope"][..., 63] = 1
