@@ -48,7 +48,7 @@ struct PrefillParams {
   int splits;      // pieces the keys of a query tile are cut into at most
   float scale2;    // scale log2 e
   float* part;     // [splits][T][H][E] normalised outputs of pieces
-  float* plse;     // [splits][T][H] log2 of their sums
+  float2* psum;    // [splits][T][H] their maxima and the sums against them
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
@@ -394,7 +394,6 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   if (qi >= lq) return;
   const int64_t row = (q0 + qi) * p.H + h;
-  const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
   if (per_piece >= ntiles) {  // all of the keys
     __bf16* op = p.out + row * p.E;
 #pragma unroll
@@ -407,7 +406,7 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
                           (__bf16)(acc[i][4 * g + 2] * inv), (__bf16)(acc[i][4 * g + 3] * inv)};
         *reinterpret_cast<bf16x4*>(op + col) = o;
       }
-    if (p.lse && lh == 0) p.lse[row] = lse2 * kLn2;
+    if (p.lse && lh == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   } else {
     const int64_t slot = piece * p.T * p.H + row;
     float* op = p.part + slot * p.E;
@@ -420,7 +419,7 @@ __global__ __launch_bounds__(kQueries * 2, 2) void latent_prefill_kernel(Prefill
         *reinterpret_cast<f32x4*>(op + col) = f32x4{acc[i][4 * g] * inv, acc[i][4 * g + 1] * inv,
                                                     acc[i][4 * g + 2] * inv, acc[i][4 * g + 3] * inv};
       }
-    if (lh == 0) p.plse[slot] = lse2;
+    if (lh == 0) p.psum[slot] = make_float2(m, l);
   }
 }
 
@@ -441,12 +440,13 @@ __global__ __launch_bounds__(256) void latent_pieces_kernel(PrefillParams p) {
   const int64_t row = (tile.q0 + i) * p.H + h;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < pieces; ++s) top = fmaxf(top, p.plse[s * step + row]);
+  for (int s = 0; s < pieces; ++s) top = fmaxf(top, p.psum[s * step + row].x);
   const float base = top == -INFINITY ? 0.f : top;
   f32x4 o = {0, 0, 0, 0};
 #pragma unroll 4
   for (int s = 0; s < pieces; ++s) {
-    const float f = exp2_hw(p.plse[s * step + row] - base);
+    const float2 ml = p.psum[s * step + row];
+    const float f = exp2_hw(ml.x - base) * ml.y;
     sum += f;
     if (c < p.E) o += f * *reinterpret_cast<const f32x4*>(p.part + (s * step + row) * p.E + c);
   }
@@ -495,7 +495,7 @@ hipError_t launch_r(const PrefillParams& p, hipStream_t stream) {
 size_t latent_prefill_workspace_bytes(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E) {
   int64_t tiles, splits;
   prefill_shape(T, S, N, H, &tiles, &splits);
-  return splits == 1 ? 0 : (size_t)(splits * T * H * (E + 1)) * 4;
+  return splits == 1 ? 0 : (size_t)(splits * T * H * (E + 2)) * 4;
 }
 
 hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t stream) {
@@ -528,7 +528,7 @@ hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t
   p.tiles = (int)tiles;
   p.splits = (int)splits;
   p.part = static_cast<float*>(a.workspace);
-  p.plse = splits > 1 ? p.part + splits * a.T * a.H * a.E : nullptr;
+  p.psum = splits > 1 ? reinterpret_cast<float2*>(p.part + splits * a.T * a.H * a.E) : nullptr;
   // (8 x 2048 tokens, 16 heads of 64: 117 us, padded to 128 columns 167)
   return a.D <= 64 && a.E <= 64 ? launch_r<64, 64>(p, stream) : launch_r<128, 128>(p, stream);
 }

@@ -282,7 +282,7 @@ def test_prefill_keys_with_infinite_components(D, R, E, lq, past):
 
 
 @pytest.mark.parametrize("low", [torch.finfo(BF16).min, -1e30, 1e30])
-@pytest.mark.parametrize("lq,past,H", [([70, 5, 130], [0, 85, 3], 2)])
+@pytest.mark.parametrize("lq,past,H", [([70, 5, 130], [0, 85, 3], 2), ([40], [1200], 3)])
 def test_prefill_scores_of_the_types_range(lq, past, H, low):
     """A mask of the type's lowest value as a score bias.  Where nothing but
     such keys is seen, their scores are equal (the rest of the sum is below
