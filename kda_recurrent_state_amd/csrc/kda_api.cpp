@@ -320,6 +320,10 @@ bool outer_span(const int64_t* size, const int64_t* stride, int n, int64_t last,
   return true;
 }
 
+// Tokens of a packed batch of latent attention: the kernel counts in 31 bits to
+// the end of the last tile (of 128 queries, of 64 keys).
+constexpr int64_t kMostTokens = 0x7fffff00;
+
 bool dim8(int64_t x, int64_t lo, int64_t hi) { return x >= lo && x <= hi && x % 8 == 0; }
 
 kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
@@ -329,7 +333,7 @@ kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
   if (a->dtype != KDA_BF16) return KDA_E_DTYPE;
   if (!dim8(a->D, 8, 128) || !dim8(a->R, 0, 64) || !dim8(a->E, 8, 128)) return KDA_E_UNSUPPORTED;
   if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
-  if (a->T > 0x7fffffff || a->S > 0x7fffffff || a->N > 0x7fffffff || a->H > 65535) return KDA_E_UNSUPPORTED;
+  if (a->T > kMostTokens || a->S > kMostTokens || a->N > kMostTokens || a->H > 65535) return KDA_E_UNSUPPORTED;
   // one workgroup for each 32 queries of a head at least: the grid stays in 31 bits
   if ((a->T / 32 + a->N + 1) > (int64_t)0x7fffff00 / a->H) return KDA_E_UNSUPPORTED;
   if (a->T == 0 || a->N == 0) return KDA_OK;
@@ -452,8 +456,8 @@ bool stores_alias(const kda_page_store_t* s, int64_t n, int64_t num_pages, const
 extern "C" {
 
 size_t kda_latent_prefill_workspace_size(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E) {
-  if (T <= 0 || S < 0 || N <= 0 || H <= 0 || E <= 0 || T > 0x7fffffff || S > 0x7fffffff || N > 0x7fffffff ||
-      H > 65536 || E > 128)
+  if (T <= 0 || S < 0 || N <= 0 || H <= 0 || E <= 0 || T > kMostTokens || S > kMostTokens || N > kMostTokens ||
+      H > 65535 || E > 128)
     return 0;
   return kda::latent_prefill_workspace_bytes(T, S, N, H, E);
 }
