@@ -371,7 +371,8 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  * device pointers; every tensor's last dim is dense and its other dims have
  * the element strides given.
  *  T, S, N, H      -- query tokens, key tokens, sequences, heads (T, S and N at
- *                     most 2^31 - 256, H at most 65535).
+ *                     most 2^31 - 256, H at most 65535, and fewer than 2^24
+ *                     workgroups, of which a head has (T + 127 N) / 128).
  *  D, R, E         -- key dim per head (8..128), rotary key dim shared by the
  *                     heads (0..64), value dim (8..128); multiples of 8.
  *  dtype           -- of q, k, k_rope, v and out: KDA_BF16.

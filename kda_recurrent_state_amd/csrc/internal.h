@@ -38,6 +38,7 @@ hipError_t noalloc_scratch(void** ptr);
 
 // Latent attention; arguments already validated.
 hipError_t launch_latent_prefill(const kda_latent_prefill_args_t& a, hipStream_t stream);
+int64_t latent_prefill_workgroups(int64_t T, int64_t S, int64_t N, int64_t H);
 size_t latent_prefill_workspace_bytes(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E);
 hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t stream);
 size_t latent_decode_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L);

@@ -334,8 +334,8 @@ kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
   if (!dim8(a->D, 8, 128) || !dim8(a->R, 0, 64) || !dim8(a->E, 8, 128)) return KDA_E_UNSUPPORTED;
   if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
   if (a->T > kMostTokens || a->S > kMostTokens || a->N > kMostTokens || a->H > 65535) return KDA_E_UNSUPPORTED;
-  // one workgroup for each 32 queries of a head at least: the grid stays in 31 bits
-  if ((a->T / 32 + a->N + 1) > (int64_t)0x7fffff00 / a->H) return KDA_E_UNSUPPORTED;
+  // (HIP launches fewer than 2^32 threads a grid dimension; a workgroup has 256)
+  if (a->N > 0 && kda::latent_prefill_workgroups(a->T, a->S, a->N, a->H) >= (int64_t)1 << 24) return KDA_E_UNSUPPORTED;
   if (a->T == 0 || a->N == 0) return KDA_OK;
   if (!a->q || !a->cu_seqlens_q || !a->cu_seqlens_k || !a->out) return KDA_E_NULL;
   if (a->S > 0 && (!a->k || !a->v || (a->R > 0 && !a->k_rope))) return KDA_E_NULL;

@@ -473,9 +473,11 @@ void prefill_shape(int64_t T, int64_t S, int64_t N, int64_t H, int64_t* tiles, i
   *splits = s < 1 ? 1 : s;
 }
 
+int64_t workgroups(int64_t tiles, int64_t splits, int64_t H) { return (tiles * H + 7) / 8 * 8 * splits; }
+
 template <int DP, int RP, int EP>
 hipError_t launch(const PrefillParams& p, hipStream_t stream) {
-  const int64_t blocks = ((int64_t)p.tiles * p.H + 7) / 8 * 8 * p.splits;
+  const int64_t blocks = workgroups(p.tiles, p.splits, p.H);
   hipLaunchKernelGGL((latent_prefill_kernel<DP, RP, EP>), dim3((unsigned)blocks), dim3(kQueries * 2), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -491,6 +493,12 @@ hipError_t launch_r(const PrefillParams& p, hipStream_t stream) {
 }
 
 }  // namespace
+
+int64_t latent_prefill_workgroups(int64_t T, int64_t S, int64_t N, int64_t H) {
+  int64_t tiles, splits;
+  prefill_shape(T, S, N, H, &tiles, &splits);
+  return workgroups(tiles, splits, H);
+}
 
 size_t latent_prefill_workspace_bytes(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E) {
   int64_t tiles, splits;

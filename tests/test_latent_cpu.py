@@ -45,6 +45,7 @@ def _prefill(**kw):
     (dict(D=12), UNSUPPORTED), (dict(D=136), UNSUPPORTED), (dict(R=4), UNSUPPORTED), (dict(R=72), UNSUPPORTED),
     (dict(E=20), UNSUPPORTED), (dict(E=136), UNSUPPORTED), (dict(H=65536), UNSUPPORTED),
     (dict(T=1 << 31), UNSUPPORTED), (dict(T=1 << 30, H=65535), UNSUPPORTED),
+    (dict(T=131072, N=131072, H=128, q_stride=(128 * 24, 24)), UNSUPPORTED), (dict(T=1 << 17, N=65408, H=256), UNSUPPORTED),
     (dict(T=(1 << 31) - 1, H=1), UNSUPPORTED), (dict(S=(1 << 31) - 1), UNSUPPORTED), (dict(S=(1 << 31) - 255), UNSUPPORTED),
     (dict(scale=0.0), UNSUPPORTED), (dict(scale=-1.0), UNSUPPORTED), (dict(scale=math.inf), UNSUPPORTED),
     (dict(scale=math.nan), UNSUPPORTED),
