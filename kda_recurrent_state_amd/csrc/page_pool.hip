@@ -24,6 +24,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxStores = 32;  // stores a copying launch takes
+// Workgroups for the sequence slots of a launch: one each up to here, beyond it
+// each takes several (HIP launches fewer than 2^32 threads a grid dimension).
+constexpr int64_t kMostTables = 1 << 20;
 
 struct Pool {
   int32_t* table;
@@ -386,24 +389,25 @@ __global__ __launch_bounds__(kPlanThreads) void compact_plan_kernel(Pool p, Comp
   }
 }
 
-// Blocks [0, tables): one sequence slot's table row each and a part of the
-// reference counts (``tables`` is 0 in a call's later launches); the others
+// Blocks [0, tables): every tables-th sequence slot's table row and a part of
+// the reference counts (``tables`` is 0 in a call's later launches); the others
 // copy pages.
 template <typename VecT>
 __global__ __launch_bounds__(kThreads) void compact_apply_kernel(Pool p, int64_t tables, CompactPlan w, Stores st) {
   const int64_t moves = w.count[0], live = w.count[1];
   if ((int64_t)blockIdx.x < tables) {
-    const int64_t s = blockIdx.x;
-    int64_t used = used_pages(p.lengths[s], p.page_size);
-    if (used > p.max_pages) used = p.max_pages;
-    int32_t* row = p.table + s * p.table_stride;
-    for (int64_t j = threadIdx.x; j < used; j += kThreads) {
-      const int64_t pg = row[j];
-      if (pg < live || pg >= p.num_pages) continue;
-      const int k = w.rank[pg];
-      if (k >= 0) row[j] = w.to[k];
+    for (int64_t s = blockIdx.x; s < p.num_seqs; s += tables) {
+      int64_t used = used_pages(p.lengths[s], p.page_size);
+      if (used > p.max_pages) used = p.max_pages;
+      int32_t* row = p.table + s * p.table_stride;
+      for (int64_t j = threadIdx.x; j < used; j += kThreads) {
+        const int64_t pg = row[j];
+        if (pg < live || pg >= p.num_pages) continue;
+        const int k = w.rank[pg];
+        if (k >= 0) row[j] = w.to[k];
+      }
     }
-    for (int64_t k = s * kThreads + threadIdx.x; k < moves; k += tables * kThreads) {
+    for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < moves; k += tables * kThreads) {
       p.refs[w.to[k]] = p.refs[w.from[k]];
       p.refs[w.from[k]] = 0;
     }
@@ -422,18 +426,19 @@ __global__ __launch_bounds__(kThreads) void compact_apply_kernel(Pool p, int64_t
 // free
 
 __global__ __launch_bounds__(kThreads) void free_kernel(Pool p, const uint8_t* release) {
-  const int64_t s = blockIdx.x;
-  if (release[s] == 0) return;
-  int64_t used = used_pages(p.lengths[s], p.page_size);
-  if (used > p.max_pages) used = p.max_pages;
-  int32_t* row = p.table + s * p.table_stride;
-  for (int64_t j = threadIdx.x; j < used; j += kThreads) {
-    const int64_t pg = row[j];
-    if (pg >= 0 && pg < p.num_pages) atomicAdd(p.refs + pg, -1);  // whole numbers: the order does not matter
-    row[j] = -1;
+  for (int64_t s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+    if (release[s] == 0) continue;
+    int64_t used = used_pages(p.lengths[s], p.page_size);
+    if (used > p.max_pages) used = p.max_pages;
+    int32_t* row = p.table + s * p.table_stride;
+    for (int64_t j = threadIdx.x; j < used; j += kThreads) {
+      const int64_t pg = row[j];
+      if (pg >= 0 && pg < p.num_pages) atomicAdd(p.refs + pg, -1);  // whole numbers: the order does not matter
+      row[j] = -1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) p.lengths[s] = 0;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) p.lengths[s] = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -539,7 +544,7 @@ hipError_t launch_page_compact(const kda_page_pool_t& a, const kda_page_store_t*
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int width = width_of(stores, num_stores);
-  int64_t at = 0, tables = a.num_seqs;
+  int64_t at = 0, tables = a.num_seqs < kMostTables ? a.num_seqs : kMostTables;
   do {
     const Stores st = stores_of(stores, num_stores, at, width);
     const dim3 grid((unsigned)(tables + copy_blocks(a.num_pages / 2, st.per_page)));
@@ -559,7 +564,8 @@ hipError_t launch_page_compact(const kda_page_pool_t& a, const kda_page_store_t*
 }
 
 hipError_t launch_page_free(const kda_page_pool_t& a, const uint8_t* release, hipStream_t stream) {
-  hipLaunchKernelGGL(free_kernel, dim3((unsigned)a.num_seqs), dim3(kThreads), 0, stream, pool_of(a), release);
+  const int64_t blocks = a.num_seqs < kMostTables ? a.num_seqs : kMostTables;
+  hipLaunchKernelGGL(free_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, pool_of(a), release);
   return hipGetLastError();
 }
 

@@ -244,6 +244,35 @@ def test_free(seqs, per, pages, page, live, dtype):
     assert torch.equal(dt.cpu(), t) and torch.equal(dr.cpu(), r)
 
 
+@pytest.mark.parametrize("seqs", [1 << 24, (1 << 24) - 4000, (1 << 20) + 300])
+def test_compact_and_free_of_very_many_slots(seqs):
+    """More slots than a launch has workgroups for (2^24 is the most a pool may
+    have); those in use lie at both ends and between."""
+    import kda_recurrent_state_amd as kda
+    pages = 700
+    gen = torch.Generator().manual_seed(13)
+    slots = torch.tensor([0, 1, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, seqs // 2, seqs - 2, seqs - 1]).unique()
+    perm = torch.randperm(pages, generator=gen)[:2 * len(slots)].int().view(-1, 2)
+    table = torch.full((seqs, 2), -1, dtype=torch.int32, device="cuda")
+    table[slots.cuda()] = perm.cuda()
+    lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+    lens[slots.cuda()] = 2
+    refs = torch.bincount(perm.view(-1).long(), minlength=pages).int().cuda()
+    cache = torch.arange(pages, dtype=torch.int32)[:, None].repeat(1, 5).cuda()
+    small = perm.clone(), _i32([2] * len(slots)), refs.cpu()
+    live = kda.kda_page_compact(table, lens, refs, 1, caches=[cache])
+    t, r, c, n = ref.compact(*small, 1, [torch.arange(pages, dtype=torch.int32)[:, None].repeat(1, 5)])
+    assert live.item() == n and torch.equal(table[slots.cuda()].cpu(), t) and torch.equal(refs.cpu(), r)
+    assert torch.equal(cache.cpu(), c[0])
+    release = torch.zeros(seqs, dtype=torch.bool, device="cuda")
+    release[slots[1:].cuda()] = True
+    kda.kda_page_free(table, lens, refs, release, 1)
+    assert lens.sum().item() == 2 and lens[0].item() == 2 and int((table >= 0).sum()) == 2
+    want = torch.zeros(pages, dtype=torch.int32)
+    want[t[0].long()] = 1
+    assert torch.equal(refs.cpu(), want)
+
+
 def test_pool_in_rows_of_a_wider_table_on_a_side_stream():
     import kda_recurrent_state_amd as kda
     pool = _pool(10, 20, 6, 200, 4, 10)
