@@ -392,7 +392,7 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  *                     query belongs to two sequences).
  *  out             -- [T, H, E] contiguous, 8-byte aligned.
  *  lse             -- [T, H] fp32, or NULL.
- *  scale           -- factor of the scores, positive and finite.
+ *  scale           -- factor of the scores, positive, at most 2^127.
  *  causal          -- nonzero: query i of a sequence with Lq queries and Lk
  *                     keys sees keys j < Lk - (Lq - 1 - i), so its queries are
  *                     the last Lq of Lk positions; zero: it sees all Lk keys.
@@ -467,7 +467,7 @@ kda_status_t kda_latent_prefill(const kda_latent_prefill_args_t* args, void* str
  *                     aligned; q_rope NULL with R == 0.
  *  out             -- [N, Q, H, L] contiguous, 16-byte aligned.
  *  lse             -- [N, Q, H] fp32, or NULL.
- *  scale           -- factor of the scores, positive and finite.
+ *  scale           -- factor of the scores, positive, at most 2^127.
  *  workspace       -- device scratch, 16-byte aligned, of at least
  *                     kda_latent_decode_workspace_size(N, Q, H, L) bytes.
  * Query i of sequence n sees the rows j < lengths[n] - (Q - 1 - i):

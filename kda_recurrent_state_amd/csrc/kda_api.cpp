@@ -320,6 +320,9 @@ bool outer_span(const int64_t* size, const int64_t* stride, int n, int64_t last,
   return true;
 }
 
+// Factor of the scores: its product with log2 e is finite.
+constexpr float kMostScale = 0x1p127f;
+
 // Tokens of a packed batch of latent attention: the kernel counts in 31 bits to
 // the end of the last tile (of 128 queries, of 64 keys).
 constexpr int64_t kMostTokens = 0x7fffff00;
@@ -332,7 +335,7 @@ kda_status_t check_latent_prefill(const kda_latent_prefill_args_t* a) {
   if (a->N == 0 && a->T != 0) return KDA_E_SHAPE;
   if (a->dtype != KDA_BF16) return KDA_E_DTYPE;
   if (!dim8(a->D, 8, 128) || !dim8(a->R, 0, 64) || !dim8(a->E, 8, 128)) return KDA_E_UNSUPPORTED;
-  if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
+  if (!(a->scale > 0.f && a->scale <= kMostScale)) return KDA_E_UNSUPPORTED;
   if (a->T > kMostTokens || a->S > kMostTokens || a->N > kMostTokens || a->H > 65535) return KDA_E_UNSUPPORTED;
   // (HIP launches fewer than 2^32 threads a grid dimension; a workgroup has 256)
   if (a->N > 0 && kda::latent_prefill_workgroups(a->T, a->S, a->N, a->H) >= (int64_t)1 << 24) return KDA_E_UNSUPPORTED;
@@ -376,7 +379,7 @@ kda_status_t check_latent_decode(const kda_latent_decode_args_t* a) {
   if (!dim8(a->L, 8, 512) || !dim8(a->R, 0, 64)) return KDA_E_UNSUPPORTED;
   if (a->Q > 1024 || a->H > 1024 || a->Q * a->H > 1024) return KDA_E_UNSUPPORTED;
   if (a->N > 65535) return KDA_E_UNSUPPORTED;  // sequences are a grid dimension
-  if (!(a->scale > 0.f) || isinf(a->scale)) return KDA_E_UNSUPPORTED;
+  if (!(a->scale > 0.f && a->scale <= kMostScale)) return KDA_E_UNSUPPORTED;
   const int64_t most = (int64_t)1 << 30, row = a->L + a->R;
   if (a->page_size > most || a->max_pages > most / a->page_size || a->num_pages > 0x7fffffff) return KDA_E_UNSUPPORTED;
   // (a workgroup's tiles are counted in 31 bits)

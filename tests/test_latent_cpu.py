@@ -48,7 +48,7 @@ def _prefill(**kw):
     (dict(T=131072, N=131072, H=128, q_stride=(128 * 24, 24)), UNSUPPORTED), (dict(T=1 << 17, N=65408, H=256), UNSUPPORTED),
     (dict(T=(1 << 31) - 1, H=1), UNSUPPORTED), (dict(S=(1 << 31) - 1), UNSUPPORTED), (dict(S=(1 << 31) - 255), UNSUPPORTED),
     (dict(scale=0.0), UNSUPPORTED), (dict(scale=-1.0), UNSUPPORTED), (dict(scale=math.inf), UNSUPPORTED),
-    (dict(scale=math.nan), UNSUPPORTED),
+    (dict(scale=math.nan), UNSUPPORTED), (dict(scale=3e38), UNSUPPORTED),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(k_rope=None), NULL), (dict(out=None), NULL),
     (dict(cu_seqlens_q=None), NULL), (dict(cu_seqlens_k=None), NULL),
     (dict(q_stride=(44, 24)), LAYOUT), (dict(q_stride=(48, -24)), LAYOUT), (dict(k_stride=(33, 16)), LAYOUT),
@@ -95,7 +95,8 @@ def _decode(lib, **kw):
     (dict(num_pages=0), SHAPE), (dict(page_size=0), SHAPE), (dict(max_pages=0), SHAPE), (dict(dtype=0), DTYPE),
     (dict(L=60), UNSUPPORTED), (dict(L=520), UNSUPPORTED), (dict(R=12), UNSUPPORTED), (dict(R=72), UNSUPPORTED),
     (dict(Q=1025, H=1), UNSUPPORTED), (dict(Q=33, H=32), UNSUPPORTED), (dict(N=65536), UNSUPPORTED),
-    (dict(scale=0.0), UNSUPPORTED), (dict(scale=math.nan), UNSUPPORTED),
+    (dict(scale=0.0), UNSUPPORTED), (dict(scale=math.nan), UNSUPPORTED), (dict(scale=3e38), UNSUPPORTED),
+    (dict(scale=math.inf), UNSUPPORTED),
     (dict(max_pages=1 << 27, table_stride=1 << 27), UNSUPPORTED), (dict(page_size=1 << 31), UNSUPPORTED),
     (dict(N=65535, max_pages=1 << 21, table_stride=1 << 21), UNSUPPORTED),
     (dict(table_stride=3), OVERLAP), (dict(page_stride=16 * 80 - 8), OVERLAP), (dict(page_stride=16 * 80 + 4), LAYOUT),
