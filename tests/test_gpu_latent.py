@@ -383,6 +383,35 @@ def test_decode_long_context_is_split():
     _check_decode(x, _decode(x, scale=0.3), scale=0.3)
 
 
+RAGGED = [700, 0, 63, 129, 2000, 1, 320, 64, 65, 0, 0, 1500, 128, 3, 900]
+
+
+@pytest.mark.parametrize("lens,Q,H,L,R,page", [
+    (RAGGED, 4, 256, 512, 64, 16),            # 16 row blocks and shares: 5 to 6 tiles a share
+    (RAGGED * 2, 1, 1000, 256, 32, 48),       # 16 shares
+    (RAGGED * 6, 1, 128, 512, 64, 64),        # two row blocks, 128 shares
+    (RAGGED * 12, 2, 32, 512, 64, 64),        # 64 query rows, 256 shares, 4 tiles a share
+    (RAGGED * 12, 1, 20, 504, 56, 33),        # 32 rows
+    (RAGGED * 12, 1, 32, 512, 0, 128),
+    (RAGGED * 16, 1, 7, 128, 64, 1),          # 16 rows
+    (RAGGED * 16, 3, 3, 512, 64, 7),
+    ([0, 20000, 0, 1] + [70] * 130 + [9000], 1, 5, 136, 8, 16)])
+@pytest.mark.parametrize("grow", [0, 4])
+def test_decode_many_tiles_a_share(lens, Q, H, L, R, page, grow):
+    """Shares of several tiles, which end one sequence, hold others (empty ones
+    among them) and begin another.  With ``grow`` a sequence's rows get larger
+    to its end, so that the maxima grow by far more than 2^8 on the way: scores
+    of up to about 400 before the scale of 0.07, whose fp32 rounding (576
+    products, 24 x 2^-24 x 400 x 0.07 = 4e-5) the bound of lse holds."""
+    x = _decode_inputs(lens, Q, H, L, R, page)
+    if grow:
+        for n, k in enumerate(lens):
+            pages = x["table"][n, :-(-k // page)].long()
+            f = torch.linspace(0, grow, pages.shape[0] * page, device="cuda").view(-1, page, 1)
+            x["cache"][pages] = (x["cache"][pages].float() * f * (576 / (L + R)) ** 0.5).to(BF16)
+    _check_decode(x, _decode(x))
+
+
 def test_decode_queries_before_the_first_token():
     # three new tokens, lengths 0 .. 3: the first queries see nothing
     x = _decode_inputs([0, 1, 2, 3], 3, 4, 512, 64, 64)

@@ -142,6 +142,79 @@ def test_fork_of_an_empty_slot_that_becomes_a_child(entries, share):
     assert not status.any()
 
 
+@pytest.mark.parametrize("entries", [60, 200, 1500])
+@pytest.mark.parametrize("share", [True, False])
+def test_fork_refusals_among_many_entries(entries, share):
+    """Bad slots, full targets, repeated targets, parents with a bad or a free
+    page or a length no row holds, among more entries than one workgroup checks
+    and than one step of the plan sums; the pages run out before the end."""
+    pool = _pool(14, 1800, 6, 4000, 4, 200, shared=0.2)
+    table, lens, refs = pool
+    full = [s for s in range(1800) if lens[s] > 0]
+    empty = [s for s in range(1800) if lens[s] == 0]
+    table[full[5], 0] = 4000
+    refs[table[full[6], 0].long()] = 0
+    lens[full[7]] = 25
+    lens[full[8]] = -1
+    refs[refs == 0] = -(torch.arange(int((refs == 0).sum())).int() % 2)
+    gen = torch.Generator().manual_seed(entries)
+    src = [full[int(torch.randint(0, len(full), (1,), generator=gen))] for _ in range(entries)]
+    dst = empty[:entries]
+    for i, (s, d) in enumerate([(-1, empty[0]), (1800, empty[1]), (full[0], full[1]), (full[2], full[2]),
+                                (full[3], dst[0]), (full[5], dst[1]), (full[6], dst[2]), (full[7], dst[3]),
+                                (full[8], dst[4]), (full[9], -7), (full[9], 1 << 20), (full[10], dst[5])]):
+        for at in (10 + 3 * i, entries - 1 - 4 * i):
+            src[at], dst[at] = s, d
+    free = int((refs <= 0).sum())
+    keep = torch.randperm(4000, generator=gen)
+    taken = [p for p in keep.tolist() if refs[p] <= 0][:max(0, free - entries * (1 if share else 3) // 2)]
+    refs[taken] = 1     # about half of the entries find pages
+    s = _check_fork(pool, 4, src, dst, share, torch.int64 if share else torch.int32, [_caches(4000, 4)[0]])
+    assert all((s == k).any() for k in (0, 1, 2))
+    if entries > 1100 and not share:
+        assert (s[1024:] == 1).any()
+
+
+@pytest.mark.parametrize("entries", [5, 140])
+@pytest.mark.parametrize("share", [True, False])
+def test_fork_of_long_parents(entries, share):
+    """Parents of 70 to 600 pages; one has a page outside the pool behind the
+    64th, one a free page behind the 256th, one behind the 512th."""
+    pages = 4000 + entries * (1 if share else 600)
+    pool = _pool(15, 400, 600, pages, 2, 6, shared=0)
+    table, lens, refs = pool
+    full = [s for s in range(400) if lens[s] > 0]
+    empty = [s for s in range(400) if lens[s] == 0]
+    at = int(refs.sum())
+    spare = [p for p in range(pages) if refs[p] == 0]
+    for s, n in zip(empty[:5], (70, 129, 300, 513, 600)):
+        for j in range(n):
+            table[s, j] = spare.pop()
+        lens[s] = 2 * n - 1
+        refs[table[s, :n].long()] = 1
+    assert int(refs.sum()) == at + 70 + 129 + 300 + 513 + 600
+    parents = empty[:5]
+    table[parents[1], 100] = -1
+    refs[table[parents[2], 270].long()] = 0
+    refs[table[parents[3], 512].long()] = -2
+    src = [parents[(i + 4) % 5] for i in range(entries)]
+    s = _check_fork(pool, 2, src, empty[5:5 + entries], share, caches=[_caches(pages, 2)[0]])
+    assert s.tolist()[:5] == [0, 0, 2, 2, 2]
+
+
+@pytest.mark.parametrize("share", [True, False])
+def test_fork_runs_out_behind_entry_1024(share):
+    """The plan's sums are carried over its steps of 1024 entries."""
+    pool = _pool(16, 3200, 2, 2600, 4, 40, shared=0)
+    table, lens, refs = pool
+    full = [s for s in range(3200) if lens[s] == 5 or lens[s] == 6]
+    empty = [s for s in range(3200) if lens[s] == 0]
+    free = [p for p in range(2600) if refs[p] == 0]
+    refs[free[(1030 if share else 2060):]] = 1
+    s = _check_fork(pool, 4, [full[i % len(full)] for i in range(1300)], empty[:1300], share, caches=[_caches(2600, 4)[0]])
+    assert not s[:1030].any() and (s[1030:] == 1).all()
+
+
 def test_fork_of_state_rows_matches_gather_and_scatter():
     """Recurrent states (page size 1, one row a slot, rows with a gap): a fork
     without sharing equals gathering the parents' rows and scattering them."""
