@@ -402,10 +402,11 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  * For query i and head h of a sequence, over the keys j it sees:
  *   s_j = scale (q_i[:D] . k_j + q_i[D:] . k_rope_j)
  *   out_i = sum_j exp(s_j - lse_i) v_j,   lse_i = log sum_j exp(s_j)
- * A query that sees no key (or only keys whose score is -inf) gets out 0 and
- * lse -inf.  Rows of q that belong to no sequence have their out and lse rows
- * left as they were.
- * Precision: products of bf16 operands with fp32 sums; scores, the running
+ * A query that sees no key (or only keys whose score is -inf, as an infinite
+ * component of a key can make it) gets out 0 and lse -inf.  Rows of q that
+ * belong to no sequence have their out and lse rows left as they were.
+ * Precision: products of bf16 operands with fp32 sums; scores (and their
+ * products with log2 e, which count as infinite beyond fp32), the running
  * maximum and sum and the output accumulate in fp32; the softmax weights are
  * rounded to bf16 as operands of the second product.
  * A NaN or infinite value row v_j can reach queries that do not see key j but

@@ -6,7 +6,6 @@
 // synchronisation, no environment scan, no conversion of int32 indices; a bad
 // layout returns an error and enqueues nothing; an empty selection validates
 // the cache view and enqueues nothing.
-#include <math.h>
 #include <string.h>
 
 #include "internal.h"

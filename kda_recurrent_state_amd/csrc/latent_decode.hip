@@ -681,8 +681,10 @@ struct Shape {
 };
 
 // Query rows a workgroup (16, 32 or 64: 16 rows of 200 ragged sequences take 98
-// us in workgroups of 16 and 112 of 64) and shares of the line: one workgroup
-// fits a CU (LDS), 256 in all; the shares are a multiple of 8, one set an XCD.
+// us in workgroups of 16 and 112 of 64) and shares of the line: one workgroup a
+// CU, 256 in all; the shares are a multiple of 8, one set an XCD.  (At L = 512
+// the LDS holds no second one.  The builds for L <= 128, and for L <= 256
+// without rotary columns, would leave room for it; that was not measured.)
 Shape decode_shape(int64_t Q, int64_t H) {
   Shape s;
   const int64_t rows = Q * H;
