@@ -304,11 +304,32 @@ def test_prefill_scores_of_the_types_range(lq, past, H, low):
     _check_lse_range(lse, want[1])
 
 
+def test_prefill_scores_of_the_types_range_over_many_tiles():
+    """As above over several key tiles of a workgroup (no split): a mask over all
+    keys, or over the first half of them."""
+    import kda_recurrent_state_amd as kda
+    lq = lk = [1100, 900]
+    x = _prefill_inputs(lq, lk, 32, 64, 32, 64)
+    assert kda.kda_latent_prefill_workspace_size(2000, 2000, 2, 32, 64) == 0
+    x["q"][..., 95] = 1
+    x["q"][:, 0, 95] = 0
+    x["k_rope"][:, 31] = 0
+    x["k_rope"][:1100, 31] = torch.finfo(BF16).min
+    x["k_rope"][1100:1550, 31] = torch.finfo(BF16).min
+    out, lse = _prefill(x, lq, lk, True)
+    want = ref.prefill(x["q"], x["k"], x["v"], x["k_rope"], _cu(lq), _cu(lk), 96 ** -0.5, True, ref.attend_far)
+    ref.check(out, None, want, "range")
+    _check_lse_range(lse, want[1])
+
+
 def _check_lse_range(lse, want):
     """Near scores of 1e30 and more lse is held relatively: the factor to base 2
     and back is rounded six times (the scale, its product with log2 e, log2 e,
     the score's product, ln 2 and its product), each by 2^-24 at most."""
     got = lse.cpu().double().reshape(want.shape)
+    empty = want == -math.inf
+    assert torch.equal(got == -math.inf, empty)
+    got, want = got[~empty], want[~empty]
     assert ((got - want).abs() <= torch.where(want.abs() < 1e6, torch.full_like(want, 1e-4), want.abs() * 2.0 ** -21)).all()
 
 
@@ -489,6 +510,27 @@ def test_decode_scores_of_the_types_range(lens, Q, H, low):
     x["cache"][..., 575] = torch.where(torch.rand(x["cache"].shape[:2], generator=gen) < 0.5, low, 0.0).to(BF16)
     for n in (0, 3):
         x["cache"][x["table"][n, :-(-lens[n] // 16)].long(), :, 575] = low
+    out, lse = _decode(x)
+    want = ref.decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], 0.07, ref.attend_far)
+    ref.check(out, None, want, "range")
+    _check_lse_range(lse, want[1])
+
+
+@pytest.mark.parametrize("Q,H,L,R", [(4, 256, 512, 64), (1, 1000, 136, 24)])
+def test_decode_scores_of_the_types_range_over_many_tiles(Q, H, L, R):
+    """Rows masked by the type's lowest value over several tiles of a share: all
+    of every third sequence, the first half of the next, every other row of the
+    last."""
+    low = torch.finfo(BF16).min
+    x = _decode_inputs(RAGGED, Q, H, L, R, 16)
+    x["q_rope"][..., R - 1] = 1
+    x["q_rope"][:, :, 0, R - 1] = 0
+    x["cache"][..., L + R - 1] = 0
+    for n, k in enumerate(RAGGED):
+        pages = x["table"][n, :-(-k // 16)].long()
+        bias = torch.zeros(pages.shape[0] * 16)
+        bias[:[k, k // 2, k][n % 3]:[1, 1, 2][n % 3]] = low
+        x["cache"][pages, :, L + R - 1] = bias.view(-1, 16).to(BF16).cuda()
     out, lse = _decode(x)
     want = ref.decode(x["cache"], x["table"], x["lens"], x["q"], x["q_rope"], 0.07, ref.attend_far)
     ref.check(out, None, want, "range")
