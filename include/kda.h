@@ -16,7 +16,10 @@
  * same packed batch: kda_latent_prefill and kda_latent_decode are those
  * layers' attention, and kda_page_fork / kda_page_compact / kda_page_free keep
  * the pages of a latent cache (and the rows of a state cache) shared, dense
- * and reclaimed.
+ * and reclaimed.  kda_latent_quantize_scatter / kda_latent_dequantize_gather write
+ * and read a latent cache in 8 bits, kda_latent_decode_fp8 attends to it, and
+ * kda_latent_decode_shared computes a prefix that sequences share (as after a
+ * fork) once for all of them.
  *
  * Sources (web pages, cited by title and section):
  *  [P1] "vllm-ascend 的 KDA 状态复制 Triton 集成：PR 17301 对齐的预编译 worker
@@ -59,7 +62,7 @@
 extern "C" {
 #endif
 
-typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype_t;
+typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_E4M3 = 2 } kda_dtype_t; /* E4M3: codes of the 8-bit latent cache alone */
 typedef enum { KDA_I32 = 0, KDA_I64 = 1 } kda_index_t;
 
 typedef enum {
@@ -515,6 +518,141 @@ size_t kda_latent_decode_workspace_size(int64_t N, int64_t Q, int64_t H, int64_t
  * KDA_E_UNSUPPORTED, KDA_E_WORKSPACE, KDA_E_ALIAS, KDA_E_HIP.
  */
 kda_status_t kda_latent_decode(const kda_latent_decode_args_t* args, void* stream);
+
+/*
+ * An 8-bit latent cache: token rows in pages, a row as L e4m3 codes (1 sign, 4
+ * exponent and 3 mantissa bits, largest 448, no infinity) with one fp32 scale, and
+ * R rotary key components in bf16.  Its value is code * scale, and the rotary key.
+ *  codes   -- [num_pages, page_size, L] bytes, 16-byte aligned.
+ *  scales  -- [num_pages, page_size] fp32.
+ *  rope    -- [num_pages, page_size, R] bf16, 16-byte aligned (NULL with R == 0).
+ *             Pages are dense inside; from page to page lie codes_page_stride
+ *             bytes (a multiple of 16), scales_page_stride fp32 and
+ *             rope_page_stride bf16 (a multiple of 8).
+ *  num_pages, page_size -- positive, num_pages * page_size below 2^31.
+ *  L, R    -- latent dim (16..512, a multiple of 16), rotary key dim (0..64, a
+ *             multiple of 8).
+ * The three arrays are three stores for kda_page_fork and kda_page_compact.
+ */
+typedef struct {
+  void* codes;
+  float* scales;
+  void* rope;
+  int64_t num_pages, page_size, L, R;
+  int64_t codes_page_stride, scales_page_stride, rope_page_stride;
+} kda_latent_store_t;
+
+/*
+ * kda_latent_quantize_scatter -- for t in [0, num_rows): if 0 <= slots[t] <
+ * num_pages * page_size, token row slots[t] (page slots[t] / page_size, place
+ * slots[t] % page_size) receives row t:
+ *   scale = 2^e with the smallest e >= -126 for which max |c| <= 448 2^e,
+ *   code  = c / scale rounded to e4m3 (ties to even),
+ *   rope  = k_rope rounded to bf16 (ties to even).
+ * A row whose c holds an infinity or a NaN gets the scale NaN and codes 0: what
+ * reads it gets NaN, and nothing else does.  Other entries are skipped.
+ *  c       -- [num_rows, L], c_stride elements from row to row; k_rope
+ *             [num_rows, R] with k_rope_stride (NULL with R == 0); both in dtype
+ *             (KDA_F32 or KDA_BF16), dense last dim, 16-byte aligned, strides
+ *             multiples of 8 elements, not negative.
+ *  slots   -- [num_rows] int32 or int64; num_rows below 2^28.
+ * Preconditions (not checked): valid slots are unique.  Aliasing (checked,
+ * KDA_E_ALIAS): codes, scales and rope overlap neither each other nor c, k_rope or
+ * slots.  num_rows == 0 enqueues nothing.
+ * Errors: KDA_E_NULL, KDA_E_DTYPE, KDA_E_SHAPE, KDA_E_LAYOUT, KDA_E_OVERLAP,
+ * KDA_E_UNSUPPORTED, KDA_E_ALIAS, KDA_E_HIP.
+ */
+kda_status_t kda_latent_quantize_scatter(const kda_latent_store_t* store, const void* c, int64_t c_stride,
+                                         const void* k_rope, int64_t k_rope_stride, kda_dtype_t dtype,
+                                         const void* slots, kda_index_t index_type, int64_t num_rows, void* stream);
+
+/*
+ * kda_latent_dequantize_gather -- out[t] = the value of token row slots[t], its L
+ * latent components (code * scale in fp32, then rounded to dtype) and its R rotary
+ * ones, or zeros where slots[t] lies outside [0, num_pages * page_size).
+ *  out     -- [num_rows, L + R] in dtype (KDA_F32 or KDA_BF16), contiguous, 16-byte
+ *             aligned: the layout of a 16-bit latent cache's rows.
+ * Slots may repeat.  out overlaps neither the store nor slots (checked).
+ * num_rows == 0 enqueues nothing.  Errors as for kda_latent_quantize_scatter.
+ */
+kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const void* slots, kda_index_t index_type,
+                                          int64_t num_rows, void* out, kda_dtype_t dtype, void* stream);
+
+/*
+ * Arguments of kda_latent_decode_fp8 and kda_latent_decode_shared: those of
+ * kda_latent_decode with a cache in 16 or in 8 bits and with groups of
+ * sequences that share their first tokens.
+ *  cache_dtype     -- KDA_BF16: cache is [num_pages, page_size, L+R] bf16 and
+ *                     page_stride in elements, as for kda_latent_decode; scales
+ *                     and rope play no part.  KDA_E4M3: cache, scales and rope
+ *                     are the three arrays of a kda_latent_store_t, with
+ *                     page_stride (bytes), scales_page_stride and
+ *                     rope_page_stride, and L is a multiple of 16.
+ *  G               -- groups, 0 .. 65535 (0: no sharing).
+ *  cu_groups       -- [G+1] int32: group g is the sequences cu_groups[g] ..
+ *                     cu_groups[g+1] - 1.  Non-decreasing (not checked: the
+ *                     kernel clamps offsets to [0, N] and raises one to the largest
+ *                     before it).  Sequences of no group share nothing.
+ *  shared          -- [G] int32: the first shared[g] tokens of the group's
+ *                     sequences are the same rows.  They are read through the
+ *                     table of the group's first sequence, up to its length;
+ *                     the others' tables are read behind that.  Any number of
+ *                     tokens, whole pages or not; negative: 0.
+ *  The rest        -- as for kda_latent_decode, and N Q H times
+ *                     max_pages * page_size may not exceed 2^48.
+ *  workspace       -- device scratch, 16-byte aligned, of at least
+ *                     kda_latent_shared_workspace_size(N, Q, H, L, G) bytes.
+ * The result is that of kda_latent_decode, whose rules on lengths, pages, empty
+ * rows and order of workgroups hold.  With a shared prefix, query rows see the
+ * first rows through the first sequence's table: where that has no page, no sequence
+ * of the group sees the row.
+ * Precision: as kda_latent_decode.  In 8 bits the queries (bf16) enter the
+ * scores as sums of two e4m3 numbers times a power of two a row: exact but for
+ * what lies 2^-18 below the row's largest component.  The 8-bit products are summed in
+ * fp32 after an alignment in the matrix unit that keeps about 2^-13 of the largest product of 128.
+ * Codes must not be NaN (0x7f, 0xff): such a code can reach all queries of a tile of
+ * 64 tokens.  A NaN or infinite scale reaches the queries that see its row and no others.
+ * A query that holds an infinity or a NaN gets NaN.
+ */
+typedef struct {
+  int64_t N, Q, H, L, R, G;
+  kda_dtype_t cache_dtype;
+  const void* cache;
+  const float* scales;
+  const void* rope;
+  int64_t num_pages, page_size;
+  int64_t page_stride, scales_page_stride, rope_page_stride;
+  const int32_t* page_table;
+  int64_t table_stride, max_pages;
+  const int32_t* lengths;
+  const int32_t* cu_groups;
+  const int32_t* shared;
+  const void* q;
+  int64_t q_stride[3];
+  const void* q_rope;
+  int64_t q_rope_stride[3];
+  void* out;
+  float* lse;
+  float scale;
+  void* workspace;
+  size_t workspace_bytes;
+} kda_latent_shared_args_t;
+
+/* Bytes of device workspace kda_latent_decode_fp8 (G = 0) and
+ * kda_latent_decode_shared need for these sizes. */
+size_t kda_latent_shared_workspace_size(int64_t N, int64_t Q, int64_t H, int64_t L, int64_t G);
+
+/*
+ * kda_latent_decode_fp8 -- latent decode over an 8-bit cache: cache_dtype is
+ * KDA_E4M3 and G is 0.  kda_latent_decode_shared -- either cache, any G.
+ * Aliasing (checked, KDA_E_ALIAS): out, lse and the workspace overlap neither each
+ * other nor any input.  Calls that can run at the same time need workspaces of
+ * their own.  N == 0 enqueues nothing.  The calls can be captured: their work
+ * follows the lengths, the tables and the groups that each replay finds.
+ * Errors: as for kda_latent_decode.
+ */
+kda_status_t kda_latent_decode_fp8(const kda_latent_shared_args_t* args, void* stream);
+kda_status_t kda_latent_decode_shared(const kda_latent_shared_args_t* args, void* stream);
 
 /*
  * The bookkeeping of a cache's pages, all on the device: sequence slot s holds

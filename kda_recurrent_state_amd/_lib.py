@@ -7,7 +7,7 @@ import os
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libkda.so")
 
-KDA_F32, KDA_BF16 = 0, 1
+KDA_F32, KDA_BF16, KDA_E4M3 = 0, 1, 2
 KDA_I32, KDA_I64 = 0, 1
 KDA_OK = 0
 STATUS_NAMES = {0: "KDA_OK", 1: "KDA_E_NULL", 2: "KDA_E_DTYPE", 3: "KDA_E_SHAPE", 4: "KDA_E_LAYOUT",
@@ -18,6 +18,8 @@ EXPORTED = ("kda_state_gather", "kda_state_scatter", "kda_chunk_prefill", "kda_c
             "kda_recurrent_decode", "kda_ckpt_quantize_scatter", "kda_ckpt_dequantize_gather",
             "kda_latent_prefill", "kda_latent_prefill_workspace_size", "kda_latent_decode",
             "kda_latent_decode_workspace_size",
+            "kda_latent_quantize_scatter", "kda_latent_dequantize_gather", "kda_latent_decode_fp8",
+            "kda_latent_decode_shared", "kda_latent_shared_workspace_size",
             "kda_page_fork", "kda_page_fork_workspace_size", "kda_page_compact", "kda_page_compact_workspace_size",
             "kda_page_free",
             "kda_status_string", "kda_last_error_detail")
@@ -84,6 +86,28 @@ class LatentDecodeArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class LatentStore(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("L", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("codes_page_stride", ctypes.c_int64),
+                ("scales_page_stride", ctypes.c_int64), ("rope_page_stride", ctypes.c_int64)]
+
+
+class LatentSharedArgs(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("Q", ctypes.c_int64), ("H", ctypes.c_int64), ("L", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("G", ctypes.c_int64), ("cache_dtype", ctypes.c_int),
+                ("cache", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("scales_page_stride", ctypes.c_int64),
+                ("rope_page_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("cu_groups", ctypes.c_void_p), ("shared", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 3),
+                ("q_rope", ctypes.c_void_p), ("q_rope_stride", ctypes.c_int64 * 3),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 class PagePool(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int64),
                 ("max_pages", ctypes.c_int64), ("lengths", ctypes.c_void_p), ("refs", ctypes.c_void_p),
@@ -141,6 +165,17 @@ def load_library(path: str = LIB_PATH):
     lib.kda_latent_prefill_workspace_size.restype = ctypes.c_size_t
     lib.kda_latent_decode_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.kda_latent_decode_workspace_size.restype = ctypes.c_size_t
+    store = ctypes.POINTER(LatentStore)
+    lib.kda_latent_quantize_scatter.argtypes = [store, vp, i64, vp, i64, ctypes.c_int, vp, ctypes.c_int, i64, vp]
+    lib.kda_latent_quantize_scatter.restype = ctypes.c_int
+    lib.kda_latent_dequantize_gather.argtypes = [store, vp, ctypes.c_int, i64, vp, ctypes.c_int, vp]
+    lib.kda_latent_dequantize_gather.restype = ctypes.c_int
+    for name in ("kda_latent_decode_fp8", "kda_latent_decode_shared"):
+        entry = getattr(lib, name)
+        entry.argtypes = [ctypes.POINTER(LatentSharedArgs), vp]
+        entry.restype = ctypes.c_int
+    lib.kda_latent_shared_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    lib.kda_latent_shared_workspace_size.restype = ctypes.c_size_t
     pool, stores = ctypes.POINTER(PagePool), ctypes.POINTER(PageStore)
     lib.kda_page_fork.argtypes = [pool, stores, i64, vp, vp, ctypes.c_int, i64, ctypes.c_int, vp, vp, ctypes.c_size_t,
                                   vp]

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libkda.so")
 SOURCES = ["kda_api.cpp", "state_copy.hip", "chunk_prefill.hip", "decode.hip", "int8_ckpt.hip",
-           "latent_prefill.hip", "latent_decode.hip", "page_pool.hip"]
+           "latent_prefill.hip", "latent_decode.hip", "latent_cache.hip", "latent_shared.hip", "page_pool.hip"]
 ARCH = "gfx950"
 
 

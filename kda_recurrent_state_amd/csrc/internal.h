@@ -42,6 +42,25 @@ int64_t latent_prefill_workgroups(int64_t T, int64_t S, int64_t N, int64_t H);
 size_t latent_prefill_workspace_bytes(int64_t T, int64_t S, int64_t N, int64_t H, int64_t E);
 hipError_t launch_latent_decode(const kda_latent_decode_args_t& a, hipStream_t stream);
 size_t latent_decode_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L);
+hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t stream);
+size_t latent_shared_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L, int64_t G);
+
+// The 8-bit latent cache; arguments already validated.
+hipError_t launch_latent_quantize_scatter(const kda_latent_store_t& s, const void* c, int64_t c_stride,
+                                          const void* k_rope, int64_t k_rope_stride, bool bf16, const void* slots,
+                                          bool index64, int64_t n, hipStream_t stream);
+hipError_t launch_latent_dequantize_gather(const kda_latent_store_t& s, const void* slots, bool index64, int64_t n,
+                                           void* out, bool bf16, hipStream_t stream);
+
+// j / d = j mul >> shift for 0 <= j < 2^31: shift = 31 + s with 2^s >= d and mul
+// = floor(2^shift / d) + 1; mul d passes 2^shift by at most d <= 2^s, too little
+// to matter.
+inline void page_divisor(int d, uint32_t* mul, int* shift) {
+  int s = 0;
+  while (((int64_t)1 << s) < d) ++s;
+  *shift = 31 + s;
+  *mul = (uint32_t)(((uint64_t)1 << (31 + s)) / (uint32_t)d + 1);
+}
 
 // Page pool operators; arguments already validated.
 hipError_t launch_page_fork(const kda_page_pool_t& a, const kda_page_store_t* stores, int64_t num_stores,

@@ -409,6 +409,92 @@ kda_status_t check_latent_decode(const kda_latent_decode_args_t* a) {
   return alias_error(outs, same, 3, ins, 5) ? KDA_E_ALIAS : KDA_OK;
 }
 
+// The arrays of an 8-bit latent cache; spans: codes, scales, rope.
+kda_status_t check_latent_store(const kda_latent_store_t* s, Span* spans) {
+  if (!s) return KDA_E_NULL;
+  if (s->num_pages <= 0 || s->page_size <= 0 || s->L <= 0 || s->R < 0) return KDA_E_SHAPE;
+  if (s->L % 16 != 0 || s->L > 512 || !dim8(s->R, 0, 64)) return KDA_E_UNSUPPORTED;
+  if (s->num_pages > 0x7fffffff / s->page_size) return KDA_E_UNSUPPORTED;
+  const int64_t room = s->page_size;
+  if (s->codes_page_stride < room * s->L || s->scales_page_stride < room ||
+      (s->R > 0 && s->rope_page_stride < room * s->R))
+    return KDA_E_OVERLAP;
+  if (s->codes_page_stride % 16 != 0 || (s->R > 0 && s->rope_page_stride % 8 != 0)) return KDA_E_LAYOUT;
+  const int64_t most = kMaxSpan / s->num_pages;
+  if (s->codes_page_stride > most || s->scales_page_stride > most || (s->R > 0 && s->rope_page_stride > most))
+    return KDA_E_SHAPE;
+  if (!s->codes || !s->scales || (s->R > 0 && !s->rope)) return KDA_E_NULL;
+  if (!aligned(s->codes, 16) || !aligned(s->scales, 4) || (s->R > 0 && !aligned(s->rope, 16))) return KDA_E_LAYOUT;
+  spans[0] = {s->codes, (s->num_pages - 1) * s->codes_page_stride + room * s->L};
+  spans[1] = {s->scales, ((s->num_pages - 1) * s->scales_page_stride + room) * 4};
+  spans[2] = {s->R > 0 ? s->rope : nullptr, s->R > 0 ? ((s->num_pages - 1) * s->rope_page_stride + room * s->R) * 2 : 0};
+  if (spans_overlap(spans[0], spans[1]) || spans_overlap(spans[0], spans[2]) || spans_overlap(spans[1], spans[2]))
+    return KDA_E_ALIAS;
+  return KDA_OK;
+}
+
+// Rows of a call on the 8-bit cache: 2^24 workgroups of 16 at most.
+constexpr int64_t kMostRows = ((int64_t)1 << 28) - 1;
+
+kda_status_t check_latent_shared(const kda_latent_shared_args_t* a) {
+  if (!a) return KDA_E_NULL;
+  if (a->N < 0 || a->Q <= 0 || a->H <= 0 || a->L <= 0 || a->R < 0 || a->G < 0) return KDA_E_SHAPE;
+  if (a->num_pages <= 0 || a->page_size <= 0 || a->max_pages <= 0) return KDA_E_SHAPE;
+  if (a->cache_dtype != KDA_BF16 && a->cache_dtype != KDA_E4M3) return KDA_E_DTYPE;
+  const bool f8 = a->cache_dtype == KDA_E4M3;
+  if (!dim8(a->L, 8, 512) || !dim8(a->R, 0, 64) || (f8 && a->L % 16 != 0)) return KDA_E_UNSUPPORTED;
+  if (a->Q > 1024 || a->H > 1024 || a->Q * a->H > 1024) return KDA_E_UNSUPPORTED;
+  if (a->N > 65535 || a->G > 65535) return KDA_E_UNSUPPORTED;  // sequences are a grid dimension
+  if (!(a->scale > 0.f && a->scale <= kMostScale)) return KDA_E_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 30, row = a->L + a->R;
+  if (a->page_size > most || a->max_pages > most / a->page_size || a->num_pages > 0x7fffffff) return KDA_E_UNSUPPORTED;
+  // (a workgroup's tiles are counted in 31 bits)
+  const int64_t room = a->max_pages * a->page_size;
+  if (a->N > 1 && room > ((int64_t)1 << 40) / a->N) return KDA_E_UNSUPPORTED;
+  if (a->N > 0 && room > ((int64_t)1 << 48) / (a->N * a->Q * a->H)) return KDA_E_UNSUPPORTED;
+  if (a->N > 1 && a->table_stride < a->max_pages) return KDA_E_OVERLAP;
+  if (a->N > 1 && a->table_stride > kMaxSpan / a->N) return KDA_E_SHAPE;
+  Span store[3] = {{nullptr, 0}, {nullptr, 0}, {nullptr, 0}};
+  if (f8) {
+    const kda_latent_store_t s = {const_cast<void*>(a->cache), const_cast<float*>(a->scales), const_cast<void*>(a->rope),
+                                  a->num_pages, a->page_size, a->L, a->R,
+                                  a->page_stride, a->scales_page_stride, a->rope_page_stride};
+    const kda_status_t st = check_latent_store(&s, store);
+    if (st != KDA_OK) return st;
+  } else {
+    if (a->page_stride < a->page_size * row) return KDA_E_OVERLAP;
+    if (a->page_stride % 8 != 0) return KDA_E_LAYOUT;
+    if (a->page_stride > kMaxSpan / a->num_pages) return KDA_E_SHAPE;
+    if (a->N > 0 && !a->cache) return KDA_E_NULL;
+    if (!aligned(a->cache, 16)) return KDA_E_LAYOUT;
+    store[0] = {a->cache, ((a->num_pages - 1) * a->page_stride + a->page_size * row) * 2};
+  }
+  if (a->N == 0) return KDA_OK;
+  if (!a->page_table || !a->lengths || !a->q || (a->R > 0 && !a->q_rope) || !a->out) return KDA_E_NULL;
+  if (a->G > 0 && (!a->cu_groups || !a->shared)) return KDA_E_NULL;
+  const int64_t nqh[3] = {a->N, a->Q, a->H};
+  int64_t qn = 0, rn = 0;
+  if (!outer_span(nqh, a->q_stride, 3, a->L, &qn) || (a->R > 0 && !outer_span(nqh, a->q_rope_stride, 3, a->R, &rn)))
+    return KDA_E_LAYOUT;
+  if (!aligned(a->q, 16) || (a->R > 0 && !aligned(a->q_rope, 16)) || !aligned(a->out, 16)) return KDA_E_LAYOUT;
+  const size_t need = kda::latent_shared_workspace_bytes(a->N, a->Q, a->H, a->L, a->G);
+  if (!a->workspace || a->workspace_bytes < need) return KDA_E_WORKSPACE;
+  if (!aligned(a->workspace, 16)) return KDA_E_LAYOUT;
+  const int64_t rows = a->N * a->Q * a->H;
+  const Span ins[9] = {store[0],
+                       store[1],
+                       store[2],
+                       {a->page_table, ((a->N - 1) * a->table_stride + a->max_pages) * 4},
+                       {a->lengths, a->N * 4},
+                       {a->q, qn * 2},
+                       {a->R > 0 ? a->q_rope : nullptr, rn * 2},
+                       {a->G > 0 ? a->cu_groups : nullptr, (a->G + 1) * 4},
+                       {a->G > 0 ? a->shared : nullptr, a->G * 4}};
+  const Span outs[3] = {{a->out, rows * a->L * 2}, {a->lse, rows * 4}, {a->workspace, (int64_t)need}};
+  const int same[3] = {-1, -1, -1};
+  return alias_error(outs, same, 3, ins, 9) ? KDA_E_ALIAS : KDA_OK;
+}
+
 kda_status_t check_pool(const kda_page_pool_t* p, Span* spans) {
   if (!p) return KDA_E_NULL;
   if (p->num_seqs <= 0 || p->max_pages <= 0 || p->num_pages <= 0 || p->page_size <= 0) return KDA_E_SHAPE;
@@ -479,6 +565,75 @@ kda_status_t kda_latent_decode(const kda_latent_decode_args_t* a, void* stream) 
   const kda_status_t st = check_latent_decode(a);
   if (st != KDA_OK || a->N == 0) return st;
   return hip_status("kda_latent_decode launch", kda::launch_latent_decode(*a, static_cast<hipStream_t>(stream)));
+}
+
+kda_status_t kda_latent_quantize_scatter(const kda_latent_store_t* store, const void* c, int64_t c_stride,
+                                         const void* k_rope, int64_t k_rope_stride, kda_dtype_t dtype,
+                                         const void* slots, kda_index_t it, int64_t num_rows, void* stream) {
+  Span outs[3];
+  const kda_status_t st = check_latent_store(store, outs);
+  if (st != KDA_OK) return st;
+  if (!valid_dtype(dtype) || (it != KDA_I32 && it != KDA_I64)) return KDA_E_DTYPE;
+  if (num_rows < 0) return KDA_E_SHAPE;
+  if (num_rows > kMostRows) return KDA_E_UNSUPPORTED;
+  if (num_rows == 0) return KDA_OK;
+  if (!c || !slots || (store->R > 0 && !k_rope)) return KDA_E_NULL;
+  int64_t cn = 0, rn = 0;
+  if (!outer_span(&num_rows, &c_stride, 1, store->L, &cn) ||
+      (store->R > 0 && !outer_span(&num_rows, &k_rope_stride, 1, store->R, &rn)))
+    return KDA_E_LAYOUT;
+  if (!aligned(c, 16) || (store->R > 0 && !aligned(k_rope, 16))) return KDA_E_LAYOUT;
+  const int64_t eb = dtype_bytes(dtype);
+  const Span ins[3] = {{c, cn * eb},
+                       {store->R > 0 ? k_rope : nullptr, rn * eb},
+                       {slots, num_rows * (it == KDA_I64 ? 8 : 4)}};
+  const int none[3] = {-1, -1, -1};
+  if (alias_error(outs, none, 3, ins, 3)) return KDA_E_ALIAS;
+  return hip_status("kda_latent_quantize_scatter launch",
+                    kda::launch_latent_quantize_scatter(*store, c, c_stride, k_rope, k_rope_stride, dtype == KDA_BF16,
+                                                        slots, it == KDA_I64, num_rows,
+                                                        static_cast<hipStream_t>(stream)));
+}
+
+kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const void* slots, kda_index_t it,
+                                          int64_t num_rows, void* out, kda_dtype_t dtype, void* stream) {
+  Span ins[4];
+  const kda_status_t st = check_latent_store(store, ins);
+  if (st != KDA_OK) return st;
+  if (!valid_dtype(dtype) || (it != KDA_I32 && it != KDA_I64)) return KDA_E_DTYPE;
+  if (num_rows < 0) return KDA_E_SHAPE;
+  if (num_rows > kMostRows) return KDA_E_UNSUPPORTED;
+  if (num_rows == 0) return KDA_OK;
+  if (!out || !slots) return KDA_E_NULL;
+  if (!aligned(out, 16)) return KDA_E_LAYOUT;
+  ins[3] = {slots, num_rows * (it == KDA_I64 ? 8 : 4)};
+  const Span outs[1] = {{out, num_rows * (store->L + store->R) * dtype_bytes(dtype)}};
+  const int none[1] = {-1};
+  if (alias_error(outs, none, 1, ins, 4)) return KDA_E_ALIAS;
+  return hip_status("kda_latent_dequantize_gather launch",
+                    kda::launch_latent_dequantize_gather(*store, slots, it == KDA_I64, num_rows, out,
+                                                         dtype == KDA_BF16, static_cast<hipStream_t>(stream)));
+}
+
+size_t kda_latent_shared_workspace_size(int64_t N, int64_t Q, int64_t H, int64_t L, int64_t G) {
+  if (N <= 0 || Q <= 0 || H <= 0 || L <= 0 || G < 0 || N > 65535 || Q > 1024 || H > 1024 || Q * H > 1024 || L > 512 ||
+      G > 65535)
+    return 0;
+  return kda::latent_shared_workspace_bytes(N, Q, H, L, G);
+}
+
+kda_status_t kda_latent_decode_fp8(const kda_latent_shared_args_t* a, void* stream) {
+  if (a && a->cache_dtype != KDA_E4M3) return KDA_E_DTYPE;
+  if (a && a->G != 0) return KDA_E_SHAPE;
+  const kda_status_t st = check_latent_shared(a);
+  if (st != KDA_OK || a->N == 0) return st;
+  return hip_status("kda_latent_decode_fp8 launch", kda::launch_latent_shared(*a, static_cast<hipStream_t>(stream)));
+}
+
+kda_status_t kda_latent_decode_shared(const kda_latent_shared_args_t* a, void* stream) {
+  const kda_status_t st = check_latent_shared(a);
+  if (st != KDA_OK || a->N == 0) return st;
+  return hip_status("kda_latent_decode_shared launch", kda::launch_latent_shared(*a, static_cast<hipStream_t>(stream)));
 }
 
 size_t kda_page_fork_workspace_size(int64_t num_forks, int64_t max_pages, int64_t num_pages, int share) {

@@ -1,0 +1,404 @@
+// A tile of cached latent rows in LDS and the two products of absorbed latent
+// attention over it, shared by the decode kernels.
+#pragma once
+
+#include "latent_common.h"
+
+namespace kda {
+namespace latent {
+
+constexpr int kTile = 64;      // tokens a tile
+constexpr int kThreads = 512;  // 8 waves
+constexpr int kWaves = kThreads / 64;
+
+// LP, RP: L and R rounded up to what the kernel is built for; NB: blocks of 16
+// query rows a workgroup; kPad: whether L < LP or R < RP.  (Builds of their own:
+// with the padding lanes' masks in all of them, 200 ragged sequences took 136.0
+// us instead of 133.9 and 64 x 16000 tokens, 128 heads, 371 instead of 364.)
+// kScalar: LDS offsets are put into scalar registers by hand, for kernels with so
+// many uniform values that the compiler leaves sums of them in vector registers.
+template <int LP, int RP, int NB, bool kPad, bool kScalar = false>
+struct Bf16Tile {
+  static constexpr int MB = 16 * NB;
+  static constexpr int DP = LP + RP;
+  static constexpr int LC = LP / 8;               // 16-byte chunks of a staged latent row
+  static constexpr int KS = DP / 32;              // contraction steps of the scores
+  static constexpr int MT = LP / (16 * kWaves);   // 16-column blocks of the output a wave
+  static constexpr int TG = NB == 4 ? 2 : 4;      // groups of tokens of a tile
+  static constexpr int TB = kTile / 16 / TG;      // blocks of 16 tokens a group
+  static constexpr int kScoring = NB * TG;        // waves that score (a row block and a group each)
+  static constexpr int kStage = kTile * LP;       // elements of a stage
+  static constexpr int kRows = kTile / kWaves;    // rows a wave fetches
+
+  // Chunk c of latent row r is staged at position c ^ 2 f(r) with f = r & 3 and
+  // bit 3 of r above it.  The LDS serves a 16-byte read in the lanes' groups
+  // {0-3, 12-15, 20-27}, {4-11, 16-19, 28-31} and these + 32, a transposed
+  // 8-byte read in halves of 32 lanes (found by timing reads in which two lanes
+  // share a bank): a group's score operands (rows 0-3 and 12-15 of one chunk,
+  // 4-11 of the next one) and a half's values (rows 0-3 and 8-11 of two chunks)
+  // then fall on distinct banks.  Rotary rows (128 B) lie apart, two tiles of
+  // them; their chunk c is at c ^ ((r >> 1) & 7).
+  static __device__ __forceinline__ int swizzle(int r) { return (r & 3) * 2 + (r & 8); }
+
+  static constexpr int RI = 64 / LC;       // latent rows a load covers
+  static constexpr int kLat = kRows / RI;  // latent loads of a wave for a tile
+
+  // What a lane adds to its rows' addresses.  The lanes of padding columns
+  // (L < LP, R < RP) are off: those stay 0 in LDS from the start, as the queries
+  // are there (anything else times 0 could be NaN), and the outputs of them are
+  // not written.
+  struct Columns {
+    unsigned lat, last, rot;
+    bool has_rot;
+  };
+  static __device__ __forceinline__ Columns columns(int L, int R, int wave, unsigned lane) {
+    Columns c;
+    c.lat = (lane % LC * 16) ^ (swizzle(wave * kRows + lane / LC) * 16);
+    c.last = (unsigned)(L - 8) * 2;
+    const unsigned r = wave * 8 + lane / 8, off = (lane % 8 ^ r / 2 % 8) * 16;
+    c.rot = off + L * 2;
+    c.has_rot = off < (unsigned)R * 2;
+    return c;
+  }
+  static __device__ __forceinline__ unsigned lds_at(unsigned x) { return kScalar ? (unsigned)uniform(x) : x; }
+  // Latent load i of the tile whose rows lie at ``at`` (lane i: token i), to
+  // the stage at ``lds``.
+  static __device__ __forceinline__ void fetch(int i, const char* at, int wave, int lane, const Columns& c,
+                                               unsigned lds) {
+    const int r = wave * kRows + i * RI;
+    const unsigned off = c.lat ^ (unsigned)(swizzle(i * RI) * 16);
+    if (RI == 1) {
+      const char* row = (const char*)lane64((int64_t)at, r);
+      if (!kPad || off <= c.last) load_lds16(row, off, lds_at(lds + r * LP * 2));
+    } else {
+      const char* row = (const char*)__shfl((int64_t)at, r + lane / LC, 64);
+      if (!kPad || off <= c.last) load_lds16(row + off, lds_at(lds + r * LP * 2));
+    }
+  }
+  // The tile's rotary rows, 8 a wave.
+  static __device__ __forceinline__ void fetch_rotary(const char* at, int wave, int lane, const Columns& c,
+                                                      unsigned lds) {
+    if (RP > 0) {
+      const char* row = (const char*)__shfl((int64_t)at, wave * 8 + lane / 8, 64);
+      if (!kPad || c.has_rot) load_lds16(row + c.rot, lds_at(lds + wave * 8 * RP * 2));
+    }
+  }
+
+  // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i
+  // of each block.  Operands are read a group ahead of their products, and
+  // load(i), 0 <= i < kLat, is called along the way: a wave stands still while
+  // the memory pipeline takes a load, so they are spread over its products.
+  template <typename Load>
+  static __device__ __forceinline__ void scores(const __bf16* lat_row, const __bf16* rot_row, const bf16x8 (&qf)[KS],
+                                                int ln, int lg, f32x4 (&s)[TB], const Load& load) {
+    const char *lat = reinterpret_cast<const char*>(lat_row), *rot = reinterpret_cast<const char*>(rot_row);
+    const int x = (lg ^ swizzle(ln)) * 16, y = (lg ^ ((ln >> 1) & 7)) * 16;
+    constexpr int F = KS * TB, G = NB == 4 ? 4 : 6, NG = (F + G - 1) / G, LG = (kLat + NG - 1) / NG;
+    bf16x8 kf[2][G];
+    auto read = [&](int g) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int f = g * G + i, k = f / TB, j = f % TB;
+        if (f >= F) continue;
+        const char* at = k < LP / 32 ? lat + (x ^ ((k & 3) * 64)) + (k >> 2) * 256 + j * 16 * LP * 2
+                                     : rot + (y ^ ((k - LP / 32) * 64)) + j * 16 * RP * 2;
+        kf[g & 1][i] = *reinterpret_cast<const bf16x8*>(at);
+      }
+    };
+    f32x4 part[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains of products
+    read(0);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      if (g + 1 < NG) read(g + 1);
+      hold_order();
+#pragma unroll
+      for (int i = g * LG; i < kLat && i < (g + 1) * LG; ++i) load(i);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int f = g * G + i;
+        if (f < F) part[f & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[g & 1][i], qf[f / TB], part[f & 1], 0, 0, 0);
+      }
+      hold_order();
+    }
+    if (TB == 1) {
+      s[0] = part[0] + part[1];
+    } else {
+      s[0] = part[0];
+      s[TB - 1] = part[1];
+    }
+  }
+
+  // out^T[column][row] += rows^T P^T for the wave's columns, the operands read
+  // one block of NB products ahead
+  static __device__ __forceinline__ void values(const __bf16* tile, const __bf16* prob, int wave, int ln, int lg,
+                                                f32x4 (&acc)[MT][NB]) {
+    const int r0 = 8 * lg + (ln >> 2);  // rows r0 and r0 + 4 of each 32
+    const int c0 = wave * (MT * 2) + ((ln & 3) >> 1);
+    const char* rows = reinterpret_cast<const char*>(tile + r0 * LP) + (ln & 1) * 8;
+    constexpr int B = kTile / 32 * MT;
+    bf16x8 pf[NB], vf[2];
+    auto weights = [&](int k) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        pf[j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kTile + (((4 * k + lg) ^ (ln & 7)) << 3));
+    };
+    auto read = [&](int b) {
+      const int k = b / MT, i = b % MT;
+      const int x = ((c0 + 2 * i) ^ swizzle(r0)) * 16;
+      vf[b & 1] = join(read_tr(rows + x + k * 32 * LP * 2), read_tr(rows + x + (k * 32 + 4) * LP * 2));
+    };
+    weights(0);
+    read(0);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (b == MT) weights(1);
+      if (b + 1 < B) read(b + 1);
+      hold_order();
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[b % MT][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[b & 1], pf[j], acc[b % MT][j], 0, 0, 0);
+      hold_order();
+    }
+  }
+};
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Transposed 8-byte LDS read of bytes: in each group of 16 lanes, lane i points
+// at columns 8 (i % 2) .. + 7 of row i / 2 of an 8 x 16 block and receives column
+// i of the eight rows.
+__device__ __forceinline__ i32x2 read_tr8(const void* lds) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)lds);
+}
+
+// eight e4m3 codes as bf16 (exact)
+__device__ __forceinline__ bf16x8 widen(const i32x2& codes) {
+  typedef unsigned u32x4_ __attribute__((ext_vector_type(4)));
+  u32x4_ r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)codes[i], 1.f, false));
+    r[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)codes[i], 1.f, true));
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// The same tile of e4m3 codes, with a scale a token and the rotary keys in bf16.
+// The scores' product runs on the codes as they are: a bf16 query, over a power
+// of two that brings its largest component to [128, 256), is the sum of two e4m3
+// numbers (its 8 bits are 4 and, with a sign, 4), so two 8-bit products,
+// at twice the rate of one in bf16, take the place of the conversion
+// of every code in each wave that scores it.  What the split drops of components
+// far below the largest is at most 2^-18 of that; the 8-bit product's own
+// sums keep about 2^-16 of their usual size (measured: 2e-5 over 128 terms, no
+// bias).  The values' product converts codes to bf16 on the way in, and the scales
+// go into the weights before these are rounded to bf16.
+template <int LP, int RP, int NB, bool kPad>
+struct Fp8Tile {
+  static constexpr int MB = 16 * NB;
+  static constexpr int LC = LP / 16;              // 16-byte chunks of a staged latent row
+  static constexpr int KS = LP / 128;             // contraction steps of the latent scores
+  static constexpr int KR = RP / 32;              // and of the rotary ones
+  static constexpr int MT = LP / (16 * kWaves);   // 16-column blocks of the output a wave
+  static constexpr int TG = NB == 4 ? 2 : 4;      // groups of tokens of a tile
+  static constexpr int TB = kTile / 16 / TG;      // blocks of 16 tokens a group
+  static constexpr int kScoring = NB * TG;        // waves that score
+  static constexpr int kStage = kTile * LP;       // bytes of a stage
+  static constexpr int kRows = kTile / kWaves;    // rows a wave fetches
+  static constexpr int RI = 64 / LC;              // rows a load covers
+  static constexpr int kLat = kRows / RI;         // latent loads of a wave for a tile
+  static constexpr int kLoads = kLat + (RP > 0 ? 1 : 0) + 1;  // and all of them
+
+  // Chunk c of latent row r is staged at position c ^ swizzle(r): a service
+  // group of 16-byte reads (rows 0-3 and 12-15 of one chunk, 4-11 of the chunk
+  // two further) and a half wave of transposed reads (16 rows of one chunk) then
+  // fall on distinct banks.  Rows of 128 B lie two to a pass over the banks.
+  static __device__ __forceinline__ int swizzle(int r) { return LP == 128 ? ((r >> 1) + 2) & 7 : r & 15; }
+
+  // A lane's part of its rows' addresses; lanes of padding columns are off, as
+  // in Bf16Tile (every load still has lanes that are on, so a wave's loads
+  // can be counted).
+  struct Columns {
+    int lat, L;
+    unsigned rot;
+    bool has_rot;
+  };
+  static __device__ __forceinline__ Columns columns(int L, int R, int wave, unsigned lane) {
+    Columns c;
+    const unsigned r = wave * 8 + lane / 8;
+    c.rot = (lane % 8 ^ r / 2 % 8) * 16;
+    c.has_rot = c.rot < (unsigned)R * 2;
+    c.lat = ((lane % LC) ^ swizzle(wave * kRows + lane / LC)) * 16;
+    c.L = L;
+    return c;
+  }
+  // All of a wave's loads for the tile whose codes, rotary keys and scales lie at
+  // lat, rot and scale (lane i: token i).
+  static __device__ __forceinline__ void fetch(const char* lat, const char* rot, const char* scale, int wave, int lane,
+                                               const Columns& c, unsigned lat_lds, unsigned rot_lds, unsigned scale_lds) {
+    if (lane / 8 == wave) load_lds4(scale, uniform(scale_lds));
+    if (RP > 0) {
+      const char* row = (const char*)__shfl((int64_t)rot, wave * 8 + lane / 8, 64);
+      if (!kPad || c.has_rot) load_lds16(row + c.rot, uniform(rot_lds + wave * 8 * RP * 2));
+    }
+#pragma unroll
+    for (int i = 0; i < kLat; ++i) {
+      const int r = wave * kRows + i * RI;
+      const int at = c.lat ^ ((swizzle(i * RI) ^ swizzle(0)) * 16);
+      const char* row = (const char*)__shfl((int64_t)lat, r + lane / LC, 64);
+      if (!kPad || at < c.L) load_lds16(row + at, uniform(lat_lds + r * LP));
+    }
+  }
+
+  // A lane's part of a query row: components 128 k + 32 lg .. + 31 of the latent
+  // part, 32 k + 8 lg .. + 7 of the rotary part.
+  struct Raw {
+    u32x4 lat[KS][4];
+    bf16x8 rot[KR > 0 ? KR : 1];
+  };
+  struct Query {
+    i32x8 hi[KS], lo[KS];
+    bf16x8 rot[KR > 0 ? KR : 1];
+    float size;  // the power of two taken out
+  };
+  static __device__ __forceinline__ void request(const __bf16* q, const __bf16* qr, int L, int R, int lg, Raw& x) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 128 * k + 32 * lg + 8 * j;
+        x.lat[k][j] = u32x4{0, 0, 0, 0};
+        if (!kPad || c < L) x.lat[k][j] = *reinterpret_cast<const u32x4*>(q + c);
+      }
+#pragma unroll
+    for (int k = 0; k < KR; ++k) {
+      const int c = 32 * k + 8 * lg;
+      bf16x8 y = {};
+      if (!kPad || c < R) y = *reinterpret_cast<const bf16x8*>(qr + c);
+      x.rot[k] = y;
+    }
+  }
+  static __device__ __forceinline__ void split(const Raw& x, Query& q) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m2 = {0, 0};
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, x.lat[k][j][i] & 0x7fff7fffu));
+    // (of the bits: an infinity or a NaN is the largest and becomes NaN in the codes)
+    int e = m2[0] > m2[1] ? m2[0] : m2[1];
+    e = max(e, __shfl_xor(e, 16, 64));
+    e = max(e, __shfl_xor(e, 32, 64)) >> 7;
+    e = e < 8 ? 8 : e;
+    const float inv = __builtin_bit_cast(float, (unsigned)(261 - e) << 23);
+    q.size = __builtin_bit_cast(float, (unsigned)(e - 7) << 23);
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const unsigned w0 = x.lat[k][d >> 1][2 * (d & 1)], w1 = x.lat[k][d >> 1][2 * (d & 1) + 1];
+        const float y[4] = {__builtin_bit_cast(float, w0 << 16) * inv, __builtin_bit_cast(float, w0 & 0xffff0000u) * inv,
+                            __builtin_bit_cast(float, w1 << 16) * inv, __builtin_bit_cast(float, w1 & 0xffff0000u) * inv};
+        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], hi, true);
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
+        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] - a[0], y[1] - a[1], 0, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] - b[0], y[3] - b[1], lo, true);
+        q.hi[k][d] = hi;
+        q.lo[k][d] = lo;
+        hold_order();  // (in turn, in the registers of what is split)
+      }
+#pragma unroll
+    for (int k = 0; k < KR; ++k) q.rot[k] = x.rot[k];
+  }
+
+  // S^T[token][row] of the wave's tokens and rows, and the tokens' scales; a lane
+  // holds tokens 4 lg + i of each block.  lat, rot, scale: of the group's first
+  // token.
+  static __device__ __forceinline__ void scores(const char* lat, const __bf16* rot, const float* scale, const Query& q,
+                                                int ln, int lg, f32x4 (&s)[TB], f32x4 (&sc)[TB]) {
+    constexpr int F = KS * TB;
+    const char* row = lat + ln * LP;
+    const int at0 = ((2 * lg) ^ swizzle(ln)) * 16;  // (chunk 8 k + 2 lg + i: bits 3, 4, .. of k apart from the others)
+    auto read = [&](int n) {  // codes of step n / TB, block n % TB
+      const int k = n / TB, j = n % TB;
+      const char* at = row + j * 16 * LP + (k >> 1) * 256;
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 a = *reinterpret_cast<const i32x4*>(at + (at0 ^ ((k & 1) * 128)));
+      const i32x4 b = *reinterpret_cast<const i32x4*>(at + (at0 ^ ((k & 1) * 128 + 16)));
+      return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    };
+    f32x4 hi[TB], lo[TB], ro[TB];
+    i32x8 x[2];
+    bf16x8 y[KR > 0 ? KR : 1][TB];
+    x[0] = read(0);
+#pragma unroll
+    for (int j = 0; j < TB; ++j) hi[j] = lo[j] = ro[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int n = 0; n < F; ++n) {
+      if (n + 1 < F) {
+        x[(n + 1) & 1] = read(n + 1);
+      } else {
+        const int y0 = (lg ^ ((ln >> 1) & 7)) * 16;
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+          sc[j] = *reinterpret_cast<const f32x4*>(scale + 16 * j + 4 * lg);
+#pragma unroll
+          for (int k = 0; k < KR; ++k)
+            y[k][j] = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(rot) + (16 * j + ln) * RP * 2 +
+                                                       (y0 ^ (k * 64)));
+        }
+      }
+      hold_order();
+      const int k = n / TB, j = n % TB;
+      hi[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[n & 1], q.hi[k], hi[j], 0, 0, 0, 0, 0, 0);
+      lo[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[n & 1], q.lo[k], lo[j], 0, 0, 0, 0, 0, 0);
+      hold_order();
+    }
+#pragma unroll
+    for (int k = 0; k < KR; ++k)
+#pragma unroll
+      for (int j = 0; j < TB; ++j) ro[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[k][j], q.rot[k], ro[j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[j][i] = fmaf(hi[j][i] + lo[j][i], q.size * sc[j][i], ro[j][i]);
+  }
+
+  // out^T[column][row] += codes^T P^T for the wave's columns (P has the scales)
+  static __device__ __forceinline__ void values(const char* tile, const __bf16* prob, int wave, int ln, int lg,
+                                                f32x4 (&acc)[MT][NB]) {
+    const int r0 = 8 * lg + (ln >> 1);  // of each 32
+    const char* rows = tile + r0 * LP + (ln & 1) * 8;
+    const int at0 = ((wave * MT) ^ swizzle(r0)) * 16;
+    constexpr int B = kTile / 32 * MT;
+    bf16x8 pf[NB];
+    i32x2 vf[2];
+    auto weights = [&](int k) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        pf[j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kTile + (((4 * k + lg) ^ (ln & 7)) << 3));
+    };
+    auto read = [&](int b) { vf[b & 1] = read_tr8(rows + b / MT * 32 * LP + (at0 ^ (b % MT * 16))); };
+    weights(0);
+    read(0);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (b == MT) weights(1);
+      if (b + 1 < B) read(b + 1);
+      hold_order();
+      const bf16x8 v = widen(vf[b & 1]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[b % MT][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pf[j], acc[b % MT][j], 0, 0, 0);
+      hold_order();
+    }
+  }
+};
+
+}  // namespace latent
+}  // namespace kda

@@ -11,7 +11,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import KDA_BF16, KDAError, LatentDecodeArgs, LatentPrefillArgs, PagePool, PageStore
+from ._lib import (KDA_BF16, KDA_E4M3, KDA_F32, KDAError, LatentDecodeArgs, LatentPrefillArgs, LatentSharedArgs,
+                   LatentStore, PagePool, PageStore)
 from .api import _device as _checked_device, _index_code, _on_stream, _stream_handle
 
 
@@ -198,6 +199,226 @@ def kda_latent_decode(cache: torch.Tensor, page_table: torch.Tensor, lengths: to
                          q4.stride()[:3], *rope, out.data_ptr(), None if lse is None else lse.data_ptr(), scale, *ws)
     _call(what, dev, stream, made, lib.kda_latent_decode, a)
     return out, lse
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _pages(what: str, name: str, t: torch.Tensor, dense: int) -> int:
+    """Elements from page to page of a cache tensor [num_pages, page_size, ...] with dense pages."""
+    shape, stride = t.shape, t.stride()
+    run = 1
+    for d in range(len(shape) - 1, 0, -1):
+        if shape[d] != 1 and stride[d] != run:
+            raise KDAError(what, 4, "%s: the pages must be dense" % name)
+        run *= shape[d]
+    return stride[0] if shape[0] > 1 else max(run, dense)
+
+
+def _store(what: str, codes: torch.Tensor, scales: torch.Tensor, rope: Optional[torch.Tensor]):
+    """(num_pages, page_size, L, R, page strides) of an 8-bit latent cache's tensors."""
+    if codes.dim() != 3 or scales.dim() != 2 or (rope is not None and rope.dim() != 3):
+        raise KDAError(what, 3, "codes and rope must be 3-D, scales 2-D")
+    if codes.dtype not in _CODES:
+        raise KDAError(what, 2, "codes must be float8_e4m3fn or uint8, got %s" % codes.dtype)
+    if scales.dtype != torch.float32 or (rope is not None and rope.dtype != torch.bfloat16):
+        raise KDAError(what, 2, "scales must be float32 and rope bfloat16")
+    num_pages, page_size, L = codes.shape
+    R = 0 if rope is None else rope.shape[2]
+    if scales.shape != codes.shape[:2] or (rope is not None and rope.shape[:2] != codes.shape[:2]):
+        raise KDAError(what, 3, "need codes [num_pages,page_size,L], scales [num_pages,page_size], "
+                                "rope [num_pages,page_size,R]")
+    return (num_pages, page_size, L, R,
+            _pages(what, "codes", codes, -(-page_size * L // 16) * 16), _pages(what, "scales", scales, 1),
+            _pages(what, "rope", rope, -(-page_size * R // 8) * 8) if R > 0 else 0)
+
+
+def _rows(what: str, name: str, t: torch.Tensor) -> int:
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise KDAError(what, 4, "the last dim of %s must be dense" % name)
+    return t.stride(0)
+
+
+_VALUES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+
+
+def kda_latent_quantize_scatter(c: torch.Tensor, k_rope: Optional[torch.Tensor], slots: torch.Tensor,
+                                codes: torch.Tensor, scales: torch.Tensor, rope: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """Writes token rows into an 8-bit latent cache.
+
+    c: [T,L] latent vectors and k_rope: [T,R] rotary keys, both bf16 or both
+    fp32, rows with any strides that are multiples of 8 (None: R = 0); slots: [T] int32 or
+    int64, the token row (page * page_size + place) each goes to, entries
+    outside the cache are skipped; codes: [num_pages, page_size, L]
+    float8_e4m3fn (or uint8, the bits); scales: [num_pages, page_size] fp32; rope:
+    [num_pages, page_size, R] bf16 (dense pages, any page stride that keeps 16 bytes' alignment).
+    A row's scale is the smallest power of two under which its largest
+    component is at most 448, its codes c / scale rounded to e4m3.  A row that
+    is not finite gets the scale NaN.  Valid slots must be unique.
+    """
+    what = "kda_latent_quantize_scatter"
+    lib = _lib.load_library()
+    dev = _device(c, k_rope, slots, codes, scales, rope)
+    num_pages, page_size, L, R, *strides = _store(what, codes, scales, rope)
+    if c.dim() != 2 or slots.dim() != 1 or (k_rope is not None and k_rope.dim() != 2):
+        raise KDAError(what, 3, "c and k_rope must be 2-D, slots 1-D")
+    T = c.shape[0]
+    if (c.shape[1] != L or slots.shape[0] != T or (0 if k_rope is None else k_rope.shape[1]) != R or
+            (k_rope is not None and k_rope.shape[0] != T)):
+        raise KDAError(what, 3, "need c [T,L], k_rope [T,R], slots [T] with the cache's L and R")
+    if c.dtype not in _VALUES or (k_rope is not None and k_rope.dtype != c.dtype):
+        raise KDAError(what, 2, "c and k_rope must both be bfloat16 or both float32")
+    if not slots.is_contiguous():
+        raise KDAError(what, 4, "slots must be contiguous")
+    index = _index_code(slots)
+    rope_at = (k_rope.data_ptr(), _rows(what, "k_rope", k_rope)) if R > 0 else (None, 0)
+    store = LatentStore(codes.data_ptr(), scales.data_ptr(), rope.data_ptr() if R > 0 else None, num_pages, page_size,
+                        L, R, *strides)
+    _call(what, dev, stream, [], lib.kda_latent_quantize_scatter, store, c.data_ptr(), _rows(what, "c", c), *rope_at,
+          _VALUES[c.dtype], slots.data_ptr(), index, T)
+
+
+def kda_latent_dequantize_gather(codes: torch.Tensor, scales: torch.Tensor, rope: Optional[torch.Tensor],
+                                 slots: torch.Tensor, out: Optional[torch.Tensor] = None,
+                                 dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Reads token rows of an 8-bit latent cache: [T, L+R], the latent vector
+    (code * scale) and the rotary key, in bf16 or fp32 (``dtype``, or that of
+    ``out``); zeros for slots outside the cache.  The cache's tensors and slots
+    as for :func:`kda_latent_quantize_scatter`; slots may repeat."""
+    what = "kda_latent_dequantize_gather"
+    lib = _lib.load_library()
+    dev = _device(codes, scales, rope, slots, out)
+    num_pages, page_size, L, R, *strides = _store(what, codes, scales, rope)
+    if slots.dim() != 1:
+        raise KDAError(what, 3, "slots must be 1-D")
+    if not slots.is_contiguous():
+        raise KDAError(what, 4, "slots must be contiguous")
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _VALUES:
+        raise KDAError(what, 2, "rows are read as bfloat16 or float32, not %s" % dtype)
+    T = slots.shape[0]
+    index = _index_code(slots)
+    made = []
+    out = _out(what, "out", out, (T, L + R), dtype, dev, made)
+    store = LatentStore(codes.data_ptr(), scales.data_ptr(), rope.data_ptr() if R > 0 else None, num_pages, page_size,
+                        L, R, *strides)
+    _call(what, dev, stream, made, lib.kda_latent_dequantize_gather, store, slots.data_ptr(), index, T,
+          out.data_ptr(), _VALUES[dtype])
+    return out
+
+
+def kda_latent_shared_workspace_size(N: int, Q: int, H: int, L: int, G: int = 0) -> int:
+    return int(_lib.load_library().kda_latent_shared_workspace_size(N, Q, H, L, G))
+
+
+def _decode_shared(what: str, cache, page_table, lengths, cu_groups, shared, q, q_rope, scale, out, lse, with_lse,
+                   workspace, stream):
+    lib = _lib.load_library()
+    if scale is None:
+        raise KDAError(what, 3, "scale must be given: the expanded form's key dim is not known here")
+    fp8 = isinstance(cache, (tuple, list))
+    if fp8 and len(cache) != 3:
+        raise KDAError(what, 3, "an 8-bit cache is (codes, scales, rope)")
+    codes, scales, rope = cache if fp8 else (cache, None, None)
+    dev = _device(codes, scales, rope, page_table, lengths, cu_groups, shared, q, q_rope, out, lse, workspace)
+    if q.dim() not in (3, 4) or (q_rope is not None and q_rope.dim() != q.dim()):
+        raise KDAError(what, 3, "q and q_rope must be 3-D or 4-D")
+    _operand(what, "q", q)
+    _int32(what, "page_table", page_table, 2)
+    _int32(what, "lengths", lengths, 1)
+    shape = q.shape
+    q4 = q.unsqueeze(1) if len(shape) == 3 else q
+    N, Q, H, L = q4.shape
+    R, rope_q = 0, (None, (0, 0, 0))
+    if q_rope is not None:
+        _operand(what, "q_rope", q_rope)
+        r4 = q_rope.unsqueeze(1) if len(shape) == 3 else q_rope
+        R = r4.shape[3]
+        if r4.shape[:3] != q4.shape[:3]:
+            raise KDAError(what, 3, "q_rope must be [N,(Q,)H,R]")
+        if R > 0:
+            rope_q = (r4.data_ptr(), r4.stride()[:3])
+    if fp8:
+        num_pages, page_size, Lc, Rc, *strides = _store(what, codes, scales, rope)
+        if Lc != L or Rc != R:
+            raise KDAError(what, 3, "cache rows hold %d + %d values, q and q_rope %d + %d" % (Lc, Rc, L, R))
+        head = (KDA_E4M3, codes.data_ptr(), scales.data_ptr(), rope.data_ptr() if R > 0 else None)
+    else:
+        if cache.dim() != 3:
+            raise KDAError(what, 3, "cache must be 3-D")
+        if cache.dtype != torch.bfloat16:
+            raise KDAError(what, 2, "cache must be bfloat16 or (codes, scales, rope), got %s" % cache.dtype)
+        num_pages, page_size, D = cache.shape
+        if D != L + R:
+            raise KDAError(what, 3, "cache rows hold %d values, q and q_rope %d" % (D, L + R))
+        strides = (_pages(what, "cache", cache, 1), 0, 0)
+        head = (KDA_BF16, cache.data_ptr(), None, None)
+    if page_table.shape[0] != N or lengths.shape[0] != N:
+        raise KDAError(what, 3, "page_table must be [N,max_pages] and lengths [N]")
+    if (page_table.shape[1] > 1 and page_table.stride(1) != 1) or not lengths.is_contiguous():
+        raise KDAError(what, 4, "page_table rows and lengths must be dense")
+    G, groups = 0, (None, None)
+    if cu_groups is not None:
+        _int32(what, "cu_groups", cu_groups, 1)
+        _int32(what, "shared", shared, 1)
+        G = shared.shape[0]
+        if cu_groups.shape[0] != G + 1:
+            raise KDAError(what, 3, "cu_groups must be [G+1] and shared [G]")
+        if not (cu_groups.is_contiguous() and shared.is_contiguous()):
+            raise KDAError(what, 4, "cu_groups and shared must be contiguous")
+        groups = (cu_groups.data_ptr(), shared.data_ptr())
+    made = []
+    out = _out(what, "out", out, shape, torch.bfloat16, dev, made)
+    if lse is not None or with_lse:
+        lse = _out(what, "lse", lse, shape[:-1], torch.float32, dev, made)
+    ws = _workspace(workspace, lib.kda_latent_shared_workspace_size(N, Q, H, L, G), dev, made)
+    a = LatentSharedArgs(N, Q, H, L, R, G, *head, num_pages, page_size, *strides, page_table.data_ptr(),
+                         page_table.stride(0), page_table.shape[1], lengths.data_ptr(), *groups, q4.data_ptr(),
+                         q4.stride()[:3], *rope_q, out.data_ptr(), None if lse is None else lse.data_ptr(), scale, *ws)
+    _call(what, dev, stream, made, lib.kda_latent_decode_fp8 if what == "kda_latent_decode_fp8" else
+          lib.kda_latent_decode_shared, a)
+    return out, lse
+
+
+def kda_latent_decode_fp8(codes: torch.Tensor, scales: torch.Tensor, rope: Optional[torch.Tensor],
+                          page_table: torch.Tensor, lengths: torch.Tensor, q: torch.Tensor,
+                          q_rope: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          with_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """:func:`kda_latent_decode` over a cache in 8 bits.
+
+    codes, scales, rope: the cache's tensors, as
+    :func:`kda_latent_quantize_scatter` writes them; any scale is taken, not only
+    powers of two.  The rest as for :func:`kda_latent_decode`, with the
+    workspace of :func:`kda_latent_shared_workspace_size` (G = 0).
+    """
+    return _decode_shared("kda_latent_decode_fp8", (codes, scales, rope), page_table, lengths, None, None, q, q_rope,
+                          scale, out, lse, with_lse, workspace, stream)
+
+
+def kda_latent_decode_shared(cache, page_table: torch.Tensor, lengths: torch.Tensor, cu_groups: torch.Tensor,
+                             shared: torch.Tensor, q: torch.Tensor, q_rope: Optional[torch.Tensor] = None,
+                             scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None, with_lse: bool = False,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """:func:`kda_latent_decode` for sequences that share their first tokens,
+    which are read and computed once for all of them.
+
+    cache: a 16-bit cache's tensor, or (codes, scales, rope) of one in 8 bits;
+    cu_groups: [G+1] int32, group g is the sequences cu_groups[g] ..
+    cu_groups[g+1] - 1; shared: [G] int32, how many first tokens its sequences
+    have in common (the same rows, as after a fork: they are read through the
+    table of the group's first sequence).  Sequences of no group share
+    nothing.  The rest, and the results, as for :func:`kda_latent_decode`; the
+    workspace has :func:`kda_latent_shared_workspace_size` bytes.
+    """
+    what = "kda_latent_decode_shared"
+    if cu_groups is None or shared is None:
+        raise KDAError(what, 1, "cu_groups and shared must be given")
+    return _decode_shared(what, cache, page_table, lengths, cu_groups, shared, q, q_rope, scale, out, lse, with_lse,
+                          workspace, stream)
 
 
 def _pool(what: str, table: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_size: int) -> PagePool:
