@@ -469,6 +469,11 @@ kda_status_t check_latent_shared(const kda_latent_shared_args_t* a) {
     if (!aligned(a->cache, 16)) return KDA_E_LAYOUT;
     store[0] = {a->cache, ((a->num_pages - 1) * a->page_stride + a->page_size * row) * 2};
   }
+  // (the kernel's page strides are 32 bits of bytes)
+  const int64_t far = (int64_t)1 << 32;
+  if (a->num_pages > 1 && (a->page_stride * (f8 ? 1 : 2) >= far ||
+                           (f8 && (a->scales_page_stride * 4 >= far || (a->R > 0 && a->rope_page_stride * 2 >= far)))))
+    return KDA_E_UNSUPPORTED;
   if (a->N == 0) return KDA_OK;
   if (!a->page_table || !a->lengths || !a->q || (a->R > 0 && !a->q_rope) || !a->out) return KDA_E_NULL;
   if (a->G > 0 && (!a->cu_groups || !a->shared)) return KDA_E_NULL;

@@ -39,6 +39,10 @@ __device__ __forceinline__ void load_lds16(const char* lane_address, unsigned ld
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(lane_address), "s"(lds)
                : "memory");
 }
+__device__ __forceinline__ void load_lds4(const char* base, unsigned offset, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dword %1, %0" ::"s"(base), "v"(offset), "s"(lds)
+               : "memory");
+}
 __device__ __forceinline__ void load_lds4(const void* lane_address, unsigned lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(lane_address), "s"(lds)
                : "memory");
@@ -135,6 +139,10 @@ __device__ __forceinline__ float sum_quarters(float x) {
 
 // The value of the first active lane, the same in all and known to be.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ const char* uniform(const char* x) {
+  const uint64_t v = (uint64_t)x;
+  return (const char*)(((uint64_t)(unsigned)uniform((int)(v >> 32)) << 32) | (unsigned)uniform((int)v));
+}
 
 // The value of lane ``src`` (uniform).
 __device__ __forceinline__ int64_t lane64(int64_t x, int src) {

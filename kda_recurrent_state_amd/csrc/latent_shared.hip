@@ -13,8 +13,10 @@
 // chunks of at least a workgroup's share, a chunk's tiles stand on the line for
 // one row block after another, and workgroups get equal shares of the line, neighbours on one
 // XCD: the row blocks of a chunk are computed at the same time behind one
-// L2, which then serves all but the first.  What one workgroup computes of one
-// chunk and row block, a piece, is written as output if it is all there is for
+// L2, which then serves all but the first.  A unit (a row block of a chunk) ends with
+// queries to load and outputs to write, kEnd tiles' time; entities of one chunk, of which a
+// share can hold many, have that much room on the line before each row block.  What one workgroup computes of one
+// unit, a piece, is written as output if it is all there is for
 // its sequence, otherwise with its maximum and sum to the workspace, and
 // the join kernel weighs the pieces of a row.  The plan is made on the device by one
 // workgroup, so a captured call follows its lengths, groups and tables.
@@ -34,9 +36,11 @@ using namespace latent;
 
 constexpr int kShares = 256;       // workgroups, one a CU
 constexpr int kPlanThreads = 1024;
+constexpr int kEnd = 4;            // room before a unit of an entity of one chunk
+constexpr int kPlanLds = 4096;     // entities whose places the plan keeps in LDS
 
 struct Entity {
-  int64_t base;            // place on the line
+  int64_t base, first;     // place on the line, and the number of its first tile
   int32_t tiles, row_blocks;
   int32_t chunks, chunk;   // and the tiles of one; the first ``longer`` ones have one more
   int32_t longer;
@@ -45,6 +49,12 @@ struct Entity {
   int32_t slot;            // of its first row block's pieces that no share cuts and that are not chunks
   int32_t group;           // of a sequence: the entity of its prefix, or -1
 
+  __device__ __forceinline__ int room() const { return chunks == 1 ? kEnd : 0; }
+  // place on the line, from the entity's, of row block rb of chunk k (its room, then its tiles)
+  __device__ __forceinline__ int64_t unit_begin(int k, int rb) const {
+    return (int64_t)chunk_begin(k) * row_blocks + (int64_t)rb * (chunk_tiles(k) + room());
+  }
+  __device__ __forceinline__ int64_t line() const { return (int64_t)row_blocks * (tiles + room()); }
   __device__ __forceinline__ int chunk_begin(int k) const { return k * chunk + min(k, longer); }
   __device__ __forceinline__ int chunk_tiles(int k) const { return chunk + (k < longer ? 1 : 0); }
 };
@@ -56,11 +66,12 @@ struct Start {  // where a workgroup begins: tile t of row block rb of chunk k o
 
 struct SharedParams {
   const char *lat, *rot, *scales;                // 16-bit cache: lat alone
-  int64_t lat_page, rot_page, scales_page;       // bytes
+  uint32_t lat_page, rot_page, scales_page;      // bytes
   int lat_row;                                   // bytes from token to token
   int num_pages, page_size, L, R;
   uint32_t page_mul;
   int page_shift;
+  int eights;                                    // whether page_size is a multiple of 8
   const int32_t* table;
   int64_t table_stride;
   int max_pages;
@@ -137,8 +148,12 @@ __device__ __forceinline__ T block_scan(T x, T* wsum, T* all) {
 __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams p, int MB) {
   __shared__ long long lsum[kPlanThreads / 64];
   __shared__ int isum[kPlanThreads / 64];
+  __shared__ long long places[kPlanLds], number[kShares + 1];
+  __shared__ int lbounds[kPlanThreads + 1], lprefix[kPlanThreads];
   const int own_blocks = (p.rows + MB - 1) / MB;
   const int tid = threadIdx.x, E = p.G + p.N;
+  // (in LDS where they fit: what follows searches them)
+  int *bounds = p.G <= kPlanThreads ? lbounds : p.bounds, *prefix = p.G <= kPlanThreads ? lprefix : p.prefix;
   // the groups' bounds: inside the batch, and not before an earlier one
   if (p.G > 0) {
     int carry = 0;
@@ -161,126 +176,145 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
       v = max(v, carry);
       carry = most;
       __syncthreads();
-      if (i <= p.G) p.bounds[i] = v;
+      if (i <= p.G) bounds[i] = v;
     }
     __syncthreads();
     for (int g = tid; g < p.G; g += kPlanThreads) {
-      const int n0 = p.bounds[g], n1 = p.bounds[g + 1];
+      const int n0 = bounds[g], n1 = bounds[g + 1];
       int pre = 0;
       if (n1 - n0 >= 2) {
         const int len = seq_tokens(p, n0), s = p.shared[g];
         pre = s < 0 ? 0 : (s > len ? len : s);
       }
-      p.prefix[g] = pre;
+      prefix[g] = pre;
     }
     __syncthreads();
   }
-  // the entities, and the length of the line
-  long long total = 0;
-  for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
-    const int e = e0 + tid;
-    long long mine = 0;
-    if (e < E) {
-      Entity x;
-      x.group = -1;
-      if (e < p.G) {
-        const int n0 = p.bounds[e], n1 = p.bounds[e + 1];
-        x.row0 = n0 * p.rows;
-        x.rows = (n1 - n0) * p.rows;
-        x.seq = n0;
-        x.t0 = 0;
-        x.t1 = p.prefix[e];
-        x.slot = 2 * kShares + p.N * own_blocks + x.row0 / MB + e;  // (an earlier group's are fewer)
-      } else {
-        const int n = e - p.G;
-        x.row0 = n * p.rows;
-        x.rows = p.rows;
-        x.seq = n;
-        x.t0 = 0;
-        x.t1 = seq_tokens(p, n);
-        x.slot = 2 * kShares + n * own_blocks;
-        if (p.G > 0 && n >= p.bounds[0] && n < p.bounds[p.G]) {
-          int lo = 0, hi = p.G;  // the last group that begins at n or before
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.bounds[mid] <= n) lo = mid; else hi = mid;
-          }
-          x.t0 = min(p.prefix[lo], x.t1);
-          if (x.t0 > 0) x.group = lo;
+  // entity e, but for its place and chunks
+  auto entity = [&](int e) {
+    Entity x;
+    x.group = -1;
+    x.t0 = 0;
+    x.base = x.first = 0;
+    x.chunks = 0;
+    x.chunk = 1;
+    x.longer = 0;
+    if (e < p.G) {
+      const int n0 = bounds[e], n1 = bounds[e + 1];
+      x.row0 = n0 * p.rows;
+      x.rows = (n1 - n0) * p.rows;
+      x.seq = n0;
+      x.t1 = prefix[e];
+      x.slot = 2 * kShares + p.N * own_blocks + x.row0 / MB + e;  // (an earlier group's are fewer)
+    } else {
+      const int n = e - p.G;
+      x.row0 = n * p.rows;
+      x.rows = p.rows;
+      x.seq = n;
+      x.t1 = seq_tokens(p, n);
+      x.slot = 2 * kShares + n * own_blocks;
+      if (p.G > 0 && n >= bounds[0] && n < bounds[p.G]) {
+        int lo = 0, hi = p.G;  // the last group that begins at n or before
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (bounds[mid] <= n) lo = mid; else hi = mid;
         }
+        x.t0 = min(prefix[lo], x.t1);
+        if (x.t0 > 0) x.group = lo;
       }
-      x.tiles = (int)(((int64_t)x.t1 - x.t0 + kTile - 1) / kTile);
-      x.row_blocks = (x.rows + MB - 1) / MB;
-      mine = (long long)x.tiles * x.row_blocks;
-      p.ents[e] = x;
     }
-    long long all;
-    block_scan(mine, lsum, &all);
+    x.tiles = (int)(((int64_t)x.t1 - x.t0 + kTile - 1) / kTile);
+    x.row_blocks = (x.rows + MB - 1) / MB;
+    return x;
+  };
+  // the line's length with room for every entity, and from that the chunks; then the line
+  long long total = 0;
+  Entity mine;  // the last one of this thread: the only one, mostly
+  for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
+    long long n = 0, all;
+    if (e0 + tid < E) {
+      mine = entity(e0 + tid);
+      n = mine.tiles > 0 ? (long long)mine.row_blocks * (mine.tiles + kEnd) : 0;
+    }
+    block_scan(n, lsum, &all);
     total += all;
   }
-  const Shares sh = shares_of(total);
-  const int share = sh.quot > (1 << 30) ? 1 << 30 : (int)sh.quot;
-  long long base = 0;
+  const long long quot = shares_of(total).quot;
+  const int share = quot > (1 << 30) ? 1 << 30 : (int)quot;
+  long long base = 0, first = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
     const int e = e0 + tid;
-    int tiles = 0, blocks = 0;
+    long long n = 0, tiles = 0, all, all_tiles;
     if (e < E) {
-      tiles = p.ents[e].tiles;
-      blocks = p.ents[e].row_blocks;
+      if (E > kPlanThreads) mine = entity(e);
+      if (mine.tiles > 0) {
+        mine.chunks = max(1, mine.tiles / share);
+        mine.chunk = mine.tiles / mine.chunks;
+        mine.longer = mine.tiles % mine.chunks;
+        n = mine.line();
+        tiles = (long long)mine.tiles * mine.row_blocks;
+      }
     }
-    const long long mine = (long long)tiles * blocks;
-    long long all;
-    const long long to = base + block_scan(mine, lsum, &all);
+    const long long upto = block_scan(n, lsum, &all), tiles_upto = block_scan(tiles, lsum, &all_tiles);
     if (e < E) {
-      const int chunks = mine == 0 ? 0 : max(1, tiles / share);
-      p.ents[e].base = to - mine;
-      p.ents[e].chunks = chunks;
-      p.ents[e].chunk = chunks > 0 ? tiles / chunks : 1;
-      p.ents[e].longer = chunks > 0 ? tiles % chunks : 0;
+      mine.base = base + upto - n;
+      mine.first = first + tiles_upto - tiles;
+      p.ents[e] = mine;
+      if (e < kPlanLds) places[e] = mine.base;
     }
     base += all;
+    first += all_tiles;
   }
-  if (tid == 0) *p.total = total;
+  if (tid == 0) *p.total = base;
+  if (tid < kShares) p.starts[tid].left = 0;
   __syncthreads();
-  if (tid < kShares) {
-    const int per = (int)((sh.count + 7) / 8), w = (tid & 7) * per + (tid >> 3);
-    Start s = {};
-    if ((tid >> 3) < per && w < sh.count) {
-      const int64_t at = share_begin(sh, w);
-      int lo = 0, hi = E;  // the last entity that begins there or before: it holds the tile, if empty ones at its
-      while (hi - lo > 1) {  // place are before it
-        const int mid = (lo + hi) >> 1;
-        if (p.ents[mid].base <= at) lo = mid; else hi = mid;
-      }
-      s.ent = p.ents[lo];
-      s.e = lo;
-      s.w = w;
-      s.left = (int)(share_begin(sh, w + 1) - at);
-      const int64_t in = at - s.ent.base;
-      const int y = (int)(in / s.ent.row_blocks), longer = s.ent.longer * (s.ent.chunk + 1);
-      s.k = y < longer ? y / (s.ent.chunk + 1) : s.ent.longer + (y - longer) / s.ent.chunk;
-      const int64_t rest = in - (int64_t)s.ent.chunk_begin(s.k) * s.ent.row_blocks;
-      s.rb = (int)(rest / s.ent.chunk_tiles(s.k));
-      s.t = (int)(rest - (int64_t)s.rb * s.ent.chunk_tiles(s.k));
+  const Shares sh = shares_of(base);
+  Start s;
+  if (tid < sh.count) {
+    const int64_t from = share_begin(sh, tid);
+    auto place = [&](int e) { return E <= kPlanLds ? places[e] : (long long)p.ents[e].base; };
+    int lo = 0, hi = E;  // the last entity that begins there or before: it holds the place, if empty ones at its
+    while (hi - lo > 1) {  // place are before it
+      const int mid = (lo + hi) >> 1;
+      if (place(mid) <= from) lo = mid; else hi = mid;
     }
-    p.starts[tid] = s;
+    // the unit and tile of that place; a unit's room counts as its first tile
+    s.ent = p.ents[lo];
+    const Entity& x = s.ent;
+    const int64_t in = from - x.base;
+    if (x.chunks == 1) {
+      s.k = 0;
+      s.rb = (int)(in / (x.tiles + kEnd));
+    } else {
+      const int y = (int)(in / x.row_blocks), longer = x.longer * (x.chunk + 1);
+      s.k = y < longer ? y / (x.chunk + 1) : x.longer + (y - longer) / x.chunk;
+      s.rb = (int)((in - x.unit_begin(s.k, 0)) / x.chunk_tiles(s.k));
+    }
+    const int64_t rest = in - x.unit_begin(s.k, s.rb) - x.room();
+    s.t = rest > 0 ? (int)rest : 0;
+    s.e = lo;
+    s.w = tid;
+    number[tid] = x.first + (int64_t)x.chunk_begin(s.k) * x.row_blocks + (int64_t)s.rb * x.chunk_tiles(s.k) + s.t;
+  }
+  if (tid == sh.count) number[tid] = first;
+  __syncthreads();
+  if (tid < sh.count) {
+    s.left = (int)(number[tid + 1] - number[tid]);
+    // neighbours to workgroups of one XCD, which are those of one number mod 8
+    const int per = (int)((sh.count + 7) / 8);
+    p.starts[tid % per * 8 + tid / per] = s;
   }
 }
 
-// Which tile, of which unit; the records are in scalar registers.
-struct Tile {
-  int seq, pos, end;        // tokens pos .. of this sequence, before end
-  int row0, rows, slot;     // query rows, and the unit's own place in the workspace
+// A unit: the query rows that go over a chunk together.
+struct Unit {
+  int row0, rows;  // query rows
+  int slot;        // its own place in the workspace
   int flags;
-  unsigned long long live;  // which rows are there
 };
-// tile of its unit; the unit is all there is of its entity for its rows; and of its sequence
-constexpr int kFirst = 1, kLast = 2, kSingle = 4, kAlone = 8;
-
-struct Walk {
-  Entity x;
-  int e, k, rb, t, tc;
-};
+// The unit is all there is of its entity for its rows; and of its sequence.
+constexpr int kSingle = 1, kAlone = 2;
+constexpr int kUnits = 8;  // records kept: the tiles under way are of four units at most
 
 template <typename T>
 __device__ __forceinline__ T scalar_load(const T* at) {
@@ -295,197 +329,238 @@ __device__ __forceinline__ T scalar_load(const T* at) {
   return r;
 }
 
+// A cache's kind: its tile, the stages that fit into the LDS, and whether a tile's
+// values are multiplied beside the next one's scores (kLag: the weights' exponentials
+// and exchanges then run beside matrix products, and one barrier a tile does).
 template <bool F8, int LP, int RP, int NB, bool kPad>
 struct Kind {
   typedef Bf16Tile<LP, RP, NB, kPad, true> D;
   static constexpr int kStages = 2, kStageBytes = D::kStage * 2;
+  static constexpr bool kLag = false;
 };
 template <int LP, int RP, int NB, bool kPad>
 struct Kind<true, LP, RP, NB, kPad> {
   typedef Fp8Tile<LP, RP, NB, kPad> D;
   static constexpr int kStages = 3, kStageBytes = D::kStage;
+  static constexpr bool kLag = NB == 4;
 };
 
 template <bool F8, int LP, int RP, int NB, bool kPad>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_shared_kernel(SharedParams p) {
   using K = Kind<F8, LP, RP, NB, kPad>;
   using D = typename K::D;
+  constexpr bool kLag = K::kLag;
   constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG, TB = D::TB, NS = K::kStages;
+  constexpr int kAhead = kLag ? 1 : NS - 1;  // tiles fetched ahead of the one scored
   constexpr unsigned kStageBytes = K::kStageBytes, kRotaryBytes = RP > 0 ? kTile * RP * 2 : 16;
   __shared__ __attribute__((aligned(16))) char stage[NS][kStageBytes];
   __shared__ __attribute__((aligned(16))) char rotary[NS][kRotaryBytes];
   __shared__ __attribute__((aligned(16))) float tscale[NS][F8 ? kTile : 4];
-  __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kTile];
+  __shared__ __attribute__((aligned(16))) __bf16 prob[kLag ? 2 : 1][MB * kTile];
+  __shared__ __attribute__((aligned(16))) int4 units[kUnits];
   __shared__ float smax[TG][MB];  // of a tile; at a piece's end the sums
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
   __shared__ int32_t pages[2][kWaves][64];  // page of token lane of the tile located next
-  __shared__ int grown[2];        // whether a row's maximum has grown much in this tile
+  __shared__ int grown[3];        // whether a row's maximum has grown much in this tile
+  // What is needed between units alone, so that it takes no scalar registers
+  // within them (they do not hold everything, and what they do not hold is moved
+  // to and from vector registers in every tile).
+  __shared__ SharedParams cold;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, lg = lane >> 4;
   const Start start = scalar_load(p.starts + blockIdx.x);
   if (start.left == 0) return;
-  if (tid < 2) grown[tid] = 0;
+  if (tid == 0) cold = p;
+  if (tid < 3) grown[tid] = 0;
   if (kPad) {
     u32x4 *st = reinterpret_cast<u32x4*>(stage), *ro = reinterpret_cast<u32x4*>(rotary);
     for (unsigned i = tid; i < sizeof(stage) / 16; i += kThreads) st[i] = u32x4{0, 0, 0, 0};
     for (unsigned i = tid; i < sizeof(rotary) / 16; i += kThreads) ro[i] = u32x4{0, 0, 0, 0};
   }
+  __syncthreads();
   const bool scoring = wave < D::kScoring;
   const int rblock = wave % NB;     // query rows this wave scores
   const int tg = (wave / NB) % TG;  // and tokens
-  __syncthreads();
+  const int w = start.w;
 
-  // ---- the tiles of the share, one after another
-  Walk walk;
-  walk.x = start.ent;
-  walk.e = start.e;
-  walk.k = start.k;
-  walk.rb = start.rb;
-  walk.t = start.t;
-  walk.tc = walk.x.chunk_tiles(walk.k);
-  auto here = [&]() {
-    Tile x;
-    x.seq = walk.x.seq;
-    x.pos = walk.x.t0 + (walk.x.chunk_begin(walk.k) + walk.t) * kTile;
-    x.end = walk.x.t1;
-    x.row0 = walk.x.row0 + walk.rb * MB;
-    x.rows = min(MB, walk.x.rows - walk.rb * MB);
-    x.slot = walk.x.slot + walk.rb;
-    x.flags = (walk.t == 0 ? kFirst : 0) | (walk.t == walk.tc - 1 ? kLast : 0) |
-              (walk.x.chunks == 1 ? kSingle : 0) | (walk.x.chunks == 1 && walk.e >= p.G && walk.x.t0 == 0 ? kAlone : 0);
-    x.live = 0;
-    return x;
+  // ---- the tiles of the share, one after another; what is kept of the last one asked for
+  int e = start.e, k = start.k, rb = start.rb;  // its unit
+  int rem, pos, end;                            // tiles from it to its unit's last; its tokens pos .. before end
+  const char* row_pages;                        // its sequence's row of the table
+  int asked_unit = 0;
+  auto enter = [&](const Entity& x, int t) {
+    rem = x.chunk_tiles(k) - t;
+    pos = x.t0 + (x.chunk_begin(k) + t) * kTile;
+    end = x.t1;
+    row_pages = uniform(reinterpret_cast<const char*>(cold.table + x.seq * cold.table_stride));
+    if (tid == 0) {
+      const int flags = x.chunks != 1 ? 0 : (e >= cold.G && x.t0 == 0 ? kSingle | kAlone : kSingle);
+      units[asked_unit % kUnits] = make_int4(x.row0 + rb * MB, min(MB, x.rows - rb * MB), x.slot + rb, flags);
+    }
   };
   auto follow = [&]() {  // (there is a next tile)
-    if (++walk.t < walk.tc) return;
-    walk.t = 0;
-    if (++walk.rb < walk.x.row_blocks) return;
-    walk.rb = 0;
-    if (++walk.k == walk.x.chunks) {
-      walk.k = 0;
-      do walk.x = scalar_load(p.ents + ++walk.e);
-      while (walk.x.chunks == 0);
+    pos += kTile;
+    if (--rem > 0) return;
+    auto entity = [&]() {
+      return scalar_load(reinterpret_cast<const Entity*>(uniform(reinterpret_cast<const char*>(cold.ents + e))));
+    };
+    Entity x = entity();
+    if (++rb == x.row_blocks) {
+      rb = 0;
+      if (++k == x.chunks) {
+        k = 0;
+        do {
+          ++e;
+          x = entity();
+        } while (x.chunks == 0);
+      }
     }
-    walk.tc = walk.x.chunk_tiles(walk.k);
+    ++asked_unit;
+    enter(x, 0);
+  };
+  auto unit_of = [&](int i) {
+    const int4 v = units[i % kUnits];
+    return Unit{uniform(v.x), uniform(v.y), uniform(v.z), uniform(v.w)};
   };
 
-  // where the page of token pos + lane of a tile is (the last one's for lanes
-  // behind the end), and that row's place; -1: no such row
-  auto page_of = [&](int pos) { return (unsigned)(((uint64_t)(unsigned)pos * p.page_mul) >> p.page_shift); };
-  auto lookup = [&](const Tile& x) {
-    const int pos = x.pos + lane;
-    return p.table + x.seq * p.table_stride + page_of(pos < x.end ? pos : x.end - 1);
+  // A tile under way.
+  struct Tile {
+    int pos, last;            // its first token; whether it is its unit's last tile
+    unsigned long long live;  // which rows are there
   };
-  const char *at, *rot_at, *scale_at;  // rows of the last tile located (lane i: token i)
-  // Rows that are not there are fetched from the first one that is (their
-  // weights are 0); a tile without any is not fetched and not computed.
-  auto locate = [&](int page, Tile& x) {
-    const int pos = x.pos + lane;
-    const bool there = pos < x.end && (unsigned)page < (unsigned)p.num_pages;
-    int off = pos - (int)page_of(pos) * p.page_size;
-    x.live = __ballot(there);
-    if (x.live != ~0ull) {
-      const int some = x.live != 0 ? __ffsll(x.live) - 1 : 0;
-      const int spage = x.live != 0 ? __builtin_amdgcn_readlane(page, some) : 0;
-      const int soff = x.live != 0 ? __builtin_amdgcn_readlane(off, some) : 0;
+  auto page_of = [&](int at) { return (unsigned)(((uint64_t)(unsigned)at * p.page_mul) >> p.page_shift); };
+  // where the page of token pos + lane is (the last one's for lanes behind the end)
+  auto lookup = [&]() { return row_pages + (uint64_t)page_of(min(pos + lane, end - 1)) * 4; };
+
+  // Where a tile's rows are.  Near: all are there, and each wave's 8 lie one behind
+  // the other (pages of a multiple of 8 tokens, a tile that begins at one);
+  // ``at`` is where, the same in all lanes.  Otherwise it is where token pos + lane is;
+  // rows that are not there are fetched from the
+  // first one that is (their weights are 0); a tile without any is not
+  // fetched and not computed.
+  struct Rows {
+    const char *lat, *rot, *scale;
+  };
+  struct Place {
+    bool near;
+    Rows at;
+  };
+  auto place_at = [&](unsigned page, unsigned off) {
+    Rows x;
+    x.rot = x.scale = nullptr;
+    x.lat = p.lat + (uint64_t)page * p.lat_page + (uint64_t)off * p.lat_row;
+    if (F8) {
+      x.scale = p.scales + (uint64_t)page * p.scales_page + (uint64_t)off * 4;
+      if (RP > 0) x.rot = p.rot + (uint64_t)page * p.rot_page + (uint64_t)off * (unsigned)(2 * p.R);
+    }
+    return x;
+  };
+  auto locate = [&](int page, int at, int before, Tile& x) {
+    x.live = __ballot(at + lane < before && (unsigned)page < (unsigned)p.num_pages);
+    if (x.live == ~0ull && p.eights && at % 8 == 0) {
+      const int first = at + 8 * wave;
+      const Rows y = place_at(__builtin_amdgcn_readlane(page, 8 * wave), first - page_of(first) * p.page_size);
+      return Place{true, y};
+    }
+    int off = at + lane - (int)page_of(at + lane) * p.page_size;
+    if (x.live != 0) {
+      const int some = __ffsll(x.live) - 1;
+      const bool there = x.live >> lane & 1;
+      const int spage = __builtin_amdgcn_readlane(page, some), soff = __builtin_amdgcn_readlane(off, some);
       page = there ? page : spage;
       off = there ? off : soff;
     }
-    at = p.lat + page * p.lat_page + (int64_t)off * p.lat_row;
-    if (F8) {
-      scale_at = p.scales + page * p.scales_page + (int64_t)off * 4;
-      if (RP > 0) rot_at = p.rot + page * p.rot_page + (int64_t)off * (2 * p.R);
-    }
+    return Place{false, place_at(page, off)};
   };
-  const unsigned stage_at = lds_offset(stage), rotary_at = lds_offset(rotary), scale_lds = lds_offset(tscale);
+  const unsigned stage_at = lds_offset(stage), rotary_at = lds_offset(rotary), scale_at = lds_offset(tscale);
   const unsigned pages_at = lds_offset(pages[0][wave]);
   constexpr unsigned kPagesBytes = sizeof(pages[0]), kScaleBytes = sizeof(tscale[0]);
-  const typename D::Columns columns = D::columns(p.L, p.R, wave, lane);
+  typename D::Columns columns;
+  // (anew for each tile: the loads' addresses then take no registers beside the products)
+  auto begin_loads = [&]() { columns = D::columns(p.L, p.R, wave, keep_here(tid & 63)); };
+  // Load i, 0 <= i < kLoads, of a tile that is near to stage ``to``.
+  auto fetch = [&](const Rows& y, int i, int to) {
+    const unsigned lat = stage_at + to * kStageBytes, rot = rotary_at + to * kRotaryBytes;
+    if constexpr (F8)
+      D::fetch_near(i, y.lat, y.rot, y.scale, kPad ? p.L : LP, kPad ? p.R : RP, wave, lane, columns, lat, rot,
+                    scale_at + to * kScaleBytes);
+    else
+      D::fetch_near(i, y.lat, kPad ? p.lat_row : 2 * (LP + RP), wave, lane, columns, lat, rot);
+  };
+  // All of a tile's.
+  auto fetch_all = [&](const Place& y, int to) {
+    const unsigned lat = stage_at + to * kStageBytes, rot = rotary_at + to * kRotaryBytes;
+#pragma unroll
+    for (int i = 0; i < D::kLoads; ++i) {
+      if (y.near)
+        fetch(y.at, i, to);
+      else if constexpr (F8)
+        D::fetch_far(i, y.at.lat, y.at.rot, y.at.scale, wave, lane, columns, lat, rot, scale_at + to * kScaleBytes);
+      else
+        D::fetch_far(i, y.at.lat, wave, lane, columns, lat, rot);
+    }
+  };
+
+  int left = start.left - 1;  // tiles behind the one scored
+  int ahead = left;           // and behind the last one asked for
+  Tile ring[kAhead + 1];      // the one scored, and those fetched ahead
+  auto asked = [&]() { return Tile{pos, rem == 1, 0}; };
+  auto ask = [&](int to) {
+    follow();
+    load_lds4(lookup(), uniform(pages_at + to * kPagesBytes));
+    --ahead;
+  };
+  {
+    enter(start.ent, start.t);
+    ring[0] = asked();
+    const int page0 = *reinterpret_cast<const int32_t*>(lookup()), end0 = end;
+    int page1 = 0, end1 = 0;
+    if (kAhead == 2 && ahead > 0) {
+      follow();
+      --ahead;
+      ring[kAhead - 1] = asked();
+      page1 = *reinterpret_cast<const int32_t*>(lookup());
+      end1 = end;
+    }
+    if (ahead > 0) ask(0);
+    const Place y = locate(page0, ring[0].pos, end0, ring[0]);
+    begin_loads();
+    if (ring[0].live) fetch_all(y, 0);
+    if (kAhead == 2 && left > 0) {
+      const Place z = locate(page1, ring[kAhead - 1].pos, end1, ring[kAhead - 1]);
+      if (ring[kAhead - 1].live) fetch_all(z, 1);
+    }
+    __syncthreads();  // (the units' records)
+  }
 
   // ---- queries
-  typedef bf16x8 Q16[F8 ? 1 : KS];
-  Q16 qf;
+  bf16x8 qf[KS];
   int sees = 0;  // tokens that row ln of the wave's block sees
-  struct QueryAt {
-    const __bf16 *q, *qr;
-  };
-  auto row_at = [&](const Tile& x) {
+  auto load_q = [&](const Unit& u) {
     // (rows behind the unit's last one get its first one's queries; they are not written)
-    const int r = keep_here(rblock * 16 + ln);
-    const unsigned row = x.row0 + (r < x.rows ? r : 0);
+    const int r = keep_here(rblock * 16 + ln), lg = keep_here(lane >> 4);
+    const unsigned row = u.row0 + (r < u.rows ? r : 0);
+    const SharedParams& p = cold;
     const unsigned n = row / (unsigned)p.rows, in = row - n * p.rows, qi = in / (unsigned)p.H, h = in - qi * p.H;
-    sees = seq_tokens(p, (int)n) - (p.Q - 1 - (int)qi);
-    return QueryAt{p.q + n * p.qs[0] + qi * p.qs[1] + h * p.qs[2], p.qr + n * p.qrs[0] + qi * p.qrs[1] + h * p.qrs[2]};
-  };
-  auto load_q16 = [&](const Tile& x) {
-    const QueryAt a = row_at(x);
-    const int lg8 = 8 * keep_here(lane >> 4);
+    const __bf16 *q = p.q + n * p.qs[0] + qi * p.qs[1] + h * p.qs[2], *qr = p.qr + n * p.qrs[0] + qi * p.qrs[1] + h * p.qrs[2];
 #pragma unroll
-    for (int k = 0; k < (F8 ? 0 : KS); ++k) {
-      const int c = 32 * k + lg8;
+    for (int i = 0; i < KS; ++i) {
+      int c = 32 * i + 8 * lg;
+      if constexpr (F8)
+        c = D::component(i, lg);
+      else if (i >= LP / 32)
+        c -= LP;
       bf16x8 y = {};
-      if (!kPad || (k < LP / 32 ? c < p.L : c - LP < p.R))
-        y = *reinterpret_cast<const bf16x8*>(k < LP / 32 ? a.q + c : a.qr + (c - LP));
-      qf[k] = y;
+      if (!kPad || c < (i < LP / 32 ? p.L : p.R)) y = *reinterpret_cast<const bf16x8*>((i < LP / 32 ? q : qr) + c);
+      qf[i] = y;
     }
+    sees = seq_tokens(p, (int)n) - (p.Q - 1 - (int)qi);
   };
-
-  int left = start.left - 1;  // tiles behind the one computed
-  int ahead = left;           // and behind the last one asked for
-  Tile ring[NS];              // the one computed, and those under way
-  Tile ask;
-  auto ask_next = [&](int to) {
-    follow();
-    ask = here();
-    load_lds4(lookup(ask), uniform(pages_at + to * kPagesBytes));
-    --ahead;
-  };
-  [[maybe_unused]] auto fetch16 = [&](int i, int to) {
-    if constexpr (!F8) D::fetch(i, at, wave, lane, columns, stage_at + to * kStageBytes);
-  };
-  auto fetch_all = [&](int to) {
-    if constexpr (F8) {
-      D::fetch(at, rot_at, scale_at, wave, lane, columns, stage_at + to * kStageBytes,
-               rotary_at + to * kRotaryBytes, scale_lds + to * kScaleBytes);
-    } else {
-      D::fetch_rotary(at, wave, lane, columns, rotary_at + to * kRotaryBytes);
-#pragma unroll
-      for (int i = 0; i < D::kLat; ++i) D::fetch(i, at, wave, lane, columns, stage_at + to * kStageBytes);
-    }
-  };
-  ring[0] = here();
-  const int page0 = *lookup(ring[0]);
-  int page1 = 0;
-  if (NS == 3 && ahead > 0) {
-    follow();
-    ring[1] = here();
-    --ahead;
-    page1 = *lookup(ring[1]);
-  }
-  if (ahead > 0) ask_next(0);
-  locate(page0, ring[0]);
-  if (ring[0].live) fetch_all(0);
-  if (NS == 3 && left > 0) {
-    locate(page1, ring[1]);
-    if (ring[1].live) fetch_all(1);
-  }
-
-  typedef typename std::conditional<F8, Fp8Tile<LP, RP, NB, kPad>, Fp8Tile<128, RP, NB, kPad>>::type F;
-  typename F::Query q8;
-  // (after the output has left its registers)
-  [[maybe_unused]] auto load_q8 = [&](const Tile& x) {
-    const QueryAt a = row_at(x);
-    typename F::Raw raw;
-    F::request(a.q, a.qr, p.L, p.R, keep_here(lane >> 4), raw);
-    F::split(raw, q8);
-  };
-  if constexpr (F8)
-    load_q8(ring[0]);
-  else
-    load_q16(ring[0]);
-  bool begun = ring[0].flags & kFirst;  // whether the piece begins where its unit does
-  int later = 0;                        // 1: behind the share's first piece
+  int unit = 0;               // of the tile whose values come next
+  bool begun = start.t == 0;  // whether the piece begins where its unit does
+  int later = 0;              // 1: behind the share's first piece
+  load_q(unit_of(0));
 
   float m, l;  // of row ln of the wave's block, over its tokens; units of scale2 s
   bool far;    // whether one of the wave's rows is_far
@@ -501,11 +576,168 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   };
   clear();
 
-  int st = 0;  // the stage of the tile computed
-  for (int par = 0;; par ^= 1) {
-    // this tile has landed (in 8 bits the next one's loads may be under way, and
-    // the lookup before them is done), and the readers of the one before are done
+  // ---- the scores of a tile and their weights
+  float sum = 0.f, fac = 1.f;
+  f32x4 s[TB], sc[TB];
+  // Weights of the scores against the maximum in use, for the matrix unit in bf16;
+  // their sum stays in fp32.  In 8 bits the tokens' scales go into them before
+  // they are rounded.
+  auto weigh = [&](float base, __bf16* to) {
+    sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      bf16x4 pb;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = exp2_hw(fmaf(s[j][i], p.scale2, -base));
+        sum += w;
+        pb[i] = (__bf16)(F8 ? w * sc[j][i] : w);
+      }
+      const int tk = 16 * (TB * tg + j) + 4 * lg;
+      *reinterpret_cast<bf16x4*>(to + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+    }
+  };
+  auto score = [&](const Tile& x, int st, int par, int flag, const auto& load) {
+    const char *lat = stage[0] + st * kStageBytes, *rot = rotary[0] + st * kRotaryBytes;
     if constexpr (F8) {
+      D::scores(lat + 16 * TB * tg * LP, rot + 16 * TB * tg * RP * 2, tscale[0] + st * kTile + 16 * TB * tg, qf, ln, lg, s, sc,
+                load);
+    } else {
+      D::scores(reinterpret_cast<const __bf16*>(lat) + (16 * TB * tg + ln) * LP,
+                reinterpret_cast<const __bf16*>(rot) + (16 * TB * tg + ln) * RP, qf, ln, lg, s, load);
+    }
+    if (x.live != ~0ull || __any(x.pos + kTile > sees)) {
+#pragma unroll
+      for (int j = 0; j < TB; ++j) {
+        // of the lane's four tokens: how many are seen, and which are there
+        const int at4 = 16 * (TB * tg + j) + 4 * lg, n = sees - x.pos - at4;
+        const unsigned there = (unsigned)(x.live >> at4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i >= n || !(there >> i & 1)) {
+            s[j][i] = -INFINITY;
+            if (F8) sc[j][i] = 0.f;  // (it may be NaN)
+          }
+      }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
+    mx = max_halves(max_quarters(mx)) * p.scale2;
+    if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
+    // The maximum in use follows the true one only when that is larger by
+    // more than 8 (a factor of 256), as in latent decode.
+    if (__any(mx > m + 8.f) || far) {
+      if (lane == 0) grown[flag] = 1;
+    }
+    weigh(m == -INFINITY ? 0.f : m, prob[kLag ? par : 0]);
+  };
+  // Behind a barrier, where ``grown`` is set: the new maxima, the weights again, and
+  // the older output's factor.
+  auto grow = [&](int par) {
+    if (scoring) {
+      float mx = smax[0][rblock * 16 + ln];
+#pragma unroll
+      for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
+      const float mn = mx > m + 8.f ? mx : m;
+      fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
+      m = mn;
+      if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
+    }
+    lds_barrier();  // (all have read the maxima; the weights are written again)
+    if (scoring) {
+      float base = m == -INFINITY ? 0.f : m;
+      far = __any(is_far(m));
+      if (far && is_far(m)) {
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[j][i] = from_far(s[j][i], p.scale2, m);
+        base = 0.f;
+      }
+      weigh(base, prob[kLag ? par : 0]);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const float f = sfac[j * 16 + ln];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i][j] *= f;
+    }
+    lds_barrier();
+  };
+  auto multiply = [&](int st, int par) {
+    if constexpr (F8)
+      D::values(stage[0] + st * kStageBytes, prob[kLag ? par : 0], wave, ln, lg, acc);
+    else
+      D::values(reinterpret_cast<const __bf16*>(stage[0] + st * kStageBytes), prob[0], wave, ln, lg, acc);
+  };
+
+  // ---- the end of a piece, which is its unit's end too or not
+  auto finish = [&](bool unit_ends) {
+    const SharedParams& p = cold;
+    const Unit u = unit_of(unit);
+    const float lsum = sum_halves(sum_quarters(l));
+    lds_barrier();
+    const int ln = keep_here(lane & 15), lg = keep_here(lane >> 4);
+    if (scoring && lg == 0) {
+      smax[tg][rblock * 16 + ln] = lsum;
+      if (tg == 0) sfac[rblock * 16 + ln] = m;
+    }
+    lds_barrier();
+    const bool whole = begun && unit_ends, direct = whole && (u.flags & kAlone);
+    const int64_t slot = whole && (u.flags & kSingle) ? u.slot : 2 * w + later;
+    const int col0 = wave * (MT * 16) + 4 * lg;
+    __bf16* out = p.out + ((int64_t)u.row0 + ln) * p.L + col0;
+    float* part = p.part + (slot * MB + ln) * p.L + col0;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      float sum = smax[0][j * 16 + ln];
+#pragma unroll
+      for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
+      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (j * 16 + ln < u.rows && col0 + 16 * i < p.L) {
+          const f32x4 o = acc[i][j] * inv;
+          if (direct) {
+            const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+            *reinterpret_cast<bf16x4*>(out + 16 * i) = ob;
+          } else {
+            *reinterpret_cast<f32x4*>(part + 16 * i) = o;
+          }
+        }
+      }
+      out += 16 * p.L;
+      part += 16 * p.L;
+    }
+    const int r = keep_here(tid);
+    if (r < u.rows) {
+      float sum = smax[0][r];
+#pragma unroll
+      for (int g = 1; g < TG; ++g) sum += smax[g][r];
+      if (!direct)
+        p.psum[slot * MB + r] = make_float2(sfac[r], sum);
+      else if (p.lse)
+        p.lse[(int64_t)u.row0 + r] = sum == 0.f ? -INFINITY : (sfac[r] + __log2f(sum)) * kLn2;
+    }
+    ++unit;
+    begun = true;
+    later = 1;
+  };
+  auto restart = [&]() {
+    if (kLag) lds_barrier();  // (the readers of a piece's sums and maxima are done)
+    load_q(unit_of(unit));
+    clear();
+  };
+
+  int st = 0;  // the stage of the tile scored
+  Tile prev = {0, 0, 0};  // kLag: the tile scored before it
+  for (int par = 0;; par ^= 1) {
+    // this tile has landed (the next one's loads may be under way, and the lookup
+    // before them is done), and the readers of the one before are done
+    if constexpr (F8 && kAhead == 2) {
       if (left > 0 && ring[1].live)
         wait_loads<D::kLoads>();
       else
@@ -514,186 +746,77 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       wait_loads<0>();
     }
     lds_barrier();
-    Tile& cur = ring[0];
-    const bool more = left > 0;          // a tile behind this one
-    const bool asked = left > NS - 2;    // and the one located now
-    const int to = st == 0 ? NS - 1 : st - 1;  // its stage: the one before
-    bool fetches = false;
-    if (asked) {
-      ring[NS - 1] = ask;
-      locate(pages[par][wave][lane], ring[NS - 1]);
-      if (ahead > 0) ask_next(par ^ 1);
-      fetches = ring[NS - 1].live != 0;
+    Tile cur = ring[0];
+    if (kLag && left < 0) cur.live = 0;  // (behind the last tile: its values are left)
+    [[maybe_unused]] const bool more = left > 0;  // a tile behind this one
+    const int to = kLag ? (st == NS - 1 ? 0 : st + 1) : (st == 0 ? NS - 1 : st - 1);  // the stage fetched to
+    if constexpr (kLag) {
+      if (prev.live && grown[st == 0 ? NS - 1 : st - 1]) grow(par ^ 1);
     }
-    if (tid == 0) grown[par ^ 1] = 0;
-    if constexpr (F8) {
-      if (fetches) fetch_all(to);
+    bool spread = false;  // whether the tile asked for is fetched along this one's scores
+    Rows rows = {nullptr, nullptr, nullptr};
+    if (left > kAhead - 1) {
+      Tile& x = ring[kAhead];
+      x = asked();
+      const int page = pages[par][wave][lane], before = end;
+      if (ahead > 0) ask(par ^ 1);
+      const Place y = locate(page, x.pos, before, x);
+      begin_loads();
+      spread = y.near && scoring && cur.live;
+      rows.lat = uniform(y.at.lat);
+      if (F8) {
+        rows.scale = uniform(y.at.scale);
+        if (RP > 0) rows.rot = uniform(y.at.rot);
+      }
+      if (!spread && x.live) fetch_all(y, to);
+    }
+    auto load = [&](int i) {
+      if (spread) fetch(rows, i, to);
+    };
+    constexpr int kFirst = D::kLoads - D::kLat;  // (a 16-bit tile's scores call for the latent loads alone)
+    if constexpr (!F8) {
+      if (kFirst > 0) load(0);
+    }
+    if constexpr (kLag) {
+      const int before = st == 0 ? NS - 1 : st - 1;
+      if (prev.live) l = l * fac + sum;
+      fac = 1.f;
+      if (tid == 0) grown[to] = 0;  // (read by all behind the barrier before, set behind the next one)
+      // Half of the waves (one a SIMD) score first, half multiply first, so that one
+      // wave's products run beside the other's conversions and exponentials.  Where a
+      // unit ends, all multiply first.
+      const bool ends = prev.last || left < 0, later_values = !ends && wave < kWaves / 2;
+      if (!later_values && prev.live) multiply(before, par ^ 1);
+      if (ends) {
+        finish(prev.last);
+        if (left < 0) return;
+        restart();
+      }
+      if (scoring && cur.live) score(cur, st, par, st, load);
+      if (later_values && prev.live) multiply(before, par ^ 1);
+      prev = cur;
     } else {
-      if (fetches) D::fetch_rotary(at, wave, lane, columns, rotary_at + to * kRotaryBytes);
-      if (fetches && !(scoring && cur.live)) {
-#pragma unroll
-        for (int i = 0; i < D::kLat; ++i) fetch16(i, to);
-      }
-    }
-    if (cur.live) {
-      float sum = 0.f, fac = 1.f;
-      f32x4 s[TB], sc[TB];
-      // Weights of the scores against the maximum in use, for the matrix unit
-      // in bf16; their sum stays in fp32.  In 8 bits the tokens' scales go into them
-      // before they are rounded.
-      auto weigh = [&](float base) {
-        sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-          bf16x4 pb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = exp2_hw(fmaf(s[j][i], p.scale2, -base));
-            sum += e;
-            pb[i] = (__bf16)(F8 ? e * sc[j][i] : e);
-          }
-          const int tk = 16 * (TB * tg + j) + 4 * lg;
-          *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
-        }
-      };
-      if (scoring) {
-        const char* lat = stage[0] + st * kStageBytes;
-        const __bf16* rot = reinterpret_cast<const __bf16*>(rotary[0] + st * kRotaryBytes);
-        if constexpr (F8) {
-          D::scores(lat + 16 * TB * tg * LP, rot + 16 * TB * tg * RP, tscale[st] + 16 * TB * tg, q8, ln, lg, s, sc);
-        } else {
-          D::scores(reinterpret_cast<const __bf16*>(lat) + (16 * TB * tg + ln) * LP, rot + (16 * TB * tg + ln) * RP, qf,
-                    ln, lg, s, [&](int i) {
-                      if (fetches) fetch16(i, to);
-                    });
-        }
-        if (cur.live != ~0ull || __any(cur.pos + kTile > sees)) {
-#pragma unroll
-          for (int j = 0; j < TB; ++j) {
-            // of the lane's four tokens: how many are seen, and which are there
-            const int at4 = 16 * (TB * tg + j) + 4 * lg, n = sees - cur.pos - at4;
-            const unsigned there = (unsigned)(cur.live >> at4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i >= n || !(there >> i & 1)) {
-                s[j][i] = -INFINITY;
-                if (F8) sc[j][i] = 0.f;  // (it may be NaN)
-              }
-          }
-        }
-        float mx = s[0][0];
-#pragma unroll
-        for (int j = 0; j < TB; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][i]);
-        mx = max_halves(max_quarters(mx)) * p.scale2;
-        if (lg == 0) smax[tg][rblock * 16 + ln] = mx;
-        // The maximum in use follows the true one only when that is larger by
-        // more than 8 (a factor of 256), as in latent decode.
-        if (__any(mx > m + 8.f) || far) {
-          if (lane == 0) grown[par] = 1;
-        }
-        weigh(m == -INFINITY ? 0.f : m);
-      }
-      lds_barrier();
-      if (grown[par]) {
-        if (scoring) {
-          float mx = smax[0][rblock * 16 + ln];
-#pragma unroll
-          for (int g = 1; g < TG; ++g) mx = fmaxf(mx, smax[g][rblock * 16 + ln]);
-          const float mn = mx > m + 8.f ? mx : m;
-          fac = exp2_hw(m - (mn == -INFINITY ? 0.f : mn));
-          m = mn;
-          if (tg == 0 && lg == 0) sfac[rblock * 16 + ln] = fac;
-        }
-        lds_barrier();  // (all have read the maxima; the weights are written again)
-        if (scoring) {
-          float base = m == -INFINITY ? 0.f : m;
-          far = __any(is_far(m));
-          if (far && is_far(m)) {
-#pragma unroll
-            for (int j = 0; j < TB; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[j][i] = from_far(s[j][i], p.scale2, m);
-            base = 0.f;
-          }
-          weigh(base);
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const float f = sfac[j * 16 + ln];
-#pragma unroll
-          for (int i = 0; i < MT; ++i) acc[i][j] *= f;
-        }
+      if (tid == 0) grown[par ^ 1] = 0;
+      if (cur.live) {
+        if (scoring)
+          score(cur, st, par, par, [&](int i) { load(F8 ? i : i + kFirst); });
         lds_barrier();
+        fac = 1.f;
+        if (grown[par]) grow(par);
+        l = l * fac + sum;
+        multiply(st, 0);
       }
-      l = l * fac + sum;
-      if constexpr (F8)
-        D::values(stage[0] + st * kStageBytes, prob, wave, ln, lg, acc);
-      else
-        D::values(reinterpret_cast<const __bf16*>(stage[0] + st * kStageBytes), prob, wave, ln, lg, acc);
-    }
-
-    if (!more || (cur.flags & kLast)) {
-      // ---- the end of a piece
-      if constexpr (!F8) {
-        if (more) load_q16(ring[1]);
-      }
-      l = sum_halves(sum_quarters(l));
-      lds_barrier();
-      const int ln = keep_here(lane & 15), lg = keep_here(lane >> 4);
-      if (scoring && lg == 0) {
-        smax[tg][rblock * 16 + ln] = l;
-        if (tg == 0) sfac[rblock * 16 + ln] = m;
-      }
-      lds_barrier();
-      const bool whole = begun && (cur.flags & kLast), direct = whole && (cur.flags & kAlone);
-      const int64_t slot = whole && (cur.flags & kSingle) ? cur.slot : 2 * start.w + later;
-      const int col0 = wave * (MT * 16) + 4 * lg;
-      __bf16* out = p.out + ((int64_t)cur.row0 + ln) * p.L + col0;
-      float* part = p.part + (slot * MB + ln) * p.L + col0;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        float sum = smax[0][j * 16 + ln];
-#pragma unroll
-        for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          if (j * 16 + ln < cur.rows && col0 + 16 * i < p.L) {
-            const f32x4 o = acc[i][j] * inv;
-            if (direct) {
-              const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-              *reinterpret_cast<bf16x4*>(out + 16 * i) = ob;
-            } else {
-              *reinterpret_cast<f32x4*>(part + 16 * i) = o;
-            }
-          }
+      if (!more || cur.last) {
+        finish(cur.last);
+        if (!more) {
+          wait_loads<0>();  // no load to LDS outlives the workgroup
+          return;
         }
-        out += 16 * p.L;
-        part += 16 * p.L;
+        restart();
       }
-      const int r = keep_here(tid);
-      if (r < cur.rows) {
-        float sum = smax[0][r];
-#pragma unroll
-        for (int g = 1; g < TG; ++g) sum += smax[g][r];
-        if (!direct)
-          p.psum[slot * MB + r] = make_float2(sfac[r], sum);
-        else if (p.lse)
-          p.lse[(int64_t)cur.row0 + r] = sum == 0.f ? -INFINITY : (sfac[r] + __log2f(sum)) * kLn2;
-      }
-      if (!more) {
-        wait_loads<0>();  // no load to LDS outlives the workgroup
-        return;
-      }
-      if constexpr (F8) load_q8(ring[1]);
-      clear();
-      begun = true;
-      later = 1;
     }
 #pragma unroll
-    for (int i = 0; i + 1 < NS; ++i) ring[i] = ring[i + 1];
+    for (int i = 0; i < kAhead; ++i) ring[i] = ring[i + 1];
     st = st == NS - 1 ? 0 : st + 1;
     --left;
   }
@@ -701,7 +824,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
 // Joins the pieces of a query row, its prefix's and its own, and writes the outputs of
 // empty sequences.  A wave takes one query row (8 columns a lane) and every
-// ``parts``-th chunk; grid: (groups of 8 / parts rows, sequences).
+// ``parts``-th piece; grid: (groups of 8 / parts rows, sequences).
 __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, int MB, int parts) {
   __shared__ f32x4 osum[kWaves][2][64];
   __shared__ float wtop[kWaves], wsum[kWaves];
@@ -720,39 +843,40 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
   // a sequence that one piece holds whole has its output
   if (own.t0 == 0 && own.chunks == 1) {
     const int rb = (blockIdx.x * (kWaves / parts)) / MB;  // (that of all the workgroup's rows)
-    const int64_t a = own.base + (int64_t)rb * own.tiles;
+    const int64_t a = own.base + own.unit_begin(0, rb) + own.room();
     if (share_at(sh, a) == share_at(sh, a + own.tiles - 1)) return;
   }
   float top = -INFINITY, sum = 0.f;
   f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   auto join = [&](const Entity& x) {
     const int in = (int)(grow - x.row0), rb = in / MB, r = in - rb * MB;
-    for (int k0 = 0; k0 < x.chunks; k0 += 64 * parts) {
-      // lane i: the shares of the row block in chunk k0 + part + i parts
-      const int mine = k0 + part + lane * parts;
-      const bool there = mine < x.chunks;
-      const int tc = x.chunk_tiles(mine);
-      const int64_t a = x.base + (int64_t)x.chunk_begin(mine) * x.row_blocks + (int64_t)rb * tc;
-      const int w0 = there ? share_at(sh, a) : 0, w1 = there ? share_at(sh, a + tc - 1) : 0;
-      // the pieces' places: the whole unit's own, or 2 w (+ 1 where others are before it in share w)
-      const int inside = there && a != share_begin(sh, w0) ? 1 : 0;
-      const int one = w0 == w1 && x.chunks == 1 ? x.slot + rb : 2 * w0 + inside;
-      const int here = min(64, (x.chunks - k0 - part + parts - 1) / parts);
-      for (int i = 0; i < here; i += 2) {
-        // two chunks at a time; one has at most three pieces, as it is at most two shares long
-        float e[6], s[6];
-        f32x4 v[6][2];
+    for (int k0 = 0; k0 < x.chunks; k0 += 64) {
+      // lane i: the pieces of the row block's unit in chunk k0 + i, their number and where the first one is: the
+      // whole unit's own place, or 2 w (+ 1 where others are before it in share w)
+      const int k = k0 + lane;
+      int first = 0, place = 0, count = 0;
+      if (k < x.chunks) {
+        const int64_t unit = x.base + x.unit_begin(k, rb), a = unit + x.room();
+        first = share_at(sh, a);
+        count = share_at(sh, a + x.chunk_tiles(k) - 1) - first + 1;
+        place = count == 1 && x.chunks == 1 ? x.slot + rb : 2 * first + (share_begin(sh, first) < unit ? 1 : 0);
+      }
+      const int upto = wave_scan(count, lane), pieces = __builtin_amdgcn_readlane(upto, 63);
+      for (int q0 = part; q0 < pieces; q0 += 4 * parts) {
+        // one pass with a running maximum, four pieces' loads at once
+        float e[4], s[4];
+        f32x4 v[4][2];
 #pragma unroll
-        for (int u = 0; u < 6; ++u) {
-          const int j = i + u / 3;
+        for (int u = 0; u < 4; ++u) {
+          const int q = q0 + u * parts;
           e[u] = -INFINITY;
           s[u] = 0.f;
           v[u][0] = v[u][1] = f32x4{0, 0, 0, 0};
-          if (j >= here) continue;
-          const int first = __builtin_amdgcn_readlane(w0, j), last = __builtin_amdgcn_readlane(w1, j);
-          const int w = first + u % 3;
-          if (w > last) continue;
-          const int64_t slot = w == first ? __builtin_amdgcn_readlane(one, j) : 2 * w;
+          if (q >= pieces) continue;
+          const int i = __ffsll(__ballot(upto > q)) - 1;
+          const int in_unit = q - (__builtin_amdgcn_readlane(upto, i) - __builtin_amdgcn_readlane(count, i));
+          const int64_t slot = in_unit == 0 ? __builtin_amdgcn_readlane(place, i)
+                                            : 2 * (__builtin_amdgcn_readlane(first, i) + in_unit);
           const float2 ml = p.psum[slot * MB + r];
           e[u] = ml.x;
           s[u] = ml.y;
@@ -764,13 +888,13 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
         }
         float mx = top;
 #pragma unroll
-        for (int u = 0; u < 6; ++u) mx = fmaxf(mx, e[u]);
+        for (int u = 0; u < 4; ++u) mx = fmaxf(mx, e[u]);
         const float base = mx == -INFINITY ? 0.f : mx, old = exp2_hw(top - base);
         sum *= old;
         o[0] *= old;
         o[1] *= old;
 #pragma unroll
-        for (int u = 0; u < 6; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const float f = exp2_hw(e[u] - base) * s[u];
           sum += f;
           o[0] += f * v[u][0];
@@ -877,19 +1001,20 @@ hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t s
   const bool f8 = a.cache_dtype == KDA_E4M3;
   SharedParams p = {};
   p.lat = static_cast<const char*>(a.cache);
-  p.lat_page = a.page_stride * (f8 ? 1 : 2);
+  p.lat_page = (uint32_t)(a.page_stride * (f8 ? 1 : 2));
   p.lat_row = (int)(f8 ? a.L : 2 * (a.L + a.R));
   if (f8) {
     p.scales = reinterpret_cast<const char*>(a.scales);
-    p.scales_page = a.scales_page_stride * 4;
+    p.scales_page = (uint32_t)(a.scales_page_stride * 4);
     p.rot = static_cast<const char*>(a.rope);
-    p.rot_page = a.rope_page_stride * 2;
+    p.rot_page = (uint32_t)(a.rope_page_stride * 2);
   }
   p.num_pages = (int)a.num_pages;
   p.page_size = (int)a.page_size;
   p.L = (int)a.L;
   p.R = (int)a.R;
   page_divisor(p.page_size, &p.page_mul, &p.page_shift);
+  p.eights = p.page_size % 8 == 0;
   p.table = a.page_table;
   p.table_stride = a.table_stride;
   p.max_pages = (int)a.max_pages;

@@ -84,6 +84,30 @@ struct Bf16Tile {
     }
   }
 
+  // Load i of a wave's for a tile (of kLoads: the rotary rows, the latent ones).
+  // Its 8 rows lie one behind the other at lat (uniform), ``row`` bytes each.
+  static constexpr int kLoads = kLat + (RP > 0 ? 1 : 0);
+  static __device__ __forceinline__ void fetch_near(int i, const char* lat, int row, int wave, int lane, const Columns& c,
+                                                    unsigned lat_lds, unsigned rot_lds) {
+    if (RP > 0 && i == 0) {
+      if (!kPad || c.has_rot) load_lds16(uniform(lat), c.rot + lane / 8 * row, lds_at(rot_lds + wave * 8 * RP * 2));
+      return;
+    }
+    i -= kLoads - kLat;
+    const unsigned off = c.lat ^ (unsigned)(swizzle(i * RI) * 16);
+    if (!kPad || off <= c.last)
+      load_lds16(uniform(lat + i * RI * row), RI == 1 ? off : off + lane / LC * row,
+                 lds_at(lat_lds + (wave * kRows + i * RI) * LP * 2));
+  }
+  // The same for rows anywhere: token j's at lane j's lat.
+  static __device__ __forceinline__ void fetch_far(int i, const char* lat, int wave, int lane, const Columns& c,
+                                                   unsigned lat_lds, unsigned rot_lds) {
+    if (RP > 0 && i == 0)
+      fetch_rotary(lat, wave, lane, c, rot_lds);
+    else
+      fetch(i - (kLoads - kLat), lat, wave, lane, c, lat_lds);
+  }
+
   // S^T[token][row] of the wave's tokens and rows; a lane holds tokens 4 lg + i
   // of each block.  Operands are read a group ahead of their products, and
   // load(i), 0 <= i < kLat, is called along the way: a wave stands still while
@@ -163,7 +187,6 @@ struct Bf16Tile {
 };
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Transposed 8-byte LDS read of bytes: in each group of 16 lanes, lane i points
@@ -174,33 +197,28 @@ __device__ __forceinline__ i32x2 read_tr8(const void* lds) {
 }
 
 // eight e4m3 codes as bf16 (exact)
-__device__ __forceinline__ bf16x8 widen(const i32x2& codes) {
-  typedef unsigned u32x4_ __attribute__((ext_vector_type(4)));
-  u32x4_ r;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    r[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)codes[i], 1.f, false));
-    r[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)codes[i], 1.f, true));
-  }
+__device__ __forceinline__ bf16x8 widen(unsigned a, unsigned b) {
+  u32x4 r;
+  r[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false));
+  r[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true));
+  r[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false));
+  r[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true));
   return __builtin_bit_cast(bf16x8, r);
 }
 
 // The same tile of e4m3 codes, with a scale a token and the rotary keys in bf16.
-// The scores' product runs on the codes as they are: a bf16 query, over a power
-// of two that brings its largest component to [128, 256), is the sum of two e4m3
-// numbers (its 8 bits are 4 and, with a sign, 4), so two 8-bit products,
-// at twice the rate of one in bf16, take the place of the conversion
-// of every code in each wave that scores it.  What the split drops of components
-// far below the largest is at most 2^-18 of that; the 8-bit product's own
-// sums keep about 2^-16 of their usual size (measured: 2e-5 over 128 terms, no
-// bias).  The values' product converts codes to bf16 on the way in, and the scales
-// go into the weights before these are rounded to bf16.
+// Codes become bf16 on the way into both products (a bf16 holds an e4m3 value
+// whole); the tokens' scales go onto the scores, and into the weights before these
+// are rounded to bf16.  (The 8-bit products of the matrix unit would spare the
+// scores' conversion, with the query as a sum of two e4m3 numbers, at the
+// same rate; but their sums over 128 terms keep only 2e-5 of their usual
+// size, 2^-11 of the largest term at worst, and a log-sum of few scores would show it.)
 template <int LP, int RP, int NB, bool kPad>
 struct Fp8Tile {
   static constexpr int MB = 16 * NB;
   static constexpr int LC = LP / 16;              // 16-byte chunks of a staged latent row
-  static constexpr int KS = LP / 128;             // contraction steps of the latent scores
-  static constexpr int KR = RP / 32;              // and of the rotary ones
+  static constexpr int KL = LP / 32;              // contraction steps of the latent scores
+  static constexpr int KS = (LP + RP) / 32;       // and of all
   static constexpr int MT = LP / (16 * kWaves);   // 16-column blocks of the output a wave
   static constexpr int TG = NB == 4 ? 2 : 4;      // groups of tokens of a tile
   static constexpr int TB = kTile / 16 / TG;      // blocks of 16 tokens a group
@@ -212,9 +230,9 @@ struct Fp8Tile {
   static constexpr int kLoads = kLat + (RP > 0 ? 1 : 0) + 1;  // and all of them
 
   // Chunk c of latent row r is staged at position c ^ swizzle(r): a service
-  // group of 16-byte reads (rows 0-3 and 12-15 of one chunk, 4-11 of the chunk
-  // two further) and a half wave of transposed reads (16 rows of one chunk) then
-  // fall on distinct banks.  Rows of 128 B lie two to a pass over the banks.
+  // group of 16-byte reads (rows 0-3 and 12-15 of one chunk, 4-11 of the next)
+  // and a half wave of transposed reads (16 rows of one chunk) then fall on
+  // distinct banks.  Rows of 128 B lie two to a pass over the banks.
   static __device__ __forceinline__ int swizzle(int r) { return LP == 128 ? ((r >> 1) + 2) & 7 : r & 15; }
 
   // A lane's part of its rows' addresses; lanes of padding columns are off, as
@@ -234,140 +252,108 @@ struct Fp8Tile {
     c.L = L;
     return c;
   }
-  // All of a wave's loads for the tile whose codes, rotary keys and scales lie at
-  // lat, rot and scale (lane i: token i).
-  static __device__ __forceinline__ void fetch(const char* lat, const char* rot, const char* scale, int wave, int lane,
-                                               const Columns& c, unsigned lat_lds, unsigned rot_lds, unsigned scale_lds) {
-    if (lane / 8 == wave) load_lds4(scale, uniform(scale_lds));
-    if (RP > 0) {
+  static __device__ __forceinline__ int chunk(int i, const Columns& c) {
+    return c.lat ^ ((swizzle(i * RI) ^ swizzle(0)) * 16);  // (i RI adds to no bit of the wave's first row and the lane's)
+  }
+  // Load i of a wave's for a tile (of kLoads: scales, rotary rows, latent rows).
+  // Its 8 rows lie one behind the other at lat, rot and scale (uniform).
+  static __device__ __forceinline__ void fetch_near(int i, const char* lat, const char* rot, const char* scale, int L,
+                                                    int R, int wave, int lane, const Columns& c, unsigned lat_lds,
+                                                    unsigned rot_lds, unsigned scale_lds) {
+    if (i == 0) {
+      if (lane / 8 == wave) load_lds4(uniform(scale), (unsigned)(lane % 8 * 4), uniform(scale_lds));
+    } else if (RP > 0 && i == 1) {
+      if (!kPad || c.has_rot) load_lds16(uniform(rot), lane / 8 * (2 * R) + c.rot, uniform(rot_lds + wave * 8 * RP * 2));
+    } else {
+      i -= kLoads - kLat;
+      const int at = chunk(i, c);
+      if (!kPad || at < c.L)
+        load_lds16(uniform(lat + i * RI * L), (unsigned)(lane / LC * L + at), uniform(lat_lds + (wave * kRows + i * RI) * LP));
+    }
+  }
+  // The same for rows anywhere: token j's at lane j's lat, rot and scale.
+  static __device__ __forceinline__ void fetch_far(int i, const char* lat, const char* rot, const char* scale, int wave,
+                                                   int lane, const Columns& c, unsigned lat_lds, unsigned rot_lds,
+                                                   unsigned scale_lds) {
+    if (i == 0) {
+      if (lane / 8 == wave) load_lds4(scale, uniform(scale_lds));
+    } else if (RP > 0 && i == 1) {
       const char* row = (const char*)__shfl((int64_t)rot, wave * 8 + lane / 8, 64);
       if (!kPad || c.has_rot) load_lds16(row + c.rot, uniform(rot_lds + wave * 8 * RP * 2));
-    }
-#pragma unroll
-    for (int i = 0; i < kLat; ++i) {
-      const int r = wave * kRows + i * RI;
-      const int at = c.lat ^ ((swizzle(i * RI) ^ swizzle(0)) * 16);
+    } else {
+      i -= kLoads - kLat;
+      const int r = wave * kRows + i * RI, at = chunk(i, c);
       const char* row = (const char*)__shfl((int64_t)lat, r + lane / LC, 64);
       if (!kPad || at < c.L) load_lds16(row + at, uniform(lat_lds + r * LP));
     }
   }
 
-  // A lane's part of a query row: components 128 k + 32 lg .. + 31 of the latent
-  // part, 32 k + 8 lg .. + 7 of the rotary part.
-  struct Raw {
-    u32x4 lat[KS][4];
-    bf16x8 rot[KR > 0 ? KR : 1];
-  };
-  struct Query {
-    i32x8 hi[KS], lo[KS];
-    bf16x8 rot[KR > 0 ? KR : 1];
-    float size;  // the power of two taken out
-  };
-  static __device__ __forceinline__ void request(const __bf16* q, const __bf16* qr, int L, int R, int lg, Raw& x) {
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 128 * k + 32 * lg + 8 * j;
-        x.lat[k][j] = u32x4{0, 0, 0, 0};
-        if (!kPad || c < L) x.lat[k][j] = *reinterpret_cast<const u32x4*>(q + c);
-      }
-#pragma unroll
-    for (int k = 0; k < KR; ++k) {
-      const int c = 32 * k + 8 * lg;
-      bf16x8 y = {};
-      if (!kPad || c < R) y = *reinterpret_cast<const bf16x8*>(qr + c);
-      x.rot[k] = y;
-    }
-  }
-  static __device__ __forceinline__ void split(const Raw& x, Query& q) {
-    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 m2 = {0, 0};
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, x.lat[k][j][i] & 0x7fff7fffu));
-    // (of the bits: an infinity or a NaN is the largest and becomes NaN in the codes)
-    int e = m2[0] > m2[1] ? m2[0] : m2[1];
-    e = max(e, __shfl_xor(e, 16, 64));
-    e = max(e, __shfl_xor(e, 32, 64)) >> 7;
-    e = e < 8 ? 8 : e;
-    const float inv = __builtin_bit_cast(float, (unsigned)(261 - e) << 23);
-    q.size = __builtin_bit_cast(float, (unsigned)(e - 7) << 23);
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const unsigned w0 = x.lat[k][d >> 1][2 * (d & 1)], w1 = x.lat[k][d >> 1][2 * (d & 1) + 1];
-        const float y[4] = {__builtin_bit_cast(float, w0 << 16) * inv, __builtin_bit_cast(float, w0 & 0xffff0000u) * inv,
-                            __builtin_bit_cast(float, w1 << 16) * inv, __builtin_bit_cast(float, w1 & 0xffff0000u) * inv};
-        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], hi, true);
-        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
-        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] - a[0], y[1] - a[1], 0, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] - b[0], y[3] - b[1], lo, true);
-        q.hi[k][d] = hi;
-        q.lo[k][d] = lo;
-        hold_order();  // (in turn, in the registers of what is split)
-      }
-#pragma unroll
-    for (int k = 0; k < KR; ++k) q.rot[k] = x.rot[k];
+  // Component that a lane's query operand k begins with: a lane reads 16 codes at
+  // a time, so two steps of the product take 8 each of the same 16 components.
+  static __device__ __forceinline__ int component(int k, int lg) {
+    return k < KL ? 64 * (k >> 1) + 16 * lg + 8 * (k & 1) : 32 * (k - KL) + 8 * lg;
   }
 
   // S^T[token][row] of the wave's tokens and rows, and the tokens' scales; a lane
   // holds tokens 4 lg + i of each block.  lat, rot, scale: of the group's first
-  // token.
-  static __device__ __forceinline__ void scores(const char* lat, const __bf16* rot, const float* scale, const Query& q,
-                                                int ln, int lg, f32x4 (&s)[TB], f32x4 (&sc)[TB]) {
-    constexpr int F = KS * TB;
+  // token.  Operands are read two steps ahead of their products, and load(i), 0 <= i
+  // < kLoads, is called along the way, as in Bf16Tile.
+  template <typename Load>
+  static __device__ __forceinline__ void scores(const char* lat, const char* rot, const float* scale,
+                                                const bf16x8 (&qf)[KS], int ln, int lg, f32x4 (&s)[TB], f32x4 (&sc)[TB],
+                                                const Load& load) {
+    constexpr int M = LP / 64, KR = RP / 32, LG = (kLoads + M - 1) / M;
     const char* row = lat + ln * LP;
-    const int at0 = ((2 * lg) ^ swizzle(ln)) * 16;  // (chunk 8 k + 2 lg + i: bits 3, 4, .. of k apart from the others)
-    auto read = [&](int n) {  // codes of step n / TB, block n % TB
-      const int k = n / TB, j = n % TB;
-      const char* at = row + j * 16 * LP + (k >> 1) * 256;
-      typedef int i32x4 __attribute__((ext_vector_type(4)));
-      const i32x4 a = *reinterpret_cast<const i32x4*>(at + (at0 ^ ((k & 1) * 128)));
-      const i32x4 b = *reinterpret_cast<const i32x4*>(at + (at0 ^ ((k & 1) * 128 + 16)));
-      return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    const int at0 = (lg ^ swizzle(ln)) * 16;  // of chunk 4 m + lg: m's bits are xored or above
+    u32x4 x[3][TB];
+    auto read = [&](int m) {
+#pragma unroll
+      for (int j = 0; j < TB; ++j)
+        x[m % 3][j] = *reinterpret_cast<const u32x4*>(row + j * 16 * LP + (m >> 2) * 256 + (at0 ^ ((m & 3) * 64)));
     };
-    f32x4 hi[TB], lo[TB], ro[TB];
-    i32x8 x[2];
-    bf16x8 y[KR > 0 ? KR : 1][TB];
-    x[0] = read(0);
+    f32x4 acc[TB][2], ro[TB];
+    bf16x8 y[TB];
+    const int y0 = (lg ^ ((ln >> 1) & 7)) * 16;
+    auto rotary = [&](int k) {
 #pragma unroll
-    for (int j = 0; j < TB; ++j) hi[j] = lo[j] = ro[j] = f32x4{0, 0, 0, 0};
+      for (int j = 0; j < TB; ++j) y[j] = *reinterpret_cast<const bf16x8*>(rot + (16 * j + ln) * RP * 2 + (y0 ^ (k * 64)));
+    };
 #pragma unroll
-    for (int n = 0; n < F; ++n) {
-      if (n + 1 < F) {
-        x[(n + 1) & 1] = read(n + 1);
-      } else {
-        const int y0 = (lg ^ ((ln >> 1) & 7)) * 16;
+    for (int j = 0; j < TB; ++j) acc[j][0] = acc[j][1] = ro[j] = f32x4{0, 0, 0, 0};
+    read(0);
+    if (M > 1) read(1);
 #pragma unroll
-        for (int j = 0; j < TB; ++j) {
-          sc[j] = *reinterpret_cast<const f32x4*>(scale + 16 * j + 4 * lg);
+    for (int m = 0; m < M; ++m) {
+      if (m + 2 < M) {
+        read(m + 2);
+      } else if (m + 1 == M) {
+        if (KR > 0) rotary(0);
 #pragma unroll
-          for (int k = 0; k < KR; ++k)
-            y[k][j] = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(rot) + (16 * j + ln) * RP * 2 +
-                                                       (y0 ^ (k * 64)));
-        }
+        for (int j = 0; j < TB; ++j) sc[j] = *reinterpret_cast<const f32x4*>(scale + 16 * j + 4 * lg);
       }
       hold_order();
-      const int k = n / TB, j = n % TB;
-      hi[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[n & 1], q.hi[k], hi[j], 0, 0, 0, 0, 0, 0);
-      lo[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[n & 1], q.lo[k], lo[j], 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int i = m * LG; i < kLoads && i < (m + 1) * LG; ++i) load(i);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+          acc[j][TB == 1 ? h : 0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              widen(x[m % 3][j][2 * h], x[m % 3][j][2 * h + 1]), qf[2 * m + h], acc[j][TB == 1 ? h : 0], 0, 0, 0);
       hold_order();
     }
 #pragma unroll
-    for (int k = 0; k < KR; ++k)
+    for (int k = 0; k < KR; ++k) {
 #pragma unroll
-      for (int j = 0; j < TB; ++j) ro[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[k][j], q.rot[k], ro[j], 0, 0, 0);
+      for (int j = 0; j < TB; ++j) ro[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[j], qf[KL + k], ro[j], 0, 0, 0);
+      if (k + 1 < KR) rotary(k + 1);
+    }
 #pragma unroll
-    for (int j = 0; j < TB; ++j)
+    for (int j = 0; j < TB; ++j) {
+      if (TB == 1) acc[j][0] += acc[j][1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[j][i] = fmaf(hi[j][i] + lo[j][i], q.size * sc[j][i], ro[j][i]);
+      for (int i = 0; i < 4; ++i) s[j][i] = fmaf(acc[j][0][i], sc[j][i], ro[j][i]);
+    }
   }
 
   // out^T[column][row] += codes^T P^T for the wave's columns (P has the scales)
@@ -378,21 +364,22 @@ struct Fp8Tile {
     const int at0 = ((wave * MT) ^ swizzle(r0)) * 16;
     constexpr int B = kTile / 32 * MT;
     bf16x8 pf[NB];
-    i32x2 vf[2];
+    i32x2 vf[3];
     auto weights = [&](int k) {
 #pragma unroll
       for (int j = 0; j < NB; ++j)
         pf[j] = *reinterpret_cast<const bf16x8*>(prob + (j * 16 + ln) * kTile + (((4 * k + lg) ^ (ln & 7)) << 3));
     };
-    auto read = [&](int b) { vf[b & 1] = read_tr8(rows + b / MT * 32 * LP + (at0 ^ (b % MT * 16))); };
+    auto read = [&](int b) { vf[b % 3] = read_tr8(rows + b / MT * 32 * LP + (at0 ^ (b % MT * 16))); };
     weights(0);
     read(0);
+    read(1);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (b == MT) weights(1);
-      if (b + 1 < B) read(b + 1);
+      if (b + 2 < B) read(b + 2);
       hold_order();
-      const bf16x8 v = widen(vf[b & 1]);
+      const bf16x8 v = widen((unsigned)vf[b % 3][0], (unsigned)vf[b % 3][1]);
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[b % MT][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pf[j], acc[b % MT][j], 0, 0, 0);
       hold_order();
