@@ -35,9 +35,8 @@ namespace {
 using namespace latent;
 
 constexpr int kShares = 256;       // workgroups, one a CU
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kEnd = 4;            // room before a unit of an entity of one chunk
-constexpr int kPlanLds = 4096;     // entities whose places the plan keeps in LDS
 
 struct Entity {
   int64_t base, first;     // place on the line, and the number of its first tile
@@ -99,61 +98,75 @@ __device__ __forceinline__ int seq_tokens(const SharedParams& p, int n) {
   return len < 0 ? 0 : (len > room ? (int)room : len);
 }
 
-// The line in equal shares, none empty (fewer of them where there are fewer tiles).
-struct Shares {
-  int64_t quot, rem, count;
-};
-__device__ __forceinline__ Shares shares_of(int64_t total) {
-  Shares s;
-  s.count = total < kShares ? total : kShares;
-  s.quot = total < kShares ? 1 : total / kShares;
-  s.rem = total < kShares ? 0 : total % kShares;
-  return s;
-}
-__device__ __forceinline__ int64_t share_begin(const Shares& s, int64_t w) { return w * s.quot + (w < s.rem ? w : s.rem); }
-// the share that holds tile x
-__device__ __forceinline__ int share_at(const Shares& s, int64_t x) {
-  const int64_t longer = s.rem * (s.quot + 1);
-  if ((uint64_t)(x | s.quot) < 0x7fffffffu) {
-    const unsigned q = (unsigned)s.quot;
-    return x < longer ? (int)((unsigned)x / (q + 1)) : (int)s.rem + (int)((unsigned)(x - longer) / q);
-  }
-  return x < longer ? (int)(x / (s.quot + 1)) : (int)(s.rem + (x - longer) / s.quot);
+// a / b, with 32-bit numbers where they do (a division of 64 bits is a hundred instructions)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if ((uint64_t)(a | b) >> 32 == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
 }
 
-// Sums (inclusive) over the workgroup of the threads before and with this one;
-// *all: over all.
-template <typename T>
-__device__ __forceinline__ T block_scan(T x, T* wsum, T* all) {
+// The line in equal shares, none empty (fewer of them where there are fewer tiles).
+struct Shares {
+  int64_t quot;
+  int rem, count;
+};
+__device__ __forceinline__ Shares shares_of(int64_t total) {
+  const bool few = total < kShares;
+  return {few ? 1 : (int64_t)((uint64_t)total / kShares), few ? 0 : (int)((uint64_t)total % kShares),
+          few ? (int)total : kShares};
+}
+__device__ __forceinline__ int64_t share_begin(const Shares& s, int w) { return w * s.quot + min(w, s.rem); }
+// the share that holds place x
+__device__ __forceinline__ int share_at(const Shares& s, int64_t x) {
+  const int64_t longer = s.rem * (s.quot + 1);
+  return x < longer ? (int)quotient(x, s.quot + 1) : s.rem + (int)quotient(x - longer, s.quot);
+}
+
+// Inclusive sums of two numbers over the workgroup's threads up to this one;
+// *all_x, *all_y: over all of them.
+__device__ __forceinline__ void block_scan(long long& x, long long& y, long long (&sums)[2][kPlanThreads / 64],
+                                           long long* all_x, long long* all_y) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const T y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
+    const long long a = __shfl_up(x, d, 64), b = __shfl_up(y, d, 64);
+    if (lane >= d) {
+      x += a;
+      y += b;
+    }
   }
-  if (lane == 63) wsum[wave] = x;
+  if (lane == 63) {
+    sums[0][wave] = x;
+    sums[1][wave] = y;
+  }
   __syncthreads();
-  T before = 0, sum = 0;
+  *all_x = *all_y = 0;
+  long long px = 0, py = 0;
 #pragma unroll
   for (int i = 0; i < kPlanThreads / 64; ++i) {
-    const T v = wsum[i];
-    before += i < wave ? v : 0;
-    sum += v;
+    const long long a = sums[0][i], b = sums[1][i];
+    px += i < wave ? a : 0;
+    py += i < wave ? b : 0;
+    *all_x += a;
+    *all_y += b;
   }
+  x += px;
+  y += py;
   __syncthreads();
-  *all = sum;
-  return x + before;
 }
 
+// One workgroup; what it reads is a few numbers a sequence, and what it takes is
+// the latency of what depends on what: up to kPlanThreads entities stay in
+// registers and LDS.
 __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams p, int MB) {
-  __shared__ long long lsum[kPlanThreads / 64];
-  __shared__ int isum[kPlanThreads / 64];
-  __shared__ long long places[kPlanLds], number[kShares + 1];
+  __shared__ long long sums[2][kPlanThreads / 64], number[kShares + 1];
+  __shared__ int tops[kPlanThreads / 64];
+  __shared__ Entity lents[kPlanThreads];
   __shared__ int lbounds[kPlanThreads + 1], lprefix[kPlanThreads];
   const int own_blocks = (p.rows + MB - 1) / MB;
   const int tid = threadIdx.x, E = p.G + p.N;
-  // (in LDS where they fit: what follows searches them)
-  int *bounds = p.G <= kPlanThreads ? lbounds : p.bounds, *prefix = p.G <= kPlanThreads ? lprefix : p.prefix;
+  const bool few = E <= kPlanThreads;
+  int *bounds = few ? lbounds : p.bounds, *prefix = few ? lprefix : p.prefix;
+  Entity* ents = few ? lents : p.ents;
   // the groups' bounds: inside the batch, and not before an earlier one
   if (p.G > 0) {
     int carry = 0;
@@ -166,12 +179,12 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
       }
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) v = max(v, __shfl_up(v, d, 64));
-      if (lane == 63) isum[wave] = v;
+      if (lane == 63) tops[wave] = v;
       __syncthreads();
       int most = carry;
       for (int k = 0; k < kPlanThreads / 64; ++k) {
-        if (k < wave) v = max(v, isum[k]);
-        most = max(most, isum[k]);
+        if (k < wave) v = max(v, tops[k]);
+        most = max(most, tops[k]);
       }
       v = max(v, carry);
       carry = most;
@@ -223,12 +236,12 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
         if (x.t0 > 0) x.group = lo;
       }
     }
-    x.tiles = (int)(((int64_t)x.t1 - x.t0 + kTile - 1) / kTile);
+    x.tiles = (int)((unsigned)(x.t1 - x.t0 + kTile - 1) / kTile);
     x.row_blocks = (x.rows + MB - 1) / MB;
     return x;
   };
   // the line's length with room for every entity, and from that the chunks; then the line
-  long long total = 0;
+  long long total = 0, zero = 0;
   Entity mine;  // the last one of this thread: the only one, mostly
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
     long long n = 0, all;
@@ -236,31 +249,32 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
       mine = entity(e0 + tid);
       n = mine.tiles > 0 ? (long long)mine.row_blocks * (mine.tiles + kEnd) : 0;
     }
-    block_scan(n, lsum, &all);
+    block_scan(n, zero, sums, &all, &zero);
     total += all;
   }
   const long long quot = shares_of(total).quot;
-  const int share = quot > (1 << 30) ? 1 << 30 : (int)quot;
+  const unsigned share = quot > (1 << 30) ? 1u << 30 : (unsigned)quot;
   long long base = 0, first = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
     const int e = e0 + tid;
     long long n = 0, tiles = 0, all, all_tiles;
     if (e < E) {
-      if (E > kPlanThreads) mine = entity(e);
+      if (!few) mine = entity(e);
       if (mine.tiles > 0) {
-        mine.chunks = max(1, mine.tiles / share);
-        mine.chunk = mine.tiles / mine.chunks;
-        mine.longer = mine.tiles % mine.chunks;
+        mine.chunks = (int)max(1u, (unsigned)mine.tiles / share);
+        mine.chunk = (int)((unsigned)mine.tiles / (unsigned)mine.chunks);
+        mine.longer = mine.tiles - mine.chunk * mine.chunks;
         n = mine.line();
         tiles = (long long)mine.tiles * mine.row_blocks;
       }
     }
-    const long long upto = block_scan(n, lsum, &all), tiles_upto = block_scan(tiles, lsum, &all_tiles);
+    long long upto = n, tiles_upto = tiles;
+    block_scan(upto, tiles_upto, sums, &all, &all_tiles);
     if (e < E) {
       mine.base = base + upto - n;
       mine.first = first + tiles_upto - tiles;
       p.ents[e] = mine;
-      if (e < kPlanLds) places[e] = mine.base;
+      if (few) lents[e] = mine;
     }
     base += all;
     first += all_tiles;
@@ -272,23 +286,22 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
   Start s;
   if (tid < sh.count) {
     const int64_t from = share_begin(sh, tid);
-    auto place = [&](int e) { return E <= kPlanLds ? places[e] : (long long)p.ents[e].base; };
     int lo = 0, hi = E;  // the last entity that begins there or before: it holds the place, if empty ones at its
     while (hi - lo > 1) {  // place are before it
       const int mid = (lo + hi) >> 1;
-      if (place(mid) <= from) lo = mid; else hi = mid;
+      if (ents[mid].base <= from) lo = mid; else hi = mid;
     }
     // the unit and tile of that place; a unit's room counts as its first tile
-    s.ent = p.ents[lo];
+    s.ent = ents[lo];
     const Entity& x = s.ent;
     const int64_t in = from - x.base;
     if (x.chunks == 1) {
       s.k = 0;
-      s.rb = (int)(in / (x.tiles + kEnd));
+      s.rb = (int)quotient(in, x.tiles + kEnd);
     } else {
-      const int y = (int)(in / x.row_blocks), longer = x.longer * (x.chunk + 1);
-      s.k = y < longer ? y / (x.chunk + 1) : x.longer + (y - longer) / x.chunk;
-      s.rb = (int)((in - x.unit_begin(s.k, 0)) / x.chunk_tiles(s.k));
+      const unsigned y = (unsigned)quotient(in, x.row_blocks), longer = x.longer * (x.chunk + 1);
+      s.k = (int)(y < longer ? y / (unsigned)(x.chunk + 1) : x.longer + (y - longer) / (unsigned)x.chunk);
+      s.rb = (int)quotient(in - x.unit_begin(s.k, 0), x.chunk_tiles(s.k));
     }
     const int64_t rest = in - x.unit_begin(s.k, s.rb) - x.room();
     s.t = rest > 0 ? (int)rest : 0;
@@ -301,8 +314,8 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
   if (tid < sh.count) {
     s.left = (int)(number[tid + 1] - number[tid]);
     // neighbours to workgroups of one XCD, which are those of one number mod 8
-    const int per = (int)((sh.count + 7) / 8);
-    p.starts[tid % per * 8 + tid / per] = s;
+    const unsigned per = (unsigned)(sh.count + 7) / 8;
+    p.starts[(unsigned)tid % per * 8 + (unsigned)tid / per] = s;
   }
 }
 
@@ -329,39 +342,34 @@ __device__ __forceinline__ T scalar_load(const T* at) {
   return r;
 }
 
-// A cache's kind: its tile, the stages that fit into the LDS, and whether a tile's
-// values are multiplied beside the next one's scores (kLag: the weights' exponentials
-// and exchanges then run beside matrix products, and one barrier a tile does).
+// A cache's kind: its tile, and the stages that fit into the LDS.
 template <bool F8, int LP, int RP, int NB, bool kPad>
 struct Kind {
   typedef Bf16Tile<LP, RP, NB, kPad, true> D;
   static constexpr int kStages = 2, kStageBytes = D::kStage * 2;
-  static constexpr bool kLag = false;
 };
 template <int LP, int RP, int NB, bool kPad>
 struct Kind<true, LP, RP, NB, kPad> {
   typedef Fp8Tile<LP, RP, NB, kPad> D;
   static constexpr int kStages = 3, kStageBytes = D::kStage;
-  static constexpr bool kLag = NB == 4;
 };
 
 template <bool F8, int LP, int RP, int NB, bool kPad>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_shared_kernel(SharedParams p) {
   using K = Kind<F8, LP, RP, NB, kPad>;
   using D = typename K::D;
-  constexpr bool kLag = K::kLag;
   constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG, TB = D::TB, NS = K::kStages;
-  constexpr int kAhead = kLag ? 1 : NS - 1;  // tiles fetched ahead of the one scored
+  constexpr int kAhead = NS - 1;  // tiles fetched ahead of the one computed
   constexpr unsigned kStageBytes = K::kStageBytes, kRotaryBytes = RP > 0 ? kTile * RP * 2 : 16;
   __shared__ __attribute__((aligned(16))) char stage[NS][kStageBytes];
   __shared__ __attribute__((aligned(16))) char rotary[NS][kRotaryBytes];
   __shared__ __attribute__((aligned(16))) float tscale[NS][F8 ? kTile : 4];
-  __shared__ __attribute__((aligned(16))) __bf16 prob[kLag ? 2 : 1][MB * kTile];
+  __shared__ __attribute__((aligned(16))) __bf16 prob[MB * kTile];
   __shared__ __attribute__((aligned(16))) int4 units[kUnits];
   __shared__ float smax[TG][MB];  // of a tile; at a piece's end the sums
   __shared__ float sfac[MB];      // factor of the older output; at a piece's end the maxima
-  __shared__ int32_t pages[2][kWaves][64];  // page of token lane of the tile located next
-  __shared__ int grown[3];        // whether a row's maximum has grown much in this tile
+  __shared__ int32_t pages[2][kWaves][64];  // of a batch's tokens, a copy a wave
+  __shared__ int grown[2];        // whether a row's maximum has grown much in this tile
   // What is needed between units alone, so that it takes no scalar registers
   // within them (they do not hold everything, and what they do not hold is moved
   // to and from vector registers in every tile).
@@ -372,7 +380,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const Start start = scalar_load(p.starts + blockIdx.x);
   if (start.left == 0) return;
   if (tid == 0) cold = p;
-  if (tid < 3) grown[tid] = 0;
+  if (tid < 2) grown[tid] = 0;
   if (kPad) {
     u32x4 *st = reinterpret_cast<u32x4*>(stage), *ro = reinterpret_cast<u32x4*>(rotary);
     for (unsigned i = tid; i < sizeof(stage) / 16; i += kThreads) st[i] = u32x4{0, 0, 0, 0};
@@ -384,24 +392,34 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const int tg = (wave / NB) % TG;  // and tokens
   const int w = start.w;
 
-  // ---- the tiles of the share, one after another; what is kept of the last one asked for
-  int e = start.e, k = start.k, rb = start.rb;  // its unit
-  int rem, pos, end;                            // tiles from it to its unit's last; its tokens pos .. before end
-  const char* row_pages;                        // its sequence's row of the table
+  // ---- the tiles of the share, one after another.  Pages are looked up for a batch
+  // of tiles of one unit at a time: 8 tiles and a lane for every 8 tokens of
+  // them, where 8 tokens lie in one page (pages of a multiple of 8 tokens, an
+  // entity that begins at one), otherwise one tile and a lane a token.  (A tile's
+  // own lookup by each wave took a fifth of the time.)
+  struct Batch {
+    int pos, end, rem, group;  // its tokens pos .. before end; tiles to its unit's end; 2^group tokens a lane
+  };
+  Batch asked, now;            // the one being looked up, and the one in use
+  int e = start.e, k = start.k, rb = start.rb;  // the unit of ``asked``
+  const char* row_pages;                        // and its sequence's row of the table
   int asked_unit = 0;
   auto enter = [&](const Entity& x, int t) {
-    rem = x.chunk_tiles(k) - t;
-    pos = x.t0 + (x.chunk_begin(k) + t) * kTile;
-    end = x.t1;
+    asked.rem = x.chunk_tiles(k) - t;
+    asked.pos = x.t0 + (x.chunk_begin(k) + t) * kTile;
+    asked.end = x.t1;
+    asked.group = p.eights && x.t0 % 8 == 0 ? 3 : 0;
     row_pages = uniform(reinterpret_cast<const char*>(cold.table + x.seq * cold.table_stride));
     if (tid == 0) {
       const int flags = x.chunks != 1 ? 0 : (e >= cold.G && x.t0 == 0 ? kSingle | kAlone : kSingle);
       units[asked_unit % kUnits] = make_int4(x.row0 + rb * MB, min(MB, x.rows - rb * MB), x.slot + rb, flags);
     }
   };
-  auto follow = [&]() {  // (there is a next tile)
-    pos += kTile;
-    if (--rem > 0) return;
+  auto follow = [&]() {  // (there is a next batch)
+    const int n = min(asked.rem, 1 << asked.group);
+    asked.rem -= n;
+    asked.pos += n * kTile;
+    if (asked.rem > 0) return;
     auto entity = [&]() {
       return scalar_load(reinterpret_cast<const Entity*>(uniform(reinterpret_cast<const char*>(cold.ents + e))));
     };
@@ -430,21 +448,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     unsigned long long live;  // which rows are there
   };
   auto page_of = [&](int at) { return (unsigned)(((uint64_t)(unsigned)at * p.page_mul) >> p.page_shift); };
-  // where the page of token pos + lane is (the last one's for lanes behind the end)
-  auto lookup = [&]() { return row_pages + (uint64_t)page_of(min(pos + lane, end - 1)) * 4; };
+  const unsigned pages_at = lds_offset(pages[0][wave]);
+  int asked_to = 0;  // which copy of the pages ``asked`` goes to
+  // (a lane behind the end looks up the last token's)
+  auto ask = [&]() {
+    const int at = min(asked.pos + (lane << asked.group), asked.end - 1);
+    load_lds4(row_pages + (uint64_t)page_of(at) * 4, uniform(pages_at + asked_to * (unsigned)sizeof(pages[0])));
+  };
 
-  // Where a tile's rows are.  Near: all are there, and each wave's 8 lie one behind
-  // the other (pages of a multiple of 8 tokens, a tile that begins at one);
-  // ``at`` is where, the same in all lanes.  Otherwise it is where token pos + lane is;
-  // rows that are not there are fetched from the
-  // first one that is (their weights are 0); a tile without any is not
-  // fetched and not computed.
+  // Where rows lie: the wave's 8 of a tile, the same in all lanes, or one a lane.
   struct Rows {
     const char *lat, *rot, *scale;
-  };
-  struct Place {
-    bool near;
-    Rows at;
   };
   auto place_at = [&](unsigned page, unsigned off) {
     Rows x;
@@ -456,30 +470,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
     return x;
   };
-  auto locate = [&](int page, int at, int before, Tile& x) {
-    x.live = __ballot(at + lane < before && (unsigned)page < (unsigned)p.num_pages);
-    if (x.live == ~0ull && p.eights && at % 8 == 0) {
-      const int first = at + 8 * wave;
-      const Rows y = place_at(__builtin_amdgcn_readlane(page, 8 * wave), first - page_of(first) * p.page_size);
-      return Place{true, y};
-    }
-    int off = at + lane - (int)page_of(at + lane) * p.page_size;
-    if (x.live != 0) {
-      const int some = __ffsll(x.live) - 1;
-      const bool there = x.live >> lane & 1;
-      const int spage = __builtin_amdgcn_readlane(page, some), soff = __builtin_amdgcn_readlane(off, some);
-      page = there ? page : spage;
-      off = there ? off : soff;
-    }
-    return Place{false, place_at(page, off)};
-  };
   const unsigned stage_at = lds_offset(stage), rotary_at = lds_offset(rotary), scale_at = lds_offset(tscale);
-  const unsigned pages_at = lds_offset(pages[0][wave]);
-  constexpr unsigned kPagesBytes = sizeof(pages[0]), kScaleBytes = sizeof(tscale[0]);
-  typename D::Columns columns;
+  constexpr unsigned kScaleBytes = sizeof(tscale[0]);
   // (anew for each tile: the loads' addresses then take no registers beside the products)
-  auto begin_loads = [&]() { columns = D::columns(p.L, p.R, wave, keep_here(tid & 63)); };
-  // Load i, 0 <= i < kLoads, of a tile that is near to stage ``to``.
+  auto columns_of = [&]() { return D::columns(p.L, p.R, wave, keep_here(tid & 63)); };
+  typename D::Columns columns;
+  // Load i, 0 <= i < kLoads, of a tile whose rows lie one behind the other, to stage ``to``.
   auto fetch = [&](const Rows& y, int i, int to) {
     const unsigned lat = stage_at + to * kStageBytes, rot = rotary_at + to * kRotaryBytes;
     if constexpr (F8)
@@ -488,48 +484,87 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     else
       D::fetch_near(i, y.lat, kPad ? p.lat_row : 2 * (LP + RP), wave, lane, columns, lat, rot);
   };
-  // All of a tile's.
-  auto fetch_all = [&](const Place& y, int to) {
+
+  int unlocated = start.left;     // tiles of the share behind the last one located
+  int batch_left = 0, tile = 0;   // tiles of ``now`` not located, the next one's number in it
+  unsigned long long sound = 0;   // from that one on: whether its tokens' pages are pages
+  // The next tile, whose batch's pages have landed; the next batch's are asked for
+  // with the last one.  True: it is near (all rows are there, and each wave's 8 lie one
+  // behind the other) and its loads are the caller's to issue.  Otherwise they
+  // are issued here: rows that are not there are fetched from the first one that
+  // is (their weights are 0); a tile without any is not fetched and not computed.
+  auto locate = [&](Tile& x, Rows& rows, int to) {
+    if (batch_left == 0) {
+      now = asked;
+      batch_left = min(now.rem, 1 << now.group);
+      tile = 0;
+      const int page = pages[asked_to][wave][lane];
+      sound = __ballot((unsigned)page < (unsigned)p.num_pages);
+      asked_to ^= 1;
+    }
+    const int32_t* mine = pages[asked_to ^ 1][wave];
+    const int pos = now.pos, number = tile;
+    const bool near = now.group == 3 && (sound & 255) == 255 && pos + kTile <= now.end;
+    const bool grouped = now.group == 3;
+    const int end = now.end;
+    x.pos = pos;
+    x.last = now.rem == 1;
+    x.live = ~0ull;
+    now.pos += kTile;
+    --now.rem;
+    ++tile;
+    sound >>= 8;
+    --unlocated;
+    if (--batch_left == 0 && unlocated > 0) {
+      follow();
+      ask();
+    }
+    columns = columns_of();
+    if (near) {
+      const int first = pos + 8 * wave;
+      const unsigned page = uniform(mine[number * 8 + wave]);
+      const Rows y = place_at(page, first - page_of(first) * p.page_size);
+      rows.lat = uniform(y.lat);
+      if (F8) {
+        rows.scale = uniform(y.scale);
+        if (RP > 0) rows.rot = uniform(y.rot);
+      }
+      return true;
+    }
+    int page = mine[grouped ? number * 8 + (lane >> 3) : lane];
+    int off = pos + lane - (int)page_of(pos + lane) * p.page_size;
+    x.live = __ballot(pos + lane < end && (unsigned)page < (unsigned)p.num_pages);
+    if (x.live == 0) return false;
+    const int some = __ffsll(x.live) - 1;
+    const bool there = x.live >> lane & 1;
+    const int spage = __builtin_amdgcn_readlane(page, some), soff = __builtin_amdgcn_readlane(off, some);
+    const Rows y = place_at(there ? page : spage, there ? off : soff);
     const unsigned lat = stage_at + to * kStageBytes, rot = rotary_at + to * kRotaryBytes;
 #pragma unroll
     for (int i = 0; i < D::kLoads; ++i) {
-      if (y.near)
-        fetch(y.at, i, to);
-      else if constexpr (F8)
-        D::fetch_far(i, y.at.lat, y.at.rot, y.at.scale, wave, lane, columns, lat, rot, scale_at + to * kScaleBytes);
+      if constexpr (F8)
+        D::fetch_far(i, y.lat, y.rot, y.scale, wave, lane, columns, lat, rot, scale_at + to * kScaleBytes);
       else
-        D::fetch_far(i, y.at.lat, wave, lane, columns, lat, rot);
+        D::fetch_far(i, y.lat, wave, lane, columns, lat, rot);
     }
+    return false;
+  };
+  auto fetch_all = [&](const Rows& y, int to) {
+#pragma unroll
+    for (int i = 0; i < D::kLoads; ++i) fetch(y, i, to);
   };
 
   int left = start.left - 1;  // tiles behind the one scored
-  int ahead = left;           // and behind the last one asked for
   Tile ring[kAhead + 1];      // the one scored, and those fetched ahead
-  auto asked = [&]() { return Tile{pos, rem == 1, 0}; };
-  auto ask = [&](int to) {
-    follow();
-    load_lds4(lookup(), uniform(pages_at + to * kPagesBytes));
-    --ahead;
-  };
   {
     enter(start.ent, start.t);
-    ring[0] = asked();
-    const int page0 = *reinterpret_cast<const int32_t*>(lookup()), end0 = end;
-    int page1 = 0, end1 = 0;
-    if (kAhead == 2 && ahead > 0) {
-      follow();
-      --ahead;
-      ring[kAhead - 1] = asked();
-      page1 = *reinterpret_cast<const int32_t*>(lookup());
-      end1 = end;
-    }
-    if (ahead > 0) ask(0);
-    const Place y = locate(page0, ring[0].pos, end0, ring[0]);
-    begin_loads();
-    if (ring[0].live) fetch_all(y, 0);
+    ask();
+    wait_loads<0>();
+    Rows rows = {nullptr, nullptr, nullptr};
+    if (locate(ring[0], rows, 0)) fetch_all(rows, 0);
     if (kAhead == 2 && left > 0) {
-      const Place z = locate(page1, ring[kAhead - 1].pos, end1, ring[kAhead - 1]);
-      if (ring[kAhead - 1].live) fetch_all(z, 1);
+      if (batch_left == 0) wait_loads<0>();
+      if (locate(ring[kAhead - 1], rows, 1)) fetch_all(rows, 1);
     }
     __syncthreads();  // (the units' records)
   }
@@ -557,7 +592,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
     sees = seq_tokens(p, (int)n) - (p.Q - 1 - (int)qi);
   };
-  int unit = 0;               // of the tile whose values come next
+  int unit = 0;               // of the tile computed
   bool begun = start.t == 0;  // whether the piece begins where its unit does
   int later = 0;              // 1: behind the share's first piece
   load_q(unit_of(0));
@@ -582,7 +617,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   // Weights of the scores against the maximum in use, for the matrix unit in bf16;
   // their sum stays in fp32.  In 8 bits the tokens' scales go into them before
   // they are rounded.
-  auto weigh = [&](float base, __bf16* to) {
+  auto weigh = [&](float base) {
     sum = 0.f;
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
@@ -594,18 +629,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         pb[i] = (__bf16)(F8 ? w * sc[j][i] : w);
       }
       const int tk = 16 * (TB * tg + j) + 4 * lg;
-      *reinterpret_cast<bf16x4*>(to + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
+      *reinterpret_cast<bf16x4*>(prob + (rblock * 16 + ln) * kTile + (((tk >> 3) ^ (ln & 7)) << 3) + (tk & 7)) = pb;
     }
   };
-  auto score = [&](const Tile& x, int st, int par, int flag, const auto& load) {
-    const char *lat = stage[0] + st * kStageBytes, *rot = rotary[0] + st * kRotaryBytes;
-    if constexpr (F8) {
-      D::scores(lat + 16 * TB * tg * LP, rot + 16 * TB * tg * RP * 2, tscale[0] + st * kTile + 16 * TB * tg, qf, ln, lg, s, sc,
-                load);
-    } else {
-      D::scores(reinterpret_cast<const __bf16*>(lat) + (16 * TB * tg + ln) * LP,
-                reinterpret_cast<const __bf16*>(rot) + (16 * TB * tg + ln) * RP, qf, ln, lg, s, load);
-    }
+  // The scores of what a query row does not see, their maximum, and the weights.
+  auto soften = [&](const Tile& x, int par) {
     if (x.live != ~0ull || __any(x.pos + kTile > sees)) {
 #pragma unroll
       for (int j = 0; j < TB; ++j) {
@@ -630,13 +658,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     // The maximum in use follows the true one only when that is larger by
     // more than 8 (a factor of 256), as in latent decode.
     if (__any(mx > m + 8.f) || far) {
-      if (lane == 0) grown[flag] = 1;
+      if (lane == 0) grown[par] = 1;
     }
-    weigh(m == -INFINITY ? 0.f : m, prob[kLag ? par : 0]);
+    weigh(m == -INFINITY ? 0.f : m);
   };
   // Behind a barrier, where ``grown`` is set: the new maxima, the weights again, and
   // the older output's factor.
-  auto grow = [&](int par) {
+  auto grow = [&]() {
     if (scoring) {
       float mx = smax[0][rblock * 16 + ln];
 #pragma unroll
@@ -657,7 +685,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
           for (int i = 0; i < 4; ++i) s[j][i] = from_far(s[j][i], p.scale2, m);
         base = 0.f;
       }
-      weigh(base, prob[kLag ? par : 0]);
+      weigh(base);
     }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -667,13 +695,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
     lds_barrier();
   };
-  auto multiply = [&](int st, int par) {
-    if constexpr (F8)
-      D::values(stage[0] + st * kStageBytes, prob[kLag ? par : 0], wave, ln, lg, acc);
-    else
-      D::values(reinterpret_cast<const __bf16*>(stage[0] + st * kStageBytes), prob[0], wave, ln, lg, acc);
-  };
-
   // ---- the end of a piece, which is its unit's end too or not
   auto finish = [&](bool unit_ends) {
     const SharedParams& p = cold;
@@ -689,28 +710,39 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const bool whole = begun && unit_ends, direct = whole && (u.flags & kAlone);
     const int64_t slot = whole && (u.flags & kSingle) ? u.slot : 2 * w + later;
     const int col0 = wave * (MT * 16) + 4 * lg;
-    __bf16* out = p.out + ((int64_t)u.row0 + ln) * p.L + col0;
-    float* part = p.part + (slot * MB + ln) * p.L + col0;
+    float inv[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       float sum = smax[0][j * 16 + ln];
 #pragma unroll
       for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
-      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+      inv[j] = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    }
+    if (direct) {
+      __bf16* out = p.out + ((int64_t)u.row0 + ln) * p.L + col0;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if (j * 16 + ln < u.rows && col0 + 16 * i < p.L) {
-          const f32x4 o = acc[i][j] * inv;
-          if (direct) {
+      for (int j = 0; j < NB; ++j) {
+        if (j * 16 + ln < u.rows) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const f32x4 o = acc[i][j] * inv[j];
             const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-            *reinterpret_cast<bf16x4*>(out + 16 * i) = ob;
-          } else {
-            *reinterpret_cast<f32x4*>(part + 16 * i) = o;
+            if (!kPad || col0 + 16 * i < p.L) *reinterpret_cast<bf16x4*>(out + 16 * i) = ob;
           }
         }
+        out += 16 * p.L;
       }
-      out += 16 * p.L;
-      part += 16 * p.L;
+    } else {
+      float* part = p.part + (slot * MB + ln) * p.L + col0;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (j * 16 + ln < u.rows) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            if (!kPad || col0 + 16 * i < p.L) *reinterpret_cast<f32x4*>(part + 16 * i) = acc[i][j] * inv[j];
+        }
+        part += 16 * p.L;
+      }
     }
     const int r = keep_here(tid);
     if (r < u.rows) {
@@ -726,18 +758,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     begun = true;
     later = 1;
   };
-  auto restart = [&]() {
-    if (kLag) lds_barrier();  // (the readers of a piece's sums and maxima are done)
-    load_q(unit_of(unit));
-    clear();
-  };
-
-  int st = 0;  // the stage of the tile scored
-  Tile prev = {0, 0, 0};  // kLag: the tile scored before it
+  int st = 0;  // the stage of the tile computed
   for (int par = 0;; par ^= 1) {
     // this tile has landed (the next one's loads may be under way, and the lookup
     // before them is done), and the readers of the one before are done
-    if constexpr (F8 && kAhead == 2) {
+    if constexpr (kAhead == 2) {
       if (left > 0 && ring[1].live)
         wait_loads<D::kLoads>();
       else
@@ -746,74 +771,49 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       wait_loads<0>();
     }
     lds_barrier();
-    Tile cur = ring[0];
-    if (kLag && left < 0) cur.live = 0;  // (behind the last tile: its values are left)
-    [[maybe_unused]] const bool more = left > 0;  // a tile behind this one
-    const int to = kLag ? (st == NS - 1 ? 0 : st + 1) : (st == 0 ? NS - 1 : st - 1);  // the stage fetched to
-    if constexpr (kLag) {
-      if (prev.live && grown[st == 0 ? NS - 1 : st - 1]) grow(par ^ 1);
-    }
-    bool spread = false;  // whether the tile asked for is fetched along this one's scores
+    const Tile cur = ring[0];
+    const bool more = left > 0;                // a tile behind this one
+    const int to = st == 0 ? NS - 1 : st - 1;  // the stage fetched to: that of the tile before
+    if (tid == 0) grown[par ^ 1] = 0;
+    // A near tile's first load is issued here and the others along the scores, or all here by
+    // waves that score nothing.
     Rows rows = {nullptr, nullptr, nullptr};
-    if (left > kAhead - 1) {
-      Tile& x = ring[kAhead];
-      x = asked();
-      const int page = pages[par][wave][lane], before = end;
-      if (ahead > 0) ask(par ^ 1);
-      const Place y = locate(page, x.pos, before, x);
-      begin_loads();
-      spread = y.near && scoring && cur.live;
-      rows.lat = uniform(y.at.lat);
-      if (F8) {
-        rows.scale = uniform(y.at.scale);
-        if (RP > 0) rows.rot = uniform(y.at.rot);
+    const bool fetches = left > kAhead - 1 && locate(ring[kAhead], rows, to);
+    const bool spread = fetches && scoring && cur.live;
+    constexpr int kFirst = F8 ? 1 : D::kLoads - D::kLat;  // (a 16-bit tile's scores call for its latent loads alone)
+    if (fetches && !spread) fetch_all(rows, to);
+    if (kFirst > 0 && spread) fetch(rows, 0, to);
+    if (cur.live) {
+      if (scoring) {
+        const char *lat = stage[0] + st * kStageBytes, *rot = rotary[0] + st * kRotaryBytes;
+        auto load = [&](int i) {
+          if (spread) fetch(rows, F8 ? i : i + kFirst, to);
+        };
+        if constexpr (F8)
+          D::scores(lat + 16 * TB * tg * LP, rot + 16 * TB * tg * RP * 2, tscale[0] + st * kTile + 16 * TB * tg, qf, ln, lg,
+                    s, sc, load);
+        else
+          D::scores(reinterpret_cast<const __bf16*>(lat) + (16 * TB * tg + ln) * LP,
+                    reinterpret_cast<const __bf16*>(rot) + (16 * TB * tg + ln) * RP, qf, ln, lg, s, load);
+        soften(cur, par);
       }
-      if (!spread && x.live) fetch_all(y, to);
-    }
-    auto load = [&](int i) {
-      if (spread) fetch(rows, i, to);
-    };
-    constexpr int kFirst = D::kLoads - D::kLat;  // (a 16-bit tile's scores call for the latent loads alone)
-    if constexpr (!F8) {
-      if (kFirst > 0) load(0);
-    }
-    if constexpr (kLag) {
-      const int before = st == 0 ? NS - 1 : st - 1;
-      if (prev.live) l = l * fac + sum;
+      lds_barrier();
       fac = 1.f;
-      if (tid == 0) grown[to] = 0;  // (read by all behind the barrier before, set behind the next one)
-      // Half of the waves (one a SIMD) score first, half multiply first, so that one
-      // wave's products run beside the other's conversions and exponentials.  Where a
-      // unit ends, all multiply first.
-      const bool ends = prev.last || left < 0, later_values = !ends && wave < kWaves / 2;
-      if (!later_values && prev.live) multiply(before, par ^ 1);
-      if (ends) {
-        finish(prev.last);
-        if (left < 0) return;
-        restart();
+      if (grown[par]) grow();
+      l = l * fac + sum;
+      if constexpr (F8)
+        D::values(stage[0] + st * kStageBytes, prob, wave, ln, lg, acc);
+      else
+        D::values(reinterpret_cast<const __bf16*>(stage[0] + st * kStageBytes), prob, wave, ln, lg, acc);
+    }
+    if (!more || cur.last) {
+      if (more) load_q(unit_of(unit + 1));
+      finish(cur.last);
+      if (!more) {
+        wait_loads<0>();  // no load to LDS outlives the workgroup
+        return;
       }
-      if (scoring && cur.live) score(cur, st, par, st, load);
-      if (later_values && prev.live) multiply(before, par ^ 1);
-      prev = cur;
-    } else {
-      if (tid == 0) grown[par ^ 1] = 0;
-      if (cur.live) {
-        if (scoring)
-          score(cur, st, par, par, [&](int i) { load(F8 ? i : i + kFirst); });
-        lds_barrier();
-        fac = 1.f;
-        if (grown[par]) grow(par);
-        l = l * fac + sum;
-        multiply(st, 0);
-      }
-      if (!more || cur.last) {
-        finish(cur.last);
-        if (!more) {
-          wait_loads<0>();  // no load to LDS outlives the workgroup
-          return;
-        }
-        restart();
-      }
+      clear();
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) ring[i] = ring[i + 1];

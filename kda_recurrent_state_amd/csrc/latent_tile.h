@@ -296,13 +296,13 @@ struct Fp8Tile {
 
   // S^T[token][row] of the wave's tokens and rows, and the tokens' scales; a lane
   // holds tokens 4 lg + i of each block.  lat, rot, scale: of the group's first
-  // token.  Operands are read two steps ahead of their products, and load(i), 0 <= i
+  // token.  Operands are read two steps ahead of their products, and load(i), 0 < i
   // < kLoads, is called along the way, as in Bf16Tile.
   template <typename Load>
   static __device__ __forceinline__ void scores(const char* lat, const char* rot, const float* scale,
                                                 const bf16x8 (&qf)[KS], int ln, int lg, f32x4 (&s)[TB], f32x4 (&sc)[TB],
                                                 const Load& load) {
-    constexpr int M = LP / 64, KR = RP / 32, LG = (kLoads + M - 1) / M;
+    constexpr int M = LP / 64, KR = RP / 32, LG = (kLoads - 1 + M - 1) / M;
     const char* row = lat + ln * LP;
     const int at0 = (lg ^ swizzle(ln)) * 16;  // of chunk 4 m + lg: m's bits are xored or above
     u32x4 x[3][TB];
@@ -311,7 +311,7 @@ struct Fp8Tile {
       for (int j = 0; j < TB; ++j)
         x[m % 3][j] = *reinterpret_cast<const u32x4*>(row + j * 16 * LP + (m >> 2) * 256 + (at0 ^ ((m & 3) * 64)));
     };
-    f32x4 acc[TB][2], ro[TB];
+    f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, ro[TB];  // two chains of products: a block's each, or both of one's
     bf16x8 y[TB];
     const int y0 = (lg ^ ((ln >> 1) & 7)) * 16;
     auto rotary = [&](int k) {
@@ -319,7 +319,7 @@ struct Fp8Tile {
       for (int j = 0; j < TB; ++j) y[j] = *reinterpret_cast<const bf16x8*>(rot + (16 * j + ln) * RP * 2 + (y0 ^ (k * 64)));
     };
 #pragma unroll
-    for (int j = 0; j < TB; ++j) acc[j][0] = acc[j][1] = ro[j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < TB; ++j) ro[j] = f32x4{0, 0, 0, 0};
     read(0);
     if (M > 1) read(1);
 #pragma unroll
@@ -333,13 +333,13 @@ struct Fp8Tile {
       }
       hold_order();
 #pragma unroll
-      for (int i = m * LG; i < kLoads && i < (m + 1) * LG; ++i) load(i);
+      for (int i = 1 + m * LG; i < kLoads && i < 1 + (m + 1) * LG; ++i) load(i);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < TB; ++j)
-          acc[j][TB == 1 ? h : 0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              widen(x[m % 3][j][2 * h], x[m % 3][j][2 * h + 1]), qf[2 * m + h], acc[j][TB == 1 ? h : 0], 0, 0, 0);
+          acc[h * TB + j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              widen(x[m % 3][j][2 * h], x[m % 3][j][2 * h + 1]), qf[2 * m + h], acc[h * TB + j & 1], 0, 0, 0);
       hold_order();
     }
 #pragma unroll
@@ -350,9 +350,9 @@ struct Fp8Tile {
     }
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
-      if (TB == 1) acc[j][0] += acc[j][1];
+      if (TB == 1) acc[0] += acc[1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[j][i] = fmaf(acc[j][0][i], sc[j][i], ro[j][i]);
+      for (int i = 0; i < 4; ++i) s[j][i] = fmaf(acc[j][i], sc[j][i], ro[j][i]);
     }
   }
 
