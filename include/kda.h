@@ -606,13 +606,12 @@ kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const
  * rows and order of workgroups hold.  With a shared prefix, query rows see the
  * first rows through the first sequence's table: where that has no page, no sequence
  * of the group sees the row.
- * Precision: as kda_latent_decode.  In 8 bits the queries (bf16) enter the
- * scores as sums of two e4m3 numbers times a power of two a row: exact but for
- * what lies 2^-18 below the row's largest component.  The 8-bit products are summed in
- * fp32 after an alignment in the matrix unit that keeps about 2^-13 of the largest product of 128.
+ * Precision: as kda_latent_decode; in 8 bits the codes enter both products as
+ * bf16, which holds them whole, a token's scale multiplies its latent score in fp32,
+ * and the softmax weight times the scale is rounded to bf16 once.
  * Codes must not be NaN (0x7f, 0xff): such a code can reach all queries of a tile of
- * 64 tokens.  A NaN or infinite scale reaches the queries that see its row and no others.
- * A query that holds an infinity or a NaN gets NaN.
+ * 64 tokens.  A NaN or infinite scale, or a NaN in a rotary key, reaches the queries
+ * that see its row and no others.
  */
 typedef struct {
   int64_t N, Q, H, L, R, G;

@@ -98,27 +98,33 @@ __device__ __forceinline__ int seq_tokens(const SharedParams& p, int n) {
   return len < 0 ? 0 : (len > room ? (int)room : len);
 }
 
-// a / b, with 32-bit numbers where they do (a division of 64 bits is a hundred instructions)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if ((uint64_t)(a | b) >> 32 == 0) return (unsigned)a / (unsigned)b;
-  return a / b;
+// a / b of 0 <= a < 2^52, 0 < b, or with ``narrow`` (the same in all lanes) < 2^31.  (The quotient
+// in fp64 is off by less than one; a division of 64-bit integers is four times the
+// instructions, and the plan's and the join's time is much of their own code's way
+// into the caches.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b, bool narrow) {
+  if (narrow) return (unsigned)a / (unsigned)b;
+  const int64_t q = (int64_t)((double)a / (double)b), r = a - q * b;
+  return q + (r < 0 ? -1 : (r >= b ? 1 : 0));
 }
 
 // The line in equal shares, none empty (fewer of them where there are fewer tiles).
 struct Shares {
   int64_t quot;
   int rem, count;
+  bool narrow;  // whether the line has fewer than 2^31 places
 };
 __device__ __forceinline__ Shares shares_of(int64_t total) {
   const bool few = total < kShares;
   return {few ? 1 : (int64_t)((uint64_t)total / kShares), few ? 0 : (int)((uint64_t)total % kShares),
-          few ? (int)total : kShares};
+          few ? (int)total : kShares, total >> 31 == 0};
 }
 __device__ __forceinline__ int64_t share_begin(const Shares& s, int w) { return w * s.quot + min(w, s.rem); }
 // the share that holds place x
 __device__ __forceinline__ int share_at(const Shares& s, int64_t x) {
   const int64_t longer = s.rem * (s.quot + 1);
-  return x < longer ? (int)quotient(x, s.quot + 1) : s.rem + (int)quotient(x - longer, s.quot);
+  const bool in = x < longer;
+  return (in ? 0 : s.rem) + (int)quotient(in ? x : x - longer, in ? s.quot + 1 : s.quot, s.narrow);
 }
 
 // Inclusive sums of two numbers over the workgroup's threads up to this one;
@@ -297,11 +303,11 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     const int64_t in = from - x.base;
     if (x.chunks == 1) {
       s.k = 0;
-      s.rb = (int)quotient(in, x.tiles + kEnd);
+      s.rb = (int)quotient(in, x.tiles + kEnd, sh.narrow);
     } else {
-      const unsigned y = (unsigned)quotient(in, x.row_blocks), longer = x.longer * (x.chunk + 1);
+      const unsigned y = (unsigned)quotient(in, x.row_blocks, sh.narrow), longer = x.longer * (x.chunk + 1);
       s.k = (int)(y < longer ? y / (unsigned)(x.chunk + 1) : x.longer + (y - longer) / (unsigned)x.chunk);
-      s.rb = (int)quotient(in - x.unit_begin(s.k, 0), x.chunk_tiles(s.k));
+      s.rb = (int)quotient(in - x.unit_begin(s.k, 0), x.chunk_tiles(s.k), sh.narrow);
     }
     const int64_t rest = in - x.unit_begin(s.k, s.rb) - x.room();
     s.t = rest > 0 ? (int)rest : 0;
@@ -554,21 +560,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     for (int i = 0; i < D::kLoads; ++i) fetch(y, i, to);
   };
 
-  int left = start.left - 1;  // tiles behind the one scored
-  Tile ring[kAhead + 1];      // the one scored, and those fetched ahead
-  {
-    enter(start.ent, start.t);
-    ask();
-    wait_loads<0>();
-    Rows rows = {nullptr, nullptr, nullptr};
-    if (locate(ring[0], rows, 0)) fetch_all(rows, 0);
-    if (kAhead == 2 && left > 0) {
-      if (batch_left == 0) wait_loads<0>();
-      if (locate(ring[kAhead - 1], rows, 1)) fetch_all(rows, 1);
-    }
-    __syncthreads();  // (the units' records)
-  }
-
   // ---- queries
   bf16x8 qf[KS];
   int sees = 0;  // tokens that row ln of the wave's block sees
@@ -592,10 +583,25 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
     sees = seq_tokens(p, (int)n) - (p.Q - 1 - (int)qi);
   };
+  int left = start.left - 1;  // tiles behind the one scored
+  Tile ring[kAhead + 1];      // the one scored, and those fetched ahead
+  {
+    enter(start.ent, start.t);
+    ask();
+    load_q(Unit{start.ent.row0 + rb * MB, min(MB, start.ent.rows - rb * MB), 0, 0});
+    wait_loads<0>();
+    Rows rows = {nullptr, nullptr, nullptr};
+    if (locate(ring[0], rows, 0)) fetch_all(rows, 0);
+    if (kAhead == 2 && left > 0) {
+      if (batch_left == 0) wait_loads<0>();
+      if (locate(ring[kAhead - 1], rows, 1)) fetch_all(rows, 1);
+    }
+    __syncthreads();  // (the units' records)
+  }
+
   int unit = 0;               // of the tile computed
   bool begun = start.t == 0;  // whether the piece begins where its unit does
   int later = 0;              // 1: behind the share's first piece
-  load_q(unit_of(0));
 
   float m, l;  // of row ln of the wave's block, over its tokens; units of scale2 s
   bool far;    // whether one of the wave's rows is_far
@@ -848,7 +854,9 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
   }
   float top = -INFINITY, sum = 0.f;
   f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-  auto join = [&](const Entity& x) {
+  for (int which = 0; have && which < 2; ++which) {  // the prefix's pieces, its own
+    if (which == 0 && own.group < 0) continue;
+    const Entity x = which == 1 ? own : scalar_load(p.ents + own.group);
     const int in = (int)(grow - x.row0), rb = in / MB, r = in - rb * MB;
     for (int k0 = 0; k0 < x.chunks; k0 += 64) {
       // lane i: the pieces of the row block's unit in chunk k0 + i, their number and where the first one is: the
@@ -903,10 +911,6 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
         top = mx;
       }
     }
-  };
-  if (have) {
-    if (own.group >= 0) join(scalar_load(p.ents + own.group));
-    if (own.chunks > 0) join(own);
   }
   if (parts > 1) {  // (uniform over the workgroup)
     osum[wave][0][lane] = o[0];

@@ -338,8 +338,8 @@ struct Fp8Tile {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < TB; ++j)
-          acc[h * TB + j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              widen(x[m % 3][j][2 * h], x[m % 3][j][2 * h + 1]), qf[2 * m + h], acc[h * TB + j & 1], 0, 0, 0);
+          acc[(h * TB + j) & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              widen(x[m % 3][j][2 * h], x[m % 3][j][2 * h + 1]), qf[2 * m + h], acc[(h * TB + j) & 1], 0, 0, 0);
       hold_order();
     }
 #pragma unroll

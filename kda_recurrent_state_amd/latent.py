@@ -11,7 +11,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import (KDA_BF16, KDA_E4M3, KDA_F32, KDAError, LatentDecodeArgs, LatentPrefillArgs, LatentSharedArgs,
+from ._lib import (KDA_BF16, KDA_E4M3, KDA_F32, KDA_I32, KDA_I64, KDAError, LatentDecodeArgs, LatentPrefillArgs, LatentSharedArgs,
                    LatentStore, PagePool, PageStore)
 from .api import _device as _checked_device, _index_code, _on_stream, _stream_handle
 
@@ -204,39 +204,55 @@ def kda_latent_decode(cache: torch.Tensor, page_table: torch.Tensor, lengths: to
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _pages(what: str, name: str, t: torch.Tensor, dense: int) -> int:
-    """Elements from page to page of a cache tensor [num_pages, page_size, ...] with dense pages."""
-    shape, stride = t.shape, t.stride()
-    run = 1
-    for d in range(len(shape) - 1, 0, -1):
-        if shape[d] != 1 and stride[d] != run:
-            raise KDAError(what, 4, "%s: the pages must be dense" % name)
-        run *= shape[d]
-    return stride[0] if shape[0] > 1 else max(run, dense)
+def _pages(what: str, name: str, shape, stride, run: int, align: int) -> int:
+    """Elements from page to page of a cache tensor [num_pages, page_size(, row)] whose pages, ``run`` elements, are
+    dense (of the only page: any such number that is a multiple of ``align``)."""
+    row = shape[2] if len(shape) == 3 else 1
+    if (shape[1] != 1 and stride[1] != row) or (row != 1 and stride[-1] != 1):
+        raise KDAError(what, 4, "%s: the pages must be dense" % name)
+    return stride[0] if shape[0] > 1 else -(-run // align) * align
 
 
 def _store(what: str, codes: torch.Tensor, scales: torch.Tensor, rope: Optional[torch.Tensor]):
-    """(num_pages, page_size, L, R, page strides) of an 8-bit latent cache's tensors."""
-    if codes.dim() != 3 or scales.dim() != 2 or (rope is not None and rope.dim() != 3):
-        raise KDAError(what, 3, "codes and rope must be 3-D, scales 2-D")
-    if codes.dtype not in _CODES:
-        raise KDAError(what, 2, "codes must be float8_e4m3fn or uint8, got %s" % codes.dtype)
-    if scales.dtype != torch.float32 or (rope is not None and rope.dtype != torch.bfloat16):
-        raise KDAError(what, 2, "scales must be float32 and rope bfloat16")
-    num_pages, page_size, L = codes.shape
-    R = 0 if rope is None else rope.shape[2]
-    if scales.shape != codes.shape[:2] or (rope is not None and rope.shape[:2] != codes.shape[:2]):
-        raise KDAError(what, 3, "need codes [num_pages,page_size,L], scales [num_pages,page_size], "
-                                "rope [num_pages,page_size,R]")
-    return (num_pages, page_size, L, R,
-            _pages(what, "codes", codes, -(-page_size * L // 16) * 16), _pages(what, "scales", scales, 1),
-            _pages(what, "rope", rope, -(-page_size * R // 8) * 8) if R > 0 else 0)
+    """The fields of a LatentStore for an 8-bit latent cache's tensors."""
+    shape, near = codes.shape, scales.shape
+    if len(shape) != 3 or len(near) != 2:
+        raise KDAError(what, 3, "codes must be 3-D, scales 2-D")
+    if codes.dtype not in _CODES or scales.dtype != torch.float32:
+        raise KDAError(what, 2, "codes must be float8_e4m3fn or uint8 and scales float32, got %s and %s"
+                       % (codes.dtype, scales.dtype))
+    num_pages, page_size, L = shape
+    R, rope_at, rope_page = 0, None, 0
+    if near[0] != num_pages or near[1] != page_size:
+        raise KDAError(what, 3, "need codes [num_pages,page_size,L] and scales [num_pages,page_size]")
+    if rope is not None:
+        rshape = rope.shape
+        if len(rshape) != 3 or rshape[0] != num_pages or rshape[1] != page_size:
+            raise KDAError(what, 3, "need rope [num_pages,page_size,R]")
+        if rope.dtype != torch.bfloat16:
+            raise KDAError(what, 2, "rope must be bfloat16, got %s" % rope.dtype)
+        R = rshape[2]
+        if R > 0:
+            rope_at = rope.data_ptr()
+            rope_page = _pages(what, "rope", rshape, rope.stride(), page_size * R, 8)
+    return (codes.data_ptr(), scales.data_ptr(), rope_at, num_pages, page_size, L, R,
+            _pages(what, "codes", shape, codes.stride(), page_size * L, 16),
+            _pages(what, "scales", near, scales.stride(), page_size, 1), rope_page)
 
 
 def _rows(what: str, name: str, t: torch.Tensor) -> int:
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    row, last = t.stride()
+    if last != 1 and t.shape[1] > 1:
         raise KDAError(what, 4, "the last dim of %s must be dense" % name)
-    return t.stride(0)
+    return row
+
+
+def _index(what: str, slots: torch.Tensor) -> int:
+    if slots.dtype == torch.int32:
+        return KDA_I32
+    if slots.dtype == torch.int64:
+        return KDA_I64
+    raise KDAError(what, 2, "slots must be int32 or int64, got %s" % slots.dtype)
 
 
 _VALUES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
@@ -260,23 +276,21 @@ def kda_latent_quantize_scatter(c: torch.Tensor, k_rope: Optional[torch.Tensor],
     what = "kda_latent_quantize_scatter"
     lib = _lib.load_library()
     dev = _device(c, k_rope, slots, codes, scales, rope)
-    num_pages, page_size, L, R, *strides = _store(what, codes, scales, rope)
-    if c.dim() != 2 or slots.dim() != 1 or (k_rope is not None and k_rope.dim() != 2):
-        raise KDAError(what, 3, "c and k_rope must be 2-D, slots 1-D")
-    T = c.shape[0]
-    if (c.shape[1] != L or slots.shape[0] != T or (0 if k_rope is None else k_rope.shape[1]) != R or
-            (k_rope is not None and k_rope.shape[0] != T)):
-        raise KDAError(what, 3, "need c [T,L], k_rope [T,R], slots [T] with the cache's L and R")
-    if c.dtype not in _VALUES or (k_rope is not None and k_rope.dtype != c.dtype):
+    store = _store(what, codes, scales, rope)
+    shape, given = c.shape, slots.shape
+    if len(shape) != 2 or len(given) != 1:
+        raise KDAError(what, 3, "c must be 2-D, slots 1-D")
+    T, R = shape[0], store[6]
+    dtype = _VALUES.get(c.dtype)
+    if dtype is None or (k_rope is not None and k_rope.dtype != c.dtype):
         raise KDAError(what, 2, "c and k_rope must both be bfloat16 or both float32")
+    if shape[1] != store[5] or given[0] != T or (R > 0 if k_rope is None else tuple(k_rope.shape) != (T, R)):
+        raise KDAError(what, 3, "need c [T,L], k_rope [T,R], slots [T] with the cache's L and R")
     if not slots.is_contiguous():
         raise KDAError(what, 4, "slots must be contiguous")
-    index = _index_code(slots)
-    rope_at = (k_rope.data_ptr(), _rows(what, "k_rope", k_rope)) if R > 0 else (None, 0)
-    store = LatentStore(codes.data_ptr(), scales.data_ptr(), rope.data_ptr() if R > 0 else None, num_pages, page_size,
-                        L, R, *strides)
-    _call(what, dev, stream, [], lib.kda_latent_quantize_scatter, store, c.data_ptr(), _rows(what, "c", c), *rope_at,
-          _VALUES[c.dtype], slots.data_ptr(), index, T)
+    _call(what, dev, stream, [], lib.kda_latent_quantize_scatter, LatentStore(*store), c.data_ptr(), _rows(what, "c", c),
+          k_rope.data_ptr() if R > 0 else None, _rows(what, "k_rope", k_rope) if R > 0 else 0, dtype, slots.data_ptr(),
+          _index(what, slots), T)
 
 
 def kda_latent_dequantize_gather(codes: torch.Tensor, scales: torch.Tensor, rope: Optional[torch.Tensor],
@@ -289,8 +303,9 @@ def kda_latent_dequantize_gather(codes: torch.Tensor, scales: torch.Tensor, rope
     what = "kda_latent_dequantize_gather"
     lib = _lib.load_library()
     dev = _device(codes, scales, rope, slots, out)
-    num_pages, page_size, L, R, *strides = _store(what, codes, scales, rope)
-    if slots.dim() != 1:
+    store = _store(what, codes, scales, rope)
+    given = slots.shape
+    if len(given) != 1:
         raise KDAError(what, 3, "slots must be 1-D")
     if not slots.is_contiguous():
         raise KDAError(what, 4, "slots must be contiguous")
@@ -298,14 +313,10 @@ def kda_latent_dequantize_gather(codes: torch.Tensor, scales: torch.Tensor, rope
         dtype = out.dtype
     if dtype not in _VALUES:
         raise KDAError(what, 2, "rows are read as bfloat16 or float32, not %s" % dtype)
-    T = slots.shape[0]
-    index = _index_code(slots)
     made = []
-    out = _out(what, "out", out, (T, L + R), dtype, dev, made)
-    store = LatentStore(codes.data_ptr(), scales.data_ptr(), rope.data_ptr() if R > 0 else None, num_pages, page_size,
-                        L, R, *strides)
-    _call(what, dev, stream, made, lib.kda_latent_dequantize_gather, store, slots.data_ptr(), index, T,
-          out.data_ptr(), _VALUES[dtype])
+    out = _out(what, "out", out, (given[0], store[5] + store[6]), dtype, dev, made)
+    _call(what, dev, stream, made, lib.kda_latent_dequantize_gather, LatentStore(*store), slots.data_ptr(),
+          _index(what, slots), given[0], out.data_ptr(), _VALUES[dtype])
     return out
 
 
@@ -341,20 +352,18 @@ def _decode_shared(what: str, cache, page_table, lengths, cu_groups, shared, q, 
         if R > 0:
             rope_q = (r4.data_ptr(), r4.stride()[:3])
     if fp8:
-        num_pages, page_size, Lc, Rc, *strides = _store(what, codes, scales, rope)
-        if Lc != L or Rc != R:
-            raise KDAError(what, 3, "cache rows hold %d + %d values, q and q_rope %d + %d" % (Lc, Rc, L, R))
-        head = (KDA_E4M3, codes.data_ptr(), scales.data_ptr(), rope.data_ptr() if R > 0 else None)
+        store = _store(what, codes, scales, rope)
+        if store[5] != L or store[6] != R:
+            raise KDAError(what, 3, "cache rows hold %d + %d values, q and q_rope %d + %d" % (store[5], store[6], L, R))
+        head = (KDA_E4M3, *store[:5], *store[7:])
     else:
-        if cache.dim() != 3:
-            raise KDAError(what, 3, "cache must be 3-D")
+        held = cache.shape
+        if len(held) != 3 or held[2] != L + R:
+            raise KDAError(what, 3, "cache must be [num_pages,page_size,%d] as q and q_rope are" % (L + R))
         if cache.dtype != torch.bfloat16:
             raise KDAError(what, 2, "cache must be bfloat16 or (codes, scales, rope), got %s" % cache.dtype)
-        num_pages, page_size, D = cache.shape
-        if D != L + R:
-            raise KDAError(what, 3, "cache rows hold %d values, q and q_rope %d" % (D, L + R))
-        strides = (_pages(what, "cache", cache, 1), 0, 0)
-        head = (KDA_BF16, cache.data_ptr(), None, None)
+        head = (KDA_BF16, cache.data_ptr(), None, None, held[0], held[1],
+                _pages(what, "cache", held, cache.stride(), held[1] * held[2], 8), 0, 0)
     if page_table.shape[0] != N or lengths.shape[0] != N:
         raise KDAError(what, 3, "page_table must be [N,max_pages] and lengths [N]")
     if (page_table.shape[1] > 1 and page_table.stride(1) != 1) or not lengths.is_contiguous():
@@ -374,11 +383,9 @@ def _decode_shared(what: str, cache, page_table, lengths, cu_groups, shared, q, 
     if lse is not None or with_lse:
         lse = _out(what, "lse", lse, shape[:-1], torch.float32, dev, made)
     ws = _workspace(workspace, lib.kda_latent_shared_workspace_size(N, Q, H, L, G), dev, made)
-    a = LatentSharedArgs(N, Q, H, L, R, G, *head, num_pages, page_size, *strides, page_table.data_ptr(),
-                         page_table.stride(0), page_table.shape[1], lengths.data_ptr(), *groups, q4.data_ptr(),
-                         q4.stride()[:3], *rope_q, out.data_ptr(), None if lse is None else lse.data_ptr(), scale, *ws)
-    _call(what, dev, stream, made, lib.kda_latent_decode_fp8 if what == "kda_latent_decode_fp8" else
-          lib.kda_latent_decode_shared, a)
+    a = LatentSharedArgs(N, Q, H, L, R, G, *head, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+                         lengths.data_ptr(), *groups, q4.data_ptr(), q4.stride()[:3], *rope_q, out.data_ptr(), None if lse is None else lse.data_ptr(), scale, *ws)
+    _call(what, dev, stream, made, getattr(lib, what), a)
     return out, lse
 
 

@@ -3,7 +3,6 @@ import math
 
 import torch
 
-from tests import latent_ref as ref
 
 
 def _value(code):
@@ -43,36 +42,3 @@ def quantize(x):
     up, down = grid[hi] - a, a - grid[lo]
     code = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
     return (code + torch.where(torch.signbit(y), 128, 0)).to(torch.uint8), scales
-
-
-def decode(cache, table, lengths, q, q_rope, scale):
-    """As ref.decode, over rows in fp64; rows that no query sees may hold NaN."""
-    return ref.decode(cache, table, lengths, q, q_rope, scale)
-
-
-def score_error(cache, q, scale):
-    """How far the 8-bit products' own sums can put a score off: they keep all but 2^-11 of the largest product
-    of 128, for the leading half of the query and for the rest (at most 2^-4 of it)."""
-    L = q.shape[-1]
-    big = q.double().abs().max().item() * cache[..., :L].nan_to_num(0, 0, 0).abs().max().item()
-    return scale * -(-L // 128) * (1 + 2.0 ** -4) * 2.0 ** -11 * big
-
-
-def check(out, lse, want, delta, name=""):
-    """As ref.check, with scores off by at most ``delta`` besides: each weight, and the sum that it is divided by, is off
-    by that part of itself, so out by 2 delta sum p |v| and lse by delta.  The bounds of ref.check: out is rounded to
-    bf16 (2^-8 of itself), the weights times scales were (2^-8 of sum p |v|), fp32 steps add under 2^-12; lse 1e-4."""
-    out_ref, lse_ref, mag = want
-    o = out.detach().cpu().double().reshape(out_ref.shape)
-    assert torch.isfinite(o).all(), name
-    bound = 2.0 ** -8 * out_ref.abs() + (2.0 ** -8 + 2.0 ** -12 + 2 * delta) * mag + 1e-30
-    over = ((o - out_ref).abs() / bound).max().item()
-    rel = ((o - out_ref).norm() / out_ref.norm().clamp(min=1e-30)).item()
-    print("  %s out: worst %.2f of its bound, relative L2 %.2e" % (name, over, rel), flush=True)
-    assert over <= 1.0, (name, over)
-    if lse is not None:
-        s = lse.detach().cpu().double().reshape(lse_ref.shape)
-        empty = torch.isinf(lse_ref)
-        assert torch.equal(torch.isinf(s) & (s < 0), empty), name
-        off = (s - lse_ref)[~empty].abs().max().item() if (~empty).any() else 0.0
-        assert off <= 1e-4 + delta, (name, off)

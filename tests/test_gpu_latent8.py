@@ -185,8 +185,7 @@ def test_decode8(lens, Q, H, L, R, page):
     out, lse = kda.kda_latent_decode_fp8(*_gpu(store), table.cuda(), _i32(lens), q.cuda(),
                                          None if q_rope is None else q_rope.cuda(), scale=SCALE, with_lse=True)
     rows = ref8.values(*store)
-    ref8.check(out, lse, ref8.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE),
-               ref8.score_error(rows, q, SCALE), "decode8")
+    ref.check(out, lse, ref.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE), "decode8")
 
 
 def test_decode8_bad_pages_and_lengths():
@@ -209,8 +208,7 @@ def test_decode8_bad_pages_and_lengths():
     out, lse = kda.kda_latent_decode_fp8(*_gpu(store), table.cuda(), _i32(lens), q.cuda(), q_rope.cuda(), scale=SCALE,
                                          with_lse=True)
     rows = ref8.values(*store).nan_to_num(0)
-    ref8.check(out, lse, ref8.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE),
-               ref8.score_error(rows, q, SCALE), "bad pages")
+    ref.check(out, lse, ref.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE), "bad pages")
     assert (out[1] == 0).all() and (out[2] == 0).all() and (lse[1] == -math.inf).all()
 
 
@@ -224,7 +222,7 @@ def test_decode8_row_that_is_not_finite_reaches_who_sees_it(what):
     store = _cache8(gen, pages, page, 512, 64)
     q, q_rope = _queries(gen, 2, 3, 12, 512, 64)
     rows = ref8.values(*store)
-    want = ref8.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE)
+    want = ref.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE)
     place = table[0, 149 // page], 149 % page
     if what == "scale":
         store[1][place] = math.nan
@@ -233,9 +231,8 @@ def test_decode8_row_that_is_not_finite_reaches_who_sees_it(what):
     out, lse = kda.kda_latent_decode_fp8(*_gpu(store), table.cuda(), _i32(lens), q.cuda(), q_rope.cuda(), scale=SCALE,
                                          with_lse=True)
     assert out[0, 2].isnan().all()
-    delta = ref8.score_error(rows, q, SCALE)
-    ref8.check(out[0, :2], lse[0, :2], [x[0, :2] for x in want], delta, "before it")
-    ref8.check(out[1], lse[1], [x[1] for x in want], delta, "beside it")
+    ref.check(out[0, :2], lse[0, :2], [x[0, :2] for x in want], "before it")
+    ref.check(out[1], lse[1], [x[1] for x in want], "beside it")
 
 
 # --- shared prefixes ----------------------------------------------------------
@@ -276,10 +273,8 @@ def _run_shared(store, table, lens, cu, shared, q, q_rope, **kw):
 
 
 def _check_shared(store, table, lens, q, q_rope, got, name):
-    fp8 = len(store) == 3
-    rows = ref8.values(*store) if fp8 else store[0].double()
-    want = ref8.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE)
-    ref8.check(*got, want, ref8.score_error(rows, q, SCALE) if fp8 else 0.0, name)
+    rows = ref8.values(*store) if len(store) == 3 else store[0].double()
+    ref.check(*got, ref.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE), name)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -302,3 +297,399 @@ def test_shared(groups, alone, Q, H, L, R, page, fp8):
     store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, groups, page, L, R, fp8, Q, H, alone)
     got = _run_shared(store, table, lens, cu, shared, q, q_rope)
     _check_shared(store, table, lens, q, q_rope, got, "shared")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("many", ["sequences", "groups", "room"])
+def test_shared_plans_of_large_batches(many, fp8):
+    """More sequences or groups than the kernels plan by themselves, and a table with more room than 31 bits of tiles."""
+    gen = torch.Generator().manual_seed(3)
+    if many == "sequences":
+        groups, alone = [(100, [130 + i % 50 for i in range(30)]), (64, [70] * 200), (0, [5, 9])], [40 + i % 90 for i in range(400)]
+    elif many == "groups":
+        groups, alone = [(40 + i, [60 + i, 50 + i, 30]) for i in range(70)] + [(10, [])] * 5, (90, 1)
+    else:
+        groups, alone = [(300, [310, 400, 299])], (50, 200)
+    Q, H, L, R, page = 2, 8, 128, 32, 16
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, groups, page, L, R, fp8, Q, H, alone)
+    if many == "room":
+        wide = torch.full((table.shape[0], 1 << 26), -1, dtype=torch.int32, device="cuda")
+        wide[:, : table.shape[1]] = table.cuda()
+        import kda_recurrent_state_amd as kda
+        cache = _gpu(store) if fp8 else store[0].cuda()
+        got = kda.kda_latent_decode_shared(cache, wide, _i32(lens), _i32(cu), _i32(shared), q.cuda(), q_rope.cuda(),
+                                           scale=SCALE, with_lse=True)
+    else:
+        got = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, many)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_groups_that_are_no_offsets(fp8):
+    """Bounds that fall are raised to the largest before, and clamped to the batch; shared lengths are clamped."""
+    gen = torch.Generator().manual_seed(11)
+    groups = [(64, [100, 90, 80]), (32, [50, 60])]
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, groups, 16, 128, 64, fp8, 1, 16, (30, 40))
+    for bad_cu, bad_shared in [([1, 4, 2, 6], [64, 7, 32]), ([-3, 1, 4, 6, 900], [0, 64, 32, -5]),
+                               ([1, 4, 6], [64, -9]), ([9, 1, 4], [5, 5]), ([0, 0, 0], [1000, 1000])]:
+        got = _run_shared(store, table, lens, bad_cu, bad_shared, q, q_rope)
+        _check_shared(store, table, lens, q, q_rope, got, str(bad_cu))
+    # as many shared as the first one has, or more: up to its length, which the others agree on as well
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, [(100, [100, 130, 101])], 16, 128, 64, fp8, 1, 16)
+    got = _run_shared(store, table, lens, cu, [2 ** 31 - 1], q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "long")
+
+
+def test_shared_without_groups_and_as_latent_decode():
+    """No groups: each for itself.  16 bits: as kda_latent_decode up to roundings."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(12)
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, [(500, [700, 600, 501])], 64, 512, 64, False, 1, 32, (5, 900))
+    none = _run_shared(store, table, lens, [0], [], q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, none, "no groups")
+    some = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    one = kda.kda_latent_decode(store[0].cuda(), table.cuda(), _i32(lens), q.cuda(), q_rope.cuda(), scale=SCALE, with_lse=True)
+    for x in (none, some):
+        # each is off the true result by the bounds that _check_shared has
+        assert ((x[0].float() - one[0].float()).norm() / one[0].float().norm()).item() < 2.0 ** -7
+        assert (x[1] - one[1]).abs().max().item() <= 2e-4
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_views_and_given_outputs(fp8):
+    """Queries of a joint projection, a page table and caches that are views of larger ones, outputs and a workspace
+    of exactly the size given; what lies around them stays."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(13)
+    Q, H, L, R, page = 2, 12, 256, 32, 16
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, [(160, [200, 170, 161])], page, L, R, fp8, Q, H, (70,))
+    N = len(lens)
+    joint = torch.randn(N, H, Q, L + R + 24).to(BF16).cuda()
+    joint[..., :L], joint[..., L: L + R] = q.transpose(1, 2).cuda(), q_rope.transpose(1, 2).cuda()
+    qv, rv = joint[..., :L].transpose(1, 2), joint[..., L: L + R].transpose(1, 2)
+    wide = torch.full((N, table.shape[1] + 5), 2 ** 30, dtype=torch.int32, device="cuda")
+    wide[:, : table.shape[1]] = table.cuda()
+    views = []
+    for x in _gpu(store):
+        big = torch.full((x.shape[0], 3) + tuple(x.shape[1:]), 0x7f if x.dtype == torch.uint8 else math.nan, dtype=x.dtype,
+                         device="cuda")
+        big[:, 1] = x
+        views.append(big[:, 1])
+    need = kda.kda_latent_shared_workspace_size(N, Q, H, L, 1)
+    room = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    outs = torch.full((N + 2, Q, H, L), 7.0, dtype=BF16, device="cuda")
+    lses = torch.full((N + 2, Q, H), 7.0, device="cuda")
+    out, lse = kda.kda_latent_decode_shared(tuple(views) if fp8 else views[0], wide[:, : table.shape[1]], _i32(lens), _i32(cu),
+                                            _i32(shared), qv, rv, scale=SCALE, out=outs[1: N + 1], lse=lses[1: N + 1],
+                                            workspace=room[:need])
+    assert out.data_ptr() == outs[1].data_ptr() and lse.data_ptr() == lses[1].data_ptr()
+    _check_shared(store, table, lens, q, q_rope, (out, lse), "views")
+    assert (room[need:] == 0x5a).all() and (outs[0] == 7).all() and (outs[-1] == 7).all()
+    assert (lses[0] == 7).all() and (lses[-1] == 7).all()
+    # one query row for all heads and queries: strides of 0
+    one = q[:, :1, :1].cuda().expand(N, Q, H, L), q_rope[:, :1, :1].cuda().expand(N, Q, H, R)
+    got = kda.kda_latent_decode_shared(tuple(views) if fp8 else views[0], wide[:, : table.shape[1]], _i32(lens), _i32(cu),
+                                       _i32(shared), *one, scale=SCALE, with_lse=True)
+    _check_shared(store, table, lens, q[:, :1, :1].expand(N, Q, H, L), q_rope[:, :1, :1].expand(N, Q, H, R), got, "broadcast")
+    three = kda.kda_latent_decode_shared(tuple(views) if fp8 else views[0], wide[:, : table.shape[1]], _i32(lens), _i32(cu),
+                                         _i32(shared), qv[:, 1], rv[:, 1], scale=SCALE)
+    assert three[0].shape == (N, H, L) and three[1] is None
+    _check_shared(store, table, lens, q[:, 1:], q_rope[:, 1:], (three[0], None), "3-D")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_twice_is_the_same(fp8):
+    gen = torch.Generator().manual_seed(14)
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, [(3000, [3100 + 7 * i for i in range(9)])], 64, 512, 64, fp8,
+                                                               1, 20, (900,))
+    a = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    b = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e15, 2e37])  # (the query holds 13.86 times that: bf16 ends at 3.39e38)
+def test_scores_of_any_size(size, fp8):
+    """One component of the query and of some rows is so large that their scores stand alone, far beyond the step of
+    fp32; the type's lowest value as the score of the others.  The weights are those of the large scores alone."""
+    gen = torch.Generator().manual_seed(15)
+    page, L, R, H = 16, 128, 64, 8
+    lens = [400, 330, 300]
+    table, pages = _table(gen, lens, page)
+    rows = torch.randn(pages * page, L + R, generator=gen)
+    # the rotary key is held in 16 bits in both caches: component 3 makes the scores 0 or -size or, of a few rows, size
+    rows[:, L + 3] = -1.0
+    few = [5, 100, 333]
+    for n in range(3):
+        for j in few:
+            if j < lens[n]:
+                rows[int(table[n, j // page]) * page + j % page, L + 3] = 1.0
+    store = (*[x.view(pages, page, *x.shape[1:]) for x in ref8.quantize(rows[:, :L].double())],
+             rows[:, L:].to(BF16).view(pages, page, R)) if fp8 else (rows.to(BF16).view(pages, page, L + R),)
+    if fp8:
+        store = (store[0], store[1].float(), store[2])
+    q, q_rope = _queries(gen, 3, 1, H, L, R)
+    q, q_rope = q * 0, q_rope * 0
+    q_rope[..., 3] = size / SCALE
+    got = _run_shared(store, table, lens, [0, 1], [10], q, q_rope)
+    for n in range(3):
+        seen = [j for j in few if j < lens[n]]
+        at = [int(table[n, j // page]) * page + j % page for j in seen]
+        values = (ref8.values(*store) if fp8 else store[0].double()).view(pages * page, -1)[at, :L]
+        want = values.mean(0)
+        bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * values.abs().mean(0)
+        assert ((got[0][n, 0].double().cpu() - want).abs() <= bound).all()
+        top = float(q_rope[0, 0, 0, 3].double()) * SCALE
+        assert (got[1][n].double().cpu() - (top + math.log(len(seen)))).abs().max() <= 2.0 ** -20 * top + 1e-4
+
+
+def test_decode8_query_that_is_not_finite():
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(16)
+    lens = [100, 200]
+    table, pages = _table(gen, lens, 16)
+    store = _cache8(gen, pages, 16, 128, 8)
+    q, q_rope = _queries(gen, 2, 1, 8, 128, 8)
+    rows = ref8.values(*store)
+    want = ref.decode(rows, table, torch.tensor(lens), q, q_rope, SCALE)
+    q[0, 0, 3, 5] = math.nan
+    out, lse = kda.kda_latent_decode_fp8(*_gpu(store), table.cuda(), _i32(lens), q.cuda(), q_rope.cuda(), scale=SCALE, with_lse=True)
+    assert out[0, 0, 3].isnan().all() and lse[0, 0, 3].isnan()
+    keep = torch.ones(2, 1, 8, dtype=torch.bool)
+    keep[0, 0, 3] = False
+    assert torch.isfinite(out.cpu()[keep]).all()
+    ref.check(out.cpu()[keep], lse.cpu()[keep], [x[keep] for x in want], "others")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_beyond_32_bits(fp8):
+    """A cache of over 2^32 bytes (and 2^31 elements); the sequences' pages lie at its beginning and its end."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(17)
+    page, L, R, H = 64, 512, 64, 16
+    lens = [130, 300, 64]
+    table, few = _table(gen, lens, page, extra=0)
+    pages = (1 << 32) // (page * L) + 1000 if fp8 else (1 << 32) // (page * (L + R) * 2) + 1000
+    where = torch.cat([torch.arange(few // 2), torch.arange(pages - (few - few // 2), pages)])
+    table = torch.where(table >= 0, where[table.clamp(min=0).long()].int(), table)
+    small = _cache8(gen, few, page, L, R) if fp8 else (torch.randn(few, page, L + R, generator=gen).to(BF16),)
+    big = []
+    for x in small:
+        y = torch.zeros((pages,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+        y[where.cuda()] = x.cuda()
+        big.append(y)
+    q, q_rope = _queries(gen, 3, 1, H, L, R)
+    back = {int(w): i for i, w in enumerate(where)}
+    near = torch.tensor([[back.get(int(p), -1) for p in row] for row in table], dtype=torch.int32)
+    got = kda.kda_latent_decode_shared(tuple(big) if fp8 else big[0], table.cuda(), _i32(lens), _i32([0, 3]), _i32([0]), q.cuda(),
+                                       q_rope.cuda(), scale=SCALE, with_lse=True)
+    _check_shared(small, near, lens, q, q_rope, got, "far pages")
+    if fp8:
+        # written and read at both ends
+        c, k_rope = _rows(40, L, R, BF16, 5)
+        slots = torch.cat([torch.arange(20), torch.arange(pages * page - 20, pages * page)])
+        kda.kda_latent_quantize_scatter(c, k_rope, slots.cuda(), *big)
+        want, scale = ref8.quantize(c.cpu().double())
+        assert torch.equal(big[0].view(-1, L)[slots.cuda()].cpu(), want)
+        assert torch.equal(big[1].view(-1)[slots.cuda()].cpu().double(), scale)
+        rows = kda.kda_latent_dequantize_gather(*big, slots.flip(0).cuda(), dtype=torch.float32).cpu()
+        assert torch.equal(rows[:, :L].double(), (ref8.VALUES[want.long()] * scale[:, None]).flip(0).float().double())
+        assert torch.equal(rows[:, L:], k_rope.cpu().float().flip(0))
+
+
+def test_captured_calls_follow_their_inputs():
+    """Two graphs with workspaces of their own, replayed in turn with eager work between; lengths, groups and the cache
+    change between replays."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(18)
+    page, L, R, H, N = 16, 256, 64, 16, 5
+    table, pages = _table(gen, [700] * N, page)
+    store = _gpu(_cache8(gen, pages, page, L, R))
+    q, q_rope = (x.cuda() for x in _queries(gen, N, 1, H, L, R))
+    table[1:, : 400 // page] = table[0, : 400 // page]     # the first 400 tokens are shared
+    lens, cu, shared = _i32([0] * N), _i32([0, N]), _i32([0])
+    c, k_rope = torch.randn(N, L, generator=gen).to(BF16).cuda(), torch.randn(N, R, generator=gen).to(BF16).cuda()
+    slots = torch.zeros(N, dtype=torch.int64, device="cuda")
+    dtable = table.cuda()
+    outs = []
+
+    def step(i):
+        kda.kda_latent_quantize_scatter(c, k_rope, slots, *store)
+        if i == 0:
+            kda.kda_latent_decode_shared(store, dtable, lens, cu, shared, q, q_rope, scale=SCALE, out=outs[i][0], lse=outs[i][1],
+                                         workspace=outs[i][2])
+        else:
+            kda.kda_latent_decode_fp8(*store, dtable, lens, q, q_rope, scale=SCALE, out=outs[i][0], lse=outs[i][1],
+                                      workspace=outs[i][2])
+        outs[i][3].copy_(kda.kda_latent_dequantize_gather(*store, slots, out=outs[i][4]))
+
+    graphs = []
+    for i in range(2):
+        need = kda.kda_latent_shared_workspace_size(N, 1, H, L, 1 - i)
+        outs.append((torch.empty(N, 1, H, L, dtype=BF16, device="cuda"), torch.empty(N, 1, H, device="cuda"),
+                     torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty(N, L + R, dtype=BF16, device="cuda"),
+                     torch.empty(N, L + R, dtype=BF16, device="cuda")))
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            step(i)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            step(i)
+    for turn, (ls, share) in enumerate([([500, 450, 401, 699, 640], 400), ([100, 0, 700, 1, 50], 0), ([400, 500, 600, 650, 410], 333),
+                                        ([0] * 5, 400), ([700] * 5, 400)]):
+        lens.copy_(_i32(ls))
+        shared.fill_(share)
+        # each sequence's last token is written by the call itself (behind what is shared)
+        at = [int(table[n, (ls[n] - 1) // page]) * page + (ls[n] - 1) % page if ls[n] > 400 else -1 for n in range(N)]
+        slots.copy_(torch.tensor(at, device="cuda"))
+        c.copy_(torch.randn(N, L, generator=gen))
+        for i in (0, 1):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        cpu = [x.cpu() for x in store]
+        rows = ref8.values(*cpu)
+        want = ref.decode(rows, table, torch.tensor(ls), q.cpu(), q_rope.cpu(), SCALE)
+        for i in (0, 1):
+            ref.check(outs[i][0], outs[i][1], want, "replay %d of graph %d" % (turn, i))
+            flat = torch.where((slots >= 0)[:, None].cpu(), rows.view(-1, L + R)[slots.clamp(min=0).cpu()], 0.0)
+            assert torch.equal(outs[i][3].cpu().double(), flat)
+        torch.randn(1000, device="cuda").sum().item()         # eager work between
+
+
+def test_other_streams_and_calls_at_once():
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(19)
+    sets = [_shared_inputs(gen, [(1000 + 500 * i, [1600 + 100 * i + 9 * j for j in range(6)])], 64, 512, 64, i == 1, 1, 16)
+            for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    on = [(_gpu(s[0]) if i == 1 else s[0][0].cuda(), s[1].cuda(), _i32(s[2]), _i32(s[3]), _i32(s[4]), s[5].cuda(), s[6].cuda())
+          for i, s in enumerate(sets)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            got[i].append(kda.kda_latent_decode_shared(*on[i], scale=SCALE, with_lse=True, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, s in enumerate(sets):
+        _check_shared(s[0], s[1], s[2], s[5], s[6], got[i][0], "stream %d" % i)
+        for more in got[i][1:]:
+            assert torch.equal(more[0], got[i][0][0]) and torch.equal(more[1], got[i][0][1])
+    store = _empty_store(4, 16, 128, 8)
+    c, k_rope = _rows(50, 128, 8, BF16, 2)
+    slots = torch.arange(50, device="cuda")
+    torch.cuda.synchronize()
+    kda.kda_latent_quantize_scatter(c, k_rope, slots, *store, stream=streams[0])
+    rows = kda.kda_latent_dequantize_gather(*store, slots, stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(rows.cpu().double(), ref8.values(*store).view(-1, 136)[:50])
+
+
+def test_a_serving_run():
+    """Prompts written, forked with shared pages, continued one token at a time by the children, attended to with the
+    prompt computed once, compacted, read back and freed: the rows and results are those of the tokens themselves."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(20)
+    page, L, R, H, seqs, per, pages = 16, 128, 64, 16, 8, 12, 60
+    store = _empty_store(pages, page, L, R)
+    for x in store:
+        x.zero_()
+    table = torch.full((seqs, per), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(seqs, dtype=torch.int32, device="cuda"), torch.zeros(pages, dtype=torch.int32, device="cuda")
+    tokens = {}                                                    # of a slot: its rows in fp64
+
+    def rows_of(n):
+        x = torch.randn(n, L + R, generator=gen).to(BF16)
+        codes, scales = ref8.quantize(x[:, :L].double())
+        return x.cuda(), torch.cat([ref8.VALUES[codes.long()] * scales[:, None], x[:, L:].double()], 1)
+
+    # two prompts, in pages from the end of the pool
+    at = pages
+    for s, n in ((0, 70), (4, 37)):
+        used = -(-n // page)
+        table[s, :used] = torch.arange(at - used, at, dtype=torch.int32, device="cuda")
+        at -= used
+        lens[s], refs[table[s, :used].long()] = n, 1
+        x, tokens[s] = rows_of(n)
+        j = torch.arange(n, device="cuda")
+        kda.kda_latent_quantize_scatter(x[:, :L], x[:, L:], table[s].long()[j // page] * page + j % page, *store)
+    status = kda.kda_page_fork(table, lens, refs, _i32([0, 0, 0, 4]), _i32([1, 2, 3, 5]), page, caches=list(store))
+    assert status.tolist() == [0] * 4
+    for child, parent in ((1, 0), (2, 0), (3, 0), (5, 4)):
+        tokens[child] = tokens[parent]
+    order = [0, 1, 2, 3, 4, 5]
+    cu, shared = _i32([0, 4, 6]), _i32([70 // page * page, 37 // page * page])
+    for turn in range(3):
+        # one new token each; a page of its own where the last one is full (taken by hand: the pool's first free one)
+        new, values = rows_of(len(order))
+        slots = []
+        for i, s in enumerate(order):
+            n = int(lens[s])
+            if n % page == 0:
+                free = int((refs <= 0).nonzero()[0])
+                table[s, n // page], refs[free] = free, 1
+            slots.append(int(table[s, n // page]) * page + n % page)
+            lens[s] = n + 1
+            tokens[s] = torch.cat([tokens[s], values[i: i + 1]])
+        kda.kda_latent_quantize_scatter(new[:, :L], new[:, L:], torch.tensor(slots, device="cuda"), *store)
+        q, q_rope = _queries(gen, 6, 1, H, L, R)
+        got = kda.kda_latent_decode_shared(store, table[:6], lens[:6], cu, shared, q.cuda(), q_rope.cuda(), scale=SCALE,
+                                           with_lse=True)
+        alone = kda.kda_latent_decode_fp8(*store, table[:6], lens[:6], q.cuda(), q_rope.cuda(), scale=SCALE, with_lse=True)
+        for s in order:
+            full = torch.cat([q[s, 0].double(), q_rope[s, 0].double()], -1)
+            want = ref.attend(full, tokens[s], tokens[s][:, :L], torch.full((H,), len(tokens[s])), SCALE)
+            ref.check(got[0][s, 0], got[1][s, 0], want, "turn %d, slot %d" % (turn, s))
+            ref.check(alone[0][s, 0], alone[1][s, 0], want, "turn %d, slot %d alone" % (turn, s))
+        if turn == 1:
+            kda.kda_page_compact(table, lens, refs, page, caches=list(store))
+    for s in order:
+        j = torch.arange(len(tokens[s]), device="cuda")
+        back = kda.kda_latent_dequantize_gather(*store, table[s].long()[j // page] * page + j % page)
+        assert torch.equal(back.cpu().double(), tokens[s])
+    kda.kda_page_free(table, lens, refs, torch.ones(seqs, dtype=torch.bool, device="cuda"), page)
+    assert (refs == 0).all() and (lens == 0).all()
+
+
+def test_python_refusals():
+    import kda_recurrent_state_amd as kda
+    codes, scales, rope = _empty_store(4, 16, 128, 8)
+    c, k_rope = _rows(10, 128, 8, BF16, 2)
+    slots = torch.arange(10, device="cuda")
+    q, q_rope = (x.cuda() for x in _queries(torch.Generator().manual_seed(1), 1, 1, 8, 128, 8))
+    table, lens, cu, sh = _i32([[0, 1]]), _i32([20]), _i32([0, 1]), _i32([0])
+    write, read = kda.kda_latent_quantize_scatter, kda.kda_latent_dequantize_gather
+    shared, fp8 = kda.kda_latent_decode_shared, kda.kda_latent_decode_fp8
+    store = (codes, scales, rope)
+    for call in [
+            lambda: write(c, k_rope, slots, codes.float(), scales, rope), lambda: write(c, k_rope, slots, codes, scales.double(), rope),
+            lambda: write(c, k_rope, slots, codes, scales, rope.float()), lambda: write(c, k_rope.float(), slots, *store),
+            lambda: write(c.half(), k_rope.half(), slots, *store), lambda: write(c, None, slots, *store),
+            lambda: write(c, k_rope, slots, codes, scales, None), lambda: write(c[:, :64], k_rope, slots, *store),
+            lambda: write(c, k_rope, slots[:5], *store), lambda: write(c, k_rope, slots.float(), *store),
+            lambda: write(c, k_rope, slots[::2], *store), lambda: write(c, k_rope[:9], slots, *store),
+            lambda: write(c, k_rope, slots, codes[:, ::2], scales[:, ::2], rope[:, ::2]),
+            lambda: write(c, k_rope, slots, codes[:3], scales, rope), lambda: write(c, k_rope, slots, codes.view(-1, 128), scales, rope),
+            lambda: write(c.t().contiguous().t(), k_rope, slots, *store), lambda: write(c, k_rope, slots.cpu(), *store),
+            lambda: read(*store, slots, dtype=torch.float16), lambda: read(*store, slots[None]), lambda: read(*store, slots.half()),
+            lambda: read(*store, slots, out=torch.empty(10, 128, dtype=BF16, device="cuda")),
+            lambda: read(codes[..., :120], scales, rope, slots),
+            lambda: fp8(*store, table, lens, q, q_rope), lambda: fp8(*store, table, lens, q.float(), q_rope, scale=1.0),
+            lambda: fp8(*store, table, lens, q[..., :64], q_rope, scale=1.0), lambda: fp8(*store, table, lens, q, None, scale=1.0),
+            lambda: fp8(*store, table.long(), lens, q, q_rope, scale=1.0), lambda: fp8(*store, table, lens[:0], q, q_rope, scale=1.0),
+            lambda: shared(store[:2], table, lens, cu, sh, q, q_rope, scale=1.0),
+            lambda: shared(rope, table, lens, cu, sh, q, q_rope, scale=1.0),
+            lambda: shared(store, table, lens, None, sh, q, q_rope, scale=1.0),
+            lambda: shared(store, table, lens, cu, None, q, q_rope, scale=1.0),
+            lambda: shared(store, table, lens, cu[:1], sh, q, q_rope, scale=1.0),
+            lambda: shared(store, table, lens, cu.long(), sh, q, q_rope, scale=1.0),
+            lambda: shared(store, table, lens, _i32([0, 9, 1])[::2], sh, q, q_rope, scale=1.0),
+            lambda: shared(store, table, lens, cu, sh, q, q_rope, scale=-1.0),
+            lambda: shared(store, table, lens, cu, sh, q, q_rope, scale=1.0, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+            lambda: shared(store, table, lens, cu, sh, q, q_rope, scale=1.0, out=torch.empty(1, 1, 8, 64, dtype=BF16, device="cuda"))]:
+        with pytest.raises((kda.KDAError, RuntimeError, ValueError)):
+            call()
+    write(c[:0], k_rope[:0], slots[:0], *store)                    # nothing to do
+    assert read(*store, slots[:0]).shape == (0, 136)
+    assert shared(store, table[:0], lens[:0], cu, sh, q[:0], q_rope[:0], scale=1.0)[0].shape == (0, 1, 8, 128)
