@@ -12,7 +12,9 @@
 // largest; and a scale per row leaves both products of decode as products of codes.
 //
 // Both kernels move each byte once and are bound by HBM.  A lane has 8
-// values; 16, 32 or 64 lanes have a row.
+// values; 16, 32 or 64 lanes have a row.  98304 rows of 512 + 64 values (171 MB) are
+// written in 29 us, 5.9 TB/s, and 120000 read in 34 us (215 MB, 6.4 TB/s), where
+// a copy of 1 GiB runs at 5.1; 64 rows take 4 us and are one launch's latency.
 #include "internal.h"
 #include "latent_common.h"
 
@@ -60,13 +62,30 @@ __device__ __forceinline__ Place place_of(const CacheParams& p, int64_t slot) {
   return {(int64_t)page, (int)((unsigned)slot - page * (unsigned)p.page_size)};
 }
 
+// ``kOnce``: for data that this call alone touches, so that it takes no other's place in
+// the caches.
+template <bool kOnce, typename V>
+__device__ __forceinline__ V load_vec(const char* at) {
+  const V* v = reinterpret_cast<const V*>(at);
+  return kOnce ? __builtin_nontemporal_load(v) : *v;
+}
+template <bool kOnce, typename V>
+__device__ __forceinline__ void store_vec(char* at, V x) {
+  V* v = reinterpret_cast<V*>(at);
+  if (kOnce)
+    __builtin_nontemporal_store(x, v);
+  else
+    *v = x;
+}
+
 // 8 values as they are stored
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__bf16> {
   u32x4 raw;
-  __device__ __forceinline__ void load(const char* at) { raw = *reinterpret_cast<const u32x4*>(at); }
+  template <bool kOnce>
+  __device__ __forceinline__ void load(const char* at) { raw = load_vec<kOnce, u32x4>(at); }
   __device__ __forceinline__ void clear() { raw = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int i) const {
     const unsigned w = raw[i >> 1];
@@ -77,9 +96,10 @@ struct Eight<__bf16> {
 template <>
 struct Eight<float> {
   f32x4 raw[2];
+  template <bool kOnce>
   __device__ __forceinline__ void load(const char* at) {
-    raw[0] = *reinterpret_cast<const f32x4*>(at);
-    raw[1] = *reinterpret_cast<const f32x4*>(at + 16);
+    raw[0] = load_vec<kOnce, f32x4>(at);
+    raw[1] = load_vec<kOnce, f32x4>(at + 16);
   }
   __device__ __forceinline__ void clear() { raw[0] = raw[1] = f32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int i) const { return raw[i >> 2][i & 3]; }
@@ -97,10 +117,10 @@ __device__ __forceinline__ int scale_exponent(unsigned top) {
   return e < -126 ? -126 : e;
 }
 
-// U rows a lane group, their loads issued together
-template <typename T, typename Index, int LANES, int U>
+// Many rows: two a lane group, their loads issued together, and read past the caches
+template <typename T, typename Index, int LANES, bool kMany>
 __global__ __launch_bounds__(kThreads) void quantize_scatter_kernel(CacheParams p) {
-  constexpr int kRows = 64 / LANES;  // of a wave at once
+  constexpr int U = kMany ? 2 : 1, kRows = 64 / LANES;  // rows of a lane group, and of a wave at once
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane % LANES;
   const int first = (blockIdx.x * kWaves + wave) * kRows * U + lane / LANES;
   const bool has_c = 8 * i < p.L, has_r = 8 * i < p.R;
@@ -111,8 +131,9 @@ __global__ __launch_bounds__(kThreads) void quantize_scatter_kernel(CacheParams 
     const int t = first + u * kRows;
     slot[u] = slot_of<Index>(p, t);
     x[u].clear();
-    if (t < p.n && has_c) x[u].load(p.c + t * p.c_stride + i * (8 * (int)sizeof(T)));
-    if (t < p.n && has_r) r[u].load(p.k_rope + t * p.k_rope_stride + i * (8 * (int)sizeof(T)));
+    if (t < p.n && has_c) x[u].template load<kMany>(p.c + t * p.c_stride + i * (8 * (int)sizeof(T)));
+    if (t < p.n && has_r)
+      r[u].template load<kMany>(p.k_rope + t * p.k_rope_stride + i * (8 * (int)sizeof(T)));
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -152,22 +173,23 @@ __global__ __launch_bounds__(kThreads) void quantize_scatter_kernel(CacheParams 
   }
 }
 
-template <typename T>
+template <typename T, bool kOnce>
 __device__ __forceinline__ void store8(char* at, const float (&v)[8]) {
   if (sizeof(T) == 4) {
-    reinterpret_cast<f32x4*>(at)[0] = f32x4{v[0], v[1], v[2], v[3]};
-    reinterpret_cast<f32x4*>(at)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    store_vec<kOnce>(at, f32x4{v[0], v[1], v[2], v[3]});
+    store_vec<kOnce>(at + 16, f32x4{v[4], v[5], v[6], v[7]});
   } else {
     bf16x8 b;
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = (__bf16)v[i];
-    *reinterpret_cast<bf16x8*>(at) = b;
+    store_vec<kOnce>(at, b);
   }
 }
 
-template <typename T, typename Index, int LANES, int U>
+// Many rows: two a lane group, written past the caches
+template <typename T, typename Index, int LANES, bool kMany>
 __global__ __launch_bounds__(kThreads) void dequantize_gather_kernel(CacheParams p) {
-  constexpr int kRows = 64 / LANES;
+  constexpr int U = kMany ? 2 : 1, kRows = 64 / LANES;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane % LANES;
   const int first = (blockIdx.x * kWaves + wave) * kRows * U + lane / LANES;
   const bool has_c = 8 * i < p.L, has_r = 8 * i < p.R;
@@ -185,7 +207,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_gather_kernel(CacheParams
     if (!in_cache(p, slot[u])) continue;
     const Place at = place_of(p, slot[u]);
     scale[u] = *reinterpret_cast<const float*>(p.scales + at.page * p.scales_page + (int64_t)at.off * 4);
-    if (has_c) codes[u] = *reinterpret_cast<const u32x2*>(p.codes + at.page * p.codes_page + (int64_t)at.off * p.L + 8 * i);
+    if (has_c)
+      codes[u] = *reinterpret_cast<const u32x2*>(p.codes + at.page * p.codes_page + (int64_t)at.off * p.L + 8 * i);
     if (has_r)
       r[u] = *reinterpret_cast<const u32x4*>(p.rope + at.page * p.rope_page + (int64_t)at.off * (2 * p.R) + 16 * i);
   }
@@ -205,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_gather_kernel(CacheParams
         v[4 * k + 2] = hi[0] * scale[u];
         v[4 * k + 3] = hi[1] * scale[u];
       }
-      store8<T>(row + i * (8 * (int)sizeof(T)), v);
+      store8<T, kMany>(row + i * (8 * (int)sizeof(T)), v);
     }
     if (has_r) {
       float v[8];
@@ -214,27 +237,32 @@ __global__ __launch_bounds__(kThreads) void dequantize_gather_kernel(CacheParams
         const unsigned w = r[u][k >> 1];
         v[k] = __builtin_bit_cast(float, k & 1 ? w & 0xffff0000u : w << 16);
       }
-      store8<T>(row + (p.L + 8 * i) * (int)sizeof(T), v);
+      store8<T, kMany>(row + (p.L + 8 * i) * (int)sizeof(T), v);
     }
   }
 }
 
-// Rows a lane group: 4 where that still leaves 2048 workgroups' waves busy.
+// Which calls have many rows.  Reading: those of more than 1024 workgroups (8192 rows of
+// 512 + 64 bf16 values 9.4 us either way, 32768 10.7 against 12.2 with a row a lane group and
+// plain stores, 120000 34 against 54).  Writing: inputs of more than 64 MiB, which the caches do
+// not hold from whatever wrote them (32768 rows, 38 MB, read again and again: 13.1 against
+// 12.2; 98304 rows, 113 MB: 29 against 34).  Four rows a lane group took 30 and 34 us, eight 33 and 35.
 template <bool kWrite, typename T, typename Index, int LANES>
 hipError_t launch_lanes(const CacheParams& p, hipStream_t stream) {
   constexpr int kRows = 64 / LANES * kWaves;
-  const bool many = p.n > 1024 * kRows;
-  const unsigned grid = (unsigned)(((int64_t)p.n + kRows * (many ? 4 : 1) - 1) / (kRows * (many ? 4 : 1)));
+  const bool many = kWrite ? (int64_t)p.n * (p.L + p.R) * (int)sizeof(T) > (64 << 20) : p.n > 1024 * kRows;
+  const int rows = kRows * (many ? 2 : 1);
+  const dim3 grid((unsigned)(((int64_t)p.n + rows - 1) / rows)), block(kThreads);
   if (kWrite) {
     if (many)
-      hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, 4>), dim3(grid), dim3(kThreads), 0, stream, p);
+      hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
     else
-      hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, 1>), dim3(grid), dim3(kThreads), 0, stream, p);
+      hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
   } else {
     if (many)
-      hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, 4>), dim3(grid), dim3(kThreads), 0, stream, p);
+      hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
     else
-      hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, 1>), dim3(grid), dim3(kThreads), 0, stream, p);
+      hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
   }
   return hipGetLastError();
 }
@@ -248,9 +276,8 @@ hipError_t launch_index(const CacheParams& p, hipStream_t stream) {
 
 template <bool kWrite>
 hipError_t launch(const CacheParams& p, bool bf16, bool index64, hipStream_t stream) {
-  if (bf16)
-    return index64 ? launch_index<kWrite, __bf16, int64_t>(p, stream) : launch_index<kWrite, __bf16, int32_t>(p, stream);
-  return index64 ? launch_index<kWrite, float, int64_t>(p, stream) : launch_index<kWrite, float, int32_t>(p, stream);
+  if (index64) return bf16 ? launch_index<kWrite, __bf16, int64_t>(p, stream) : launch_index<kWrite, float, int64_t>(p, stream);
+  return bf16 ? launch_index<kWrite, __bf16, int32_t>(p, stream) : launch_index<kWrite, float, int32_t>(p, stream);
 }
 
 CacheParams params(const kda_latent_store_t& s, const void* slots, int64_t n) {

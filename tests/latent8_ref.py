@@ -4,7 +4,6 @@ import math
 import torch
 
 
-
 def _value(code):
     sign, e, m = code >> 7, code >> 3 & 15, code & 7
     if e == 15 and m == 7:

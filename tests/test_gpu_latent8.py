@@ -82,6 +82,29 @@ def test_written_rows(T, L, R, page, dtype, index, gap):
             assert torch.equal(x.cpu()[:, n:], y[:, n:])
 
 
+@pytest.mark.parametrize("T,L,R,page,dtype", [(60001, 512, 64, 64, BF16), (87501, 128, 64, 16, torch.float32),
+                                              (64007, 256, 8, 64, torch.float32)])
+def test_written_rows_of_a_large_batch(T, L, R, page, dtype):
+    """Inputs of more than 64 MiB: 1999 rows many times over."""
+    import kda_recurrent_state_amd as kda
+    pages = T // page + 3
+    codes, scales, rope = _empty_store(pages, page, L, R)
+    c, k_rope = _rows(1999, L, R, dtype, T)
+    row = (torch.arange(T) * 17 + 3) % 1999
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(2))[:T]
+    bad = torch.arange(T) % 11 == 5
+    slots[bad] = -1
+    want, scale = ref8.quantize(c.cpu().double())
+    kda.kda_latent_quantize_scatter(c[row.cuda()], k_rope[row.cuda()], slots.cuda(), codes, scales, rope)
+    at, row = slots[~bad], row[~bad]
+    hit = torch.zeros(pages * page, dtype=torch.bool)
+    hit[at] = True
+    got = codes.cpu().view(-1, L), scales.cpu().view(-1), rope.cpu().view(-1, R)
+    assert torch.equal(got[0][at], want[row]) and torch.equal(got[1][at].double(), scale[row])
+    assert torch.equal(got[2][at], k_rope.to(BF16).cpu()[row])
+    assert (got[0][~hit] == 0x55).all() and (got[1][~hit] == -7).all() and (got[2][~hit] == 3).all()
+
+
 def test_rows_that_are_not_finite():
     import kda_recurrent_state_amd as kda
     codes, scales, rope = _empty_store(2, 4, 128, 8)
