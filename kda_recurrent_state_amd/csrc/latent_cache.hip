@@ -276,7 +276,9 @@ hipError_t launch_index(const CacheParams& p, hipStream_t stream) {
 
 template <bool kWrite>
 hipError_t launch(const CacheParams& p, bool bf16, bool index64, hipStream_t stream) {
-  if (index64) return bf16 ? launch_index<kWrite, __bf16, int64_t>(p, stream) : launch_index<kWrite, float, int64_t>(p, stream);
+  if (index64) {
+    return bf16 ? launch_index<kWrite, __bf16, int64_t>(p, stream) : launch_index<kWrite, float, int64_t>(p, stream);
+  }
   return bf16 ? launch_index<kWrite, __bf16, int32_t>(p, stream) : launch_index<kWrite, float, int32_t>(p, stream);
 }
 

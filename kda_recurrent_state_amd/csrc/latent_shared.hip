@@ -24,6 +24,15 @@
 // Tile.  As in latent decode: 8 waves, 64 tokens, the scores of a row block and a
 // group of tokens by a wave, the output's columns over the waves.  In 8 bits a
 // tile is 40 KB and three stages fit.
+//
+// What bounds it: the phases of a tile, which follow one another within the CU's
+// one workgroup.  64 sequences of 12000 to 20000 tokens with 128 heads, 512 + 64
+// components, take 394 us in 8 bits (660 MB, 131 us at a copy's rate; products 250 us at a large
+// matrix product's); a tile of 64 rows takes 3.1 us, and without its fetches, scores, softmax
+// or output product the call is 75, 90, 40 or 72 us shorter.  40 sequences of 256 query rows behind
+// 16384 shared tokens: 450 us in 16 bits, 495 in 8 (products 334), where decode that
+// reads the prefix for each sequence would compute the same and read 40 times as much.
+// The plan takes 6 to 9 us, the join 7 to 18.
 #include <type_traits>
 
 #include "internal.h"
@@ -36,7 +45,10 @@ using namespace latent;
 
 constexpr int kShares = 256;       // workgroups, one a CU
 constexpr int kPlanThreads = 512;
-constexpr int kEnd = 4;            // room before a unit of an entity of one chunk
+// Room before a unit of an entity of one chunk, in tiles: 40 sequences of 64 to 1024 tokens behind
+// a prefix, 256 query rows each, take 498 us with 4, 611 with 2 (the shares with many
+// units come last) and 511 with 8 (those with few).
+constexpr int kEnd = 4;
 
 struct Entity {
   int64_t base, first;     // place on the line, and the number of its first tile
@@ -361,7 +373,8 @@ struct Kind<true, LP, RP, NB, kPad> {
 };
 
 template <bool F8, int LP, int RP, int NB, bool kPad>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_shared_kernel(SharedParams p) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_shared_kernel(
+    SharedParams p) {
   using K = Kind<F8, LP, RP, NB, kPad>;
   using D = typename K::D;
   constexpr int MB = D::MB, KS = D::KS, MT = D::MT, TG = D::TG, TB = D::TB, NS = K::kStages;
@@ -569,7 +582,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const unsigned row = u.row0 + (r < u.rows ? r : 0);
     const SharedParams& p = cold;
     const unsigned n = row / (unsigned)p.rows, in = row - n * p.rows, qi = in / (unsigned)p.H, h = in - qi * p.H;
-    const __bf16 *q = p.q + n * p.qs[0] + qi * p.qs[1] + h * p.qs[2], *qr = p.qr + n * p.qrs[0] + qi * p.qrs[1] + h * p.qrs[2];
+    const __bf16* q = p.q + n * p.qs[0] + qi * p.qs[1] + h * p.qs[2];
+    const __bf16* qr = p.qr + n * p.qrs[0] + qi * p.qrs[1] + h * p.qrs[2];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       int c = 32 * i + 8 * lg;
@@ -796,8 +810,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
           if (spread) fetch(rows, F8 ? i : i + kFirst, to);
         };
         if constexpr (F8)
-          D::scores(lat + 16 * TB * tg * LP, rot + 16 * TB * tg * RP * 2, tscale[0] + st * kTile + 16 * TB * tg, qf, ln, lg,
-                    s, sc, load);
+          D::scores(lat + 16 * TB * tg * LP, rot + 16 * TB * tg * RP * 2, tscale[0] + st * kTile + 16 * TB * tg, qf,
+                    ln, lg, s, sc, load);
         else
           D::scores(reinterpret_cast<const __bf16*>(lat) + (16 * TB * tg + ln) * LP,
                     reinterpret_cast<const __bf16*>(rot) + (16 * TB * tg + ln) * RP, qf, ln, lg, s, load);
@@ -947,7 +961,9 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
   if (p.lse && lane == 0) p.lse[grow] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
-// Blocks of 16 query rows a workgroup takes at once.
+// Blocks of 16 query rows a workgroup takes at once: as few as hold a sequence's or the
+// batch's rows (64 x 4000 tokens in 8 bits, 16 heads: 63 us with one block, 68 with two,
+// 80 with four; 32 heads: 77 with two, 86 with four).
 int blocks_of(int64_t N, int64_t Q, int64_t H, int64_t G) {
   const int64_t rows = G > 0 ? N * Q * H : Q * H;
   return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
@@ -982,8 +998,9 @@ hipError_t launch_nb(const SharedParams& p, int nb, hipStream_t stream) {
 
 template <bool F8, int LP>
 hipError_t launch_r(const SharedParams& p, int nb, hipStream_t stream) {
-  if (p.R == 0) return p.L == LP ? launch_nb<F8, LP, 0, false>(p, nb, stream) : launch_nb<F8, LP, 0, true>(p, nb, stream);
-  return p.L == LP && p.R == 64 ? launch_nb<F8, LP, 64, false>(p, nb, stream) : launch_nb<F8, LP, 64, true>(p, nb, stream);
+  const bool whole = p.L == LP && (p.R == 0 || p.R == 64);  // no padding columns
+  if (p.R == 0) return whole ? launch_nb<F8, LP, 0, false>(p, nb, stream) : launch_nb<F8, LP, 0, true>(p, nb, stream);
+  return whole ? launch_nb<F8, LP, 64, false>(p, nb, stream) : launch_nb<F8, LP, 64, true>(p, nb, stream);
 }
 
 template <bool F8>
@@ -996,8 +1013,8 @@ hipError_t launch_l(const SharedParams& p, int nb, hipStream_t stream) {
 
 size_t latent_shared_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L, int64_t G) {
   const size_t rows = (size_t)slots_of(N, Q, H, G) * 16 * blocks_of(N, Q, H, G);
-  return round16(rows * (size_t)L * 4) + round16(rows * 8) + (size_t)(G + N) * sizeof(Entity) + kShares * sizeof(Start) +
-         16 + (size_t)(2 * G + 1) * 4;
+  return round16(rows * (size_t)L * 4) + round16(rows * 8) + (size_t)(G + N) * sizeof(Entity) +
+         kShares * sizeof(Start) + 16 + (size_t)(2 * G + 1) * 4;
 }
 
 hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t stream) {
@@ -1056,7 +1073,8 @@ hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t s
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = f8 ? launch_l<true>(p, nb, stream) : launch_l<false>(p, nb, stream);
   if (e != hipSuccess) return e;
-  // few rows: more waves share a row's pieces
+  // Few rows: more waves share a row's pieces (1 x 4000 tokens, 32 heads: 28 us with 8 waves a
+  // row, 45 with one; 200 sequences of 64 rows: 113 with one, 154 with 8).
   int parts = kWaves;
   while (parts > 1 && (int64_t)p.rows * p.N * parts > 2048 * kWaves) parts >>= 1;
   const int per = kWaves / parts;

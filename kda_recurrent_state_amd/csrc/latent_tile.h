@@ -253,7 +253,7 @@ struct Fp8Tile {
     return c;
   }
   static __device__ __forceinline__ int chunk(int i, const Columns& c) {
-    return c.lat ^ ((swizzle(i * RI) ^ swizzle(0)) * 16);  // (i RI adds to no bit of the wave's first row and the lane's)
+    return c.lat ^ ((swizzle(i * RI) ^ swizzle(0)) * 16);  // (i RI and those rows have no bit in common)
   }
   // Load i of a wave's for a tile (of kLoads: scales, rotary rows, latent rows).
   // Its 8 rows lie one behind the other at lat, rot and scale (uniform).
@@ -263,12 +263,14 @@ struct Fp8Tile {
     if (i == 0) {
       if (lane / 8 == wave) load_lds4(uniform(scale), (unsigned)(lane % 8 * 4), uniform(scale_lds));
     } else if (RP > 0 && i == 1) {
-      if (!kPad || c.has_rot) load_lds16(uniform(rot), lane / 8 * (2 * R) + c.rot, uniform(rot_lds + wave * 8 * RP * 2));
+      if (!kPad || c.has_rot)
+        load_lds16(uniform(rot), lane / 8 * (2 * R) + c.rot, uniform(rot_lds + wave * 8 * RP * 2));
     } else {
       i -= kLoads - kLat;
       const int at = chunk(i, c);
       if (!kPad || at < c.L)
-        load_lds16(uniform(lat + i * RI * L), (unsigned)(lane / LC * L + at), uniform(lat_lds + (wave * kRows + i * RI) * LP));
+        load_lds16(uniform(lat + i * RI * L), (unsigned)(lane / LC * L + at),
+                   uniform(lat_lds + (wave * kRows + i * RI) * LP));
     }
   }
   // The same for rows anywhere: token j's at lane j's lat, rot and scale.
@@ -316,7 +318,8 @@ struct Fp8Tile {
     const int y0 = (lg ^ ((ln >> 1) & 7)) * 16;
     auto rotary = [&](int k) {
 #pragma unroll
-      for (int j = 0; j < TB; ++j) y[j] = *reinterpret_cast<const bf16x8*>(rot + (16 * j + ln) * RP * 2 + (y0 ^ (k * 64)));
+      for (int j = 0; j < TB; ++j)
+        y[j] = *reinterpret_cast<const bf16x8*>(rot + (16 * j + ln) * RP * 2 + (y0 ^ (k * 64)));
     };
 #pragma unroll
     for (int j = 0; j < TB; ++j) ro[j] = f32x4{0, 0, 0, 0};
@@ -381,7 +384,8 @@ struct Fp8Tile {
       hold_order();
       const bf16x8 v = widen((unsigned)vf[b % 3][0], (unsigned)vf[b % 3][1]);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[b % MT][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pf[j], acc[b % MT][j], 0, 0, 0);
+      for (int j = 0; j < NB; ++j)
+        acc[b % MT][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pf[j], acc[b % MT][j], 0, 0, 0);
       hold_order();
     }
   }

@@ -11,8 +11,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import (KDA_BF16, KDA_E4M3, KDA_F32, KDA_I32, KDA_I64, KDAError, LatentDecodeArgs, LatentPrefillArgs, LatentSharedArgs,
-                   LatentStore, PagePool, PageStore)
+from ._lib import (KDA_BF16, KDA_E4M3, KDA_F32, KDA_I32, KDA_I64, KDAError, LatentDecodeArgs, LatentPrefillArgs,
+                   LatentSharedArgs, LatentStore, PagePool, PageStore)
 from .api import _device as _checked_device, _index_code, _on_stream, _stream_handle
 
 
@@ -384,7 +384,8 @@ def _decode_shared(what: str, cache, page_table, lengths, cu_groups, shared, q, 
         lse = _out(what, "lse", lse, shape[:-1], torch.float32, dev, made)
     ws = _workspace(workspace, lib.kda_latent_shared_workspace_size(N, Q, H, L, G), dev, made)
     a = LatentSharedArgs(N, Q, H, L, R, G, *head, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                         lengths.data_ptr(), *groups, q4.data_ptr(), q4.stride()[:3], *rope_q, out.data_ptr(), None if lse is None else lse.data_ptr(), scale, *ws)
+                         lengths.data_ptr(), *groups, q4.data_ptr(), q4.stride()[:3], *rope_q, out.data_ptr(),
+                         None if lse is None else lse.data_ptr(), scale, *ws)
     _call(what, dev, stream, made, getattr(lib, what), a)
     return out, lse
 
