@@ -52,7 +52,7 @@ constexpr int kEnd = 4;
 
 struct Entity {
   int64_t base, first;     // place on the line, and the number of its first tile
-  int32_t tiles, row_blocks;
+  int32_t tiles, row_blocks;  // row_blocks: a team's, of ``team`` blocks of MB rows each
   int32_t chunks, chunk;   // and the tiles of one; the first ``longer`` ones have one more
   int32_t longer;
   int32_t row0, rows;      // query rows
@@ -70,8 +70,8 @@ struct Entity {
   __device__ __forceinline__ int chunk_tiles(int k) const { return chunk + (k < longer ? 1 : 0); }
 };
 
-struct Start {  // where a workgroup begins: tile t of row block rb of chunk k of entity e
-  int32_t left, w, e, k, rb, t;  // left: tiles of the share, 0: none
+struct Start {  // where a workgroup begins: tile t of a team's row block rb of chunk k of entity e
+  int32_t left, w, e, k, rb, t;  // left: tiles of the share, 0: none; w: share * team + member
   Entity ent;
 };
 
@@ -95,6 +95,7 @@ struct SharedParams {
   __bf16* out;
   float* lse;
   int N, Q, H, rows, G;                          // rows: Q H
+  int team;                                      // workgroups of a share
   float scale2;                                  // scale log2 e
   float* part;                                   // [slots][MB][L] normalised outputs
   float2* psum;                                  // [slots][MB] the maxima and the sums against them
@@ -126,10 +127,11 @@ struct Shares {
   int rem, count;
   bool narrow;  // whether the line has fewer than 2^31 places
 };
-__device__ __forceinline__ Shares shares_of(int64_t total) {
-  const bool few = total < kShares;
-  return {few ? 1 : (int64_t)((uint64_t)total / kShares), few ? 0 : (int)((uint64_t)total % kShares),
-          few ? (int)total : kShares, total >> 31 == 0};
+__device__ __forceinline__ Shares shares_of(const SharedParams& p, int64_t total) {
+  const unsigned most = kShares / (unsigned)p.team;
+  const bool few = total < most;
+  return {few ? 1 : (int64_t)((uint64_t)total / most), few ? 0 : (int)((uint64_t)total % most),
+          few ? (int)total : (int)most, total >> 31 == 0};
 }
 __device__ __forceinline__ int64_t share_begin(const Shares& s, int w) { return w * s.quot + min(w, s.rem); }
 // the share that holds place x
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
   __shared__ int tops[kPlanThreads / 64];
   __shared__ Entity lents[kPlanThreads];
   __shared__ int lbounds[kPlanThreads + 1], lprefix[kPlanThreads];
-  const int own_blocks = (p.rows + MB - 1) / MB;
+  const int own_blocks = (p.rows + MB - 1) / MB, team_rows = MB * p.team;
   const int tid = threadIdx.x, E = p.G + p.N;
   const bool few = E <= kPlanThreads;
   int *bounds = few ? lbounds : p.bounds, *prefix = few ? lprefix : p.prefix;
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
       }
     }
     x.tiles = (int)((unsigned)(x.t1 - x.t0 + kTile - 1) / kTile);
-    x.row_blocks = (x.rows + MB - 1) / MB;
+    x.row_blocks = (unsigned)(x.rows + team_rows - 1) / (unsigned)team_rows;
     return x;
   };
   // the line's length with room for every entity, and from that the chunks; then the line
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     block_scan(n, zero, sums, &all, &zero);
     total += all;
   }
-  const long long quot = shares_of(total).quot;
+  const long long quot = shares_of(p, total).quot;
   const unsigned share = quot > (1 << 30) ? 1u << 30 : (unsigned)quot;
   long long base = 0, first = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     if (e < E) {
       if (!few) mine = entity(e);
       if (mine.tiles > 0) {
-        mine.chunks = (int)max(1u, (unsigned)mine.tiles / share);
+        mine.chunks = mine.row_blocks == 1 ? 1 : (int)max(1u, (unsigned)mine.tiles / share);
         mine.chunk = (int)((unsigned)mine.tiles / (unsigned)mine.chunks);
         mine.longer = mine.tiles - mine.chunk * mine.chunks;
         n = mine.line();
@@ -300,10 +302,11 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
   if (tid == 0) *p.total = base;
   if (tid < kShares) p.starts[tid].left = 0;
   __syncthreads();
-  const Shares sh = shares_of(base);
+  const Shares sh = shares_of(p, base);
   Start s;
-  if (tid < sh.count) {
-    const int64_t from = share_begin(sh, tid);
+  const int w = (unsigned)tid / (unsigned)p.team;  // thread: a member of this share's team
+  if (w < sh.count) {
+    const int64_t from = share_begin(sh, w);
     int lo = 0, hi = E;  // the last entity that begins there or before: it holds the place, if empty ones at its
     while (hi - lo > 1) {  // place are before it
       const int mid = (lo + hi) >> 1;
@@ -325,14 +328,14 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     s.t = rest > 0 ? (int)rest : 0;
     s.e = lo;
     s.w = tid;
-    number[tid] = x.first + (int64_t)x.chunk_begin(s.k) * x.row_blocks + (int64_t)s.rb * x.chunk_tiles(s.k) + s.t;
+    number[w] = x.first + (int64_t)x.chunk_begin(s.k) * x.row_blocks + (int64_t)s.rb * x.chunk_tiles(s.k) + s.t;
   }
-  if (tid == sh.count) number[tid] = first;
+  if (tid == 0) number[sh.count] = first;
   __syncthreads();
-  if (tid < sh.count) {
-    s.left = (int)(number[tid + 1] - number[tid]);
+  if (w < sh.count) {
+    s.left = (int)(number[w + 1] - number[w]);
     // neighbours to workgroups of one XCD, which are those of one number mod 8
-    const unsigned per = (unsigned)(sh.count + 7) / 8;
+    const unsigned per = (unsigned)(sh.count * p.team + 7) / 8;
     p.starts[(unsigned)tid % per * 8 + (unsigned)tid / per] = s;
   }
 }
@@ -423,6 +426,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   int e = start.e, k = start.k, rb = start.rb;  // the unit of ``asked``
   const char* row_pages;                        // and its sequence's row of the table
   int asked_unit = 0;
+  auto rows_of = [&](const Entity& x) {  // (a member without a row block computes the first row's and writes none)
+    const unsigned team = cold.team, b = rb * team + (unsigned)w % team;
+    const int n = min(MB, x.rows - (int)b * MB);
+    return n > 0 ? Unit{x.row0 + (int)b * MB, n, x.slot + (int)b, 0} : Unit{x.row0, 0, 0, 0};
+  };
   auto enter = [&](const Entity& x, int t) {
     asked.rem = x.chunk_tiles(k) - t;
     asked.pos = x.t0 + (x.chunk_begin(k) + t) * kTile;
@@ -431,7 +439,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     row_pages = uniform(reinterpret_cast<const char*>(cold.table + x.seq * cold.table_stride));
     if (tid == 0) {
       const int flags = x.chunks != 1 ? 0 : (e >= cold.G && x.t0 == 0 ? kSingle | kAlone : kSingle);
-      units[asked_unit % kUnits] = make_int4(x.row0 + rb * MB, min(MB, x.rows - rb * MB), x.slot + rb, flags);
+      const Unit u = rows_of(x);
+      units[asked_unit % kUnits] = make_int4(u.row0, u.rows, u.slot, flags);
     }
   };
   auto follow = [&]() {  // (there is a next batch)
@@ -602,7 +611,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   {
     enter(start.ent, start.t);
     ask();
-    load_q(Unit{start.ent.row0 + rb * MB, min(MB, start.ent.rows - rb * MB), 0, 0});
+    load_q(rows_of(start.ent));
     wait_loads<0>();
     Rows rows = {nullptr, nullptr, nullptr};
     if (locate(ring[0], rows, 0)) fetch_all(rows, 0);
@@ -859,11 +868,11 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
     if (p.lse && lane == 0) p.lse[grow] = -INFINITY;
     return;
   }
-  const Shares sh = shares_of(scalar_load(p.total));
+  const Shares sh = shares_of(p, scalar_load(p.total));
   // a sequence that one piece holds whole has its output
   if (own.t0 == 0 && own.chunks == 1) {
     const int rb = (blockIdx.x * (kWaves / parts)) / MB;  // (that of all the workgroup's rows)
-    const int64_t a = own.base + own.unit_begin(0, rb) + own.room();
+    const int64_t a = own.base + own.unit_begin(0, rb / p.team) + own.room();
     if (share_at(sh, a) == share_at(sh, a + own.tiles - 1)) return;
   }
   float top = -INFINITY, sum = 0.f;
@@ -872,16 +881,18 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
     if (which == 0 && own.group < 0) continue;
     const Entity x = which == 1 ? own : scalar_load(p.ents + own.group);
     const int in = (int)(grow - x.row0), rb = in / MB, r = in - rb * MB;
+    const int block = (unsigned)rb / (unsigned)p.team, member = rb - block * p.team;
     for (int k0 = 0; k0 < x.chunks; k0 += 64) {
       // lane i: the pieces of the row block's unit in chunk k0 + i, their number and where the first one is: the
       // whole unit's own place, or 2 w (+ 1 where others are before it in share w)
       const int k = k0 + lane;
       int first = 0, place = 0, count = 0;
       if (k < x.chunks) {
-        const int64_t unit = x.base + x.unit_begin(k, rb), a = unit + x.room();
+        const int64_t unit = x.base + x.unit_begin(k, block), a = unit + x.room();
         first = share_at(sh, a);
         count = share_at(sh, a + x.chunk_tiles(k) - 1) - first + 1;
-        place = count == 1 && x.chunks == 1 ? x.slot + rb : 2 * first + (share_begin(sh, first) < unit ? 1 : 0);
+        place = count == 1 && x.chunks == 1 ? x.slot + rb
+                                            : 2 * (first * p.team + member) + (share_begin(sh, first) < unit ? 1 : 0);
       }
       const int upto = wave_scan(count, lane), pieces = __builtin_amdgcn_readlane(upto, 63);
       for (int q0 = part; q0 < pieces; q0 += 4 * parts) {
@@ -898,7 +909,7 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
           const int i = __ffsll(__ballot(upto > q)) - 1;
           const int in_unit = q - (__builtin_amdgcn_readlane(upto, i) - __builtin_amdgcn_readlane(count, i));
           const int64_t slot = in_unit == 0 ? __builtin_amdgcn_readlane(place, i)
-                                            : 2 * (__builtin_amdgcn_readlane(first, i) + in_unit);
+                                            : 2 * ((__builtin_amdgcn_readlane(first, i) + in_unit) * p.team + member);
           const float2 ml = p.psum[slot * MB + r];
           e[u] = ml.x;
           s[u] = ml.y;
@@ -1055,6 +1066,7 @@ hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t s
   p.H = (int)a.H;
   p.rows = (int)(a.Q * a.H);
   p.G = (int)a.G;
+  p.team = (int)((a.Q * a.H + MB - 1) / MB);
   p.scale2 = a.scale * kLog2e;
   const size_t rows = (size_t)slots_of(a.N, a.Q, a.H, a.G) * MB;
   char* ws = static_cast<char*>(a.workspace);
