@@ -43,6 +43,8 @@ namespace {
 
 using namespace latent;
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kShares = 256;       // workgroups, one a CU
 constexpr int kPlanThreads = 512;
 // Room before a unit of an entity of one chunk, in tiles: 40 sequences of 64 to 1024 tokens behind
@@ -105,11 +107,11 @@ struct SharedParams {
   int32_t *bounds, *prefix;                      // [G + 1] the groups' sequences, [G] their shared tokens
 };
 
-__device__ __forceinline__ int seq_tokens(const SharedParams& p, int n) {
-  const int len = p.lengths[n];
+__device__ __forceinline__ int tokens_of(const SharedParams& p, int len) {
   const int64_t room = (int64_t)p.max_pages * p.page_size;
   return len < 0 ? 0 : (len > room ? (int)room : len);
 }
+__device__ __forceinline__ int seq_tokens(const SharedParams& p, int n) { return tokens_of(p, p.lengths[n]); }
 
 // a / b of 0 <= a < 2^52, 0 < b, or with ``narrow`` (the same in all lanes) < 2^31.  (The quotient
 // in fp64 is off by less than one; a division of 64-bit integers is four times the
@@ -363,6 +365,13 @@ __device__ __forceinline__ T scalar_load(const T* at) {
   return r;
 }
 
+// Global memory behind a pointer that came out of LDS.  (Without it the compiler takes flat
+// instructions, and every barrier for LDS waits for those.)
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(1))) T* global(const void* at) {
+  return (__attribute__((address_space(1))) T*)(uintptr_t)at;
+}
+
 // A cache's kind: its tile, and the stages that fit into the LDS.
 template <bool F8, int LP, int RP, int NB, bool kPad>
 struct Kind {
@@ -584,13 +593,15 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
   // ---- queries
   bf16x8 qf[KS];
-  int sees = 0;  // tokens that row ln of the wave's block sees
+  int sees = 0;     // tokens that row ln of the wave's block sees
+  int len = 0, behind = 0;  // its sequence's length, and the new tokens behind it
   auto load_q = [&](const Unit& u) {
     // (rows behind the unit's last one get its first one's queries; they are not written)
     const int r = keep_here(rblock * 16 + ln), lg = keep_here(lane >> 4);
     const unsigned row = u.row0 + (r < u.rows ? r : 0);
     const SharedParams& p = cold;
     const unsigned n = row / (unsigned)p.rows, in = row - n * p.rows, qi = in / (unsigned)p.H, h = in - qi * p.H;
+    len = *global<const int>(p.lengths + n);
     const __bf16* q = p.q + n * p.qs[0] + qi * p.qs[1] + h * p.qs[2];
     const __bf16* qr = p.qr + n * p.qrs[0] + qi * p.qrs[1] + h * p.qrs[2];
 #pragma unroll
@@ -601,10 +612,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       else if (i >= LP / 32)
         c -= LP;
       bf16x8 y = {};
-      if (!kPad || c < (i < LP / 32 ? p.L : p.R)) y = *reinterpret_cast<const bf16x8*>((i < LP / 32 ? q : qr) + c);
+      if (!kPad || c < (i < LP / 32 ? p.L : p.R)) y = *global<const bf16x8>((i < LP / 32 ? q : qr) + c);
       qf[i] = y;
     }
-    sees = seq_tokens(p, (int)n) - (p.Q - 1 - (int)qi);
+    behind = p.Q - 1 - (int)qi;
+  };
+  // They have landed, as has all that was asked for before.  (In every path of a piece's end: the
+  // compiler would wait for them in every tile.)
+  auto take_q = [&]() {
+    wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(qf[i]));
+    sees = tokens_of(cold, len) - behind;
   };
   int left = start.left - 1;  // tiles behind the one scored
   Tile ring[kAhead + 1];      // the one scored, and those fetched ahead
@@ -612,7 +631,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     enter(start.ent, start.t);
     ask();
     load_q(rows_of(start.ent));
-    wait_loads<0>();
+    take_q();
     Rows rows = {nullptr, nullptr, nullptr};
     if (locate(ring[0], rows, 0)) fetch_all(rows, 0);
     if (kAhead == 2 && left > 0) {
@@ -747,6 +766,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
       for (int g = 1; g < TG; ++g) sum += smax[g][j * 16 + ln];
       inv[j] = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     }
+    take_q();  // (before the stores, which nothing then waits for)
     if (direct) {
       __bf16* out = p.out + ((int64_t)u.row0 + ln) * p.L + col0;
 #pragma unroll
@@ -756,7 +776,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
           for (int i = 0; i < MT; ++i) {
             const f32x4 o = acc[i][j] * inv[j];
             const bf16x4 ob = {(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-            if (!kPad || col0 + 16 * i < p.L) *reinterpret_cast<bf16x4*>(out + 16 * i) = ob;
+            if (!kPad || col0 + 16 * i < p.L) *global<bf16x4>(out + 16 * i) = ob;
           }
         }
         out += 16 * p.L;
@@ -768,7 +788,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (j * 16 + ln < u.rows) {
 #pragma unroll
           for (int i = 0; i < MT; ++i)
-            if (!kPad || col0 + 16 * i < p.L) *reinterpret_cast<f32x4*>(part + 16 * i) = acc[i][j] * inv[j];
+            if (!kPad || col0 + 16 * i < p.L) *global<f32x4>(part + 16 * i) = acc[i][j] * inv[j];
         }
         part += 16 * p.L;
       }
@@ -779,19 +799,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
       for (int g = 1; g < TG; ++g) sum += smax[g][r];
       if (!direct)
-        p.psum[slot * MB + r] = make_float2(sfac[r], sum);
+        *global<f32x2>(p.psum + slot * MB + r) = f32x2{sfac[r], sum};
       else if (p.lse)
-        p.lse[(int64_t)u.row0 + r] = sum == 0.f ? -INFINITY : (sfac[r] + __log2f(sum)) * kLn2;
+        *global<float>(p.lse + (int64_t)u.row0 + r) = sum == 0.f ? -INFINITY : (sfac[r] + __log2f(sum)) * kLn2;
     }
     ++unit;
     begun = true;
     later = 1;
   };
-  int st = 0;  // the stage of the tile computed
+  int st = 0;           // the stage of the tile computed
+  bool landed = false;  // whether it and the next one are known to be there
   for (int par = 0;; par ^= 1) {
     // this tile has landed (the next one's loads may be under way, and the lookup
     // before them is done), and the readers of the one before are done
-    if constexpr (kAhead == 2) {
+    if (landed) {
+      landed = false;  // (at the end of a piece)
+    } else if constexpr (kAhead == 2) {
       if (left > 0 && ring[1].live)
         wait_loads<D::kLoads>();
       else
@@ -838,11 +861,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     if (!more || cur.last) {
       if (more) load_q(unit_of(unit + 1));
       finish(cur.last);
-      if (!more) {
-        wait_loads<0>();  // no load to LDS outlives the workgroup
-        return;
-      }
+      if (!more) return;  // (no load to LDS outlives the workgroup)
       clear();
+      landed = true;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) ring[i] = ring[i + 1];
