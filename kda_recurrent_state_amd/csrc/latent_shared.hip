@@ -9,14 +9,17 @@
 // sequence's own go over its own rows.
 //
 // Work split.  The batch is a line of tiles of 64 tokens.  An entity is a group's prefix
-// or a sequence's own tokens: T tiles for each of its row blocks.  It is cut into
-// chunks of at least a workgroup's share, a chunk's tiles stand on the line for
-// one row block after another, and workgroups get equal shares of the line, neighbours on one
-// XCD: the row blocks of a chunk are computed at the same time behind one
-// L2, which then serves all but the first.  A unit (a row block of a chunk) ends with
+// or a sequence's own tokens: T tiles for each of its row blocks.  As many workgroups as a
+// sequence has row blocks are a team, which goes over the line together, a row block each, so
+// that a tile comes out of HBM once for all of them (64 x 16000 tokens, 128 rows: 650 MB are
+// read, without teams 1230); a prefix has row blocks for many teams.  Teams get equal shares of the
+// line, neighbours on one XCD.  An entity with row blocks for several teams is
+// cut into chunks of at least a share, and a chunk's tiles stand on the line for
+// one team's row blocks after another: these are then computed at about the same time, and the
+// L2 serves some of the tiles.  A unit (a team's row blocks of a chunk) ends with
 // queries to load and outputs to write, kEnd tiles' time; entities of one chunk, of which a
-// share can hold many, have that much room on the line before each row block.  What one workgroup computes of one
-// unit, a piece, is written as output if it is all there is for
+// share can hold many, have that much room on the line before each unit.  What one
+// workgroup computes of one unit, a piece, is written as output if it is all there is for
 // its sequence, otherwise with its maximum and sum to the workspace, and
 // the join kernel weighs the pieces of a row.  The plan is made on the device by one
 // workgroup, so a captured call follows its lengths, groups and tables.
@@ -27,12 +30,12 @@
 //
 // What bounds it: the phases of a tile, which follow one another within the CU's
 // one workgroup.  64 sequences of 12000 to 20000 tokens with 128 heads, 512 + 64
-// components, take 394 us in 8 bits (660 MB, 131 us at a copy's rate; products 250 us at a large
-// matrix product's); a tile of 64 rows takes 3.1 us, and without its fetches, scores, softmax
-// or output product the call is 75, 90, 40 or 72 us shorter.  40 sequences of 256 query rows behind
-// 16384 shared tokens: 450 us in 16 bits, 495 in 8 (products 334), where decode that
-// reads the prefix for each sequence would compute the same and read 40 times as much.
-// The plan takes 6 to 9 us, the join 7 to 18.
+// components, take 385 us in 8 bits (660 MB, 131 us at a copy's rate; products 250 us at a large
+// matrix product's); a tile of 64 rows takes 2.8 us, the matrix unit is busy for a third of
+// it, and without its fetches, scores, softmax or output product the call is 75, 90, 40 or
+// 72 us shorter.  40 sequences of 256 query rows behind 16384 shared tokens: 430 us in 16
+// bits, 505 in 8 (products 334), where decode that reads the prefix for each sequence
+// computes the same and reads 40 times as much.  The plan takes 5 to 9 us, the join 6 to 18.
 #include <type_traits>
 
 #include "internal.h"
@@ -48,8 +51,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kShares = 256;       // workgroups, one a CU
 constexpr int kPlanThreads = 512;
 // Room before a unit of an entity of one chunk, in tiles: 40 sequences of 64 to 1024 tokens behind
-// a prefix, 256 query rows each, take 498 us with 4, 611 with 2 (the shares with many
-// units come last) and 511 with 8 (those with few).
+// a prefix, 256 query rows each, take 436 us with 4, 476 with 3 and 525 with 2 (the shares with many
+// units come last) and 433 with 6, where 200 ragged ones take 109, 110, 116 and 112.
 constexpr int kEnd = 4;
 
 struct Entity {
@@ -1001,7 +1004,7 @@ int blocks_of(int64_t N, int64_t Q, int64_t H, int64_t G) {
   return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
 }
 
-// Pieces in the workspace.  Two a share: of those that it begins with and of those
+// Pieces in the workspace.  Two a workgroup: of those that its share begins with and of those
 // behind, at most one is cut or a chunk (a chunk has a share's tiles at least, a share
 // one more at most).  With groups, also one for each row block of each
 // entity, for units that are whole.
@@ -1106,10 +1109,11 @@ hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t s
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = f8 ? launch_l<true>(p, nb, stream) : launch_l<false>(p, nb, stream);
   if (e != hipSuccess) return e;
-  // Few rows: more waves share a row's pieces (1 x 4000 tokens, 32 heads: 28 us with 8 waves a
-  // row, 45 with one; 200 sequences of 64 rows: 113 with one, 154 with 8).
+  // Few rows: more waves share a row's pieces, 4096 waves in all (a call on 1 x 4000 tokens with 32
+  // heads takes 28 us, with one wave a row 45; the join of 64 x 128 rows 14 us, with up to 16384
+  // waves 20; of 64 x 16 rows of 30 pieces 15, with up to 8192 18).
   int parts = kWaves;
-  while (parts > 1 && (int64_t)p.rows * p.N * parts > 2048 * kWaves) parts >>= 1;
+  while (parts > 1 && (int64_t)p.rows * p.N * parts > 512 * kWaves) parts >>= 1;
   const int per = kWaves / parts;
   hipLaunchKernelGGL(shared_join_kernel, dim3((unsigned)((p.rows + per - 1) / per), (unsigned)p.N), dim3(kThreads), 0,
                      stream, p, MB, parts);
