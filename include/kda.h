@@ -598,8 +598,9 @@ kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const
  *                     table of the group's first sequence, up to its length;
  *                     the others' tables are read behind that.  Any number of
  *                     tokens, whole pages or not; negative: 0.
- *  The rest        -- as for kda_latent_decode, and N Q H times
- *                     max_pages * page_size may not exceed 2^48.
+ *  The rest        -- as for kda_latent_decode, N Q H times max_pages *
+ *                     page_size may not exceed 2^48, and with several pages the
+ *                     page strides lie below 2^32 bytes.
  *  workspace       -- device scratch, 16-byte aligned, of at least
  *                     kda_latent_shared_workspace_size(N, Q, H, L, G) bytes.
  * The result is that of kda_latent_decode, whose rules on lengths, pages, empty
@@ -608,7 +609,8 @@ kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const
  * of the group sees the row.
  * Precision: as kda_latent_decode; in 8 bits the codes enter both products as
  * bf16, which holds them whole, a token's scale multiplies its latent score in fp32,
- * and the softmax weight times the scale is rounded to bf16 once.
+ * and the softmax weight times the scale is rounded to bf16 once (below 2^-126 it
+ * may count as 0).
  * Codes must not be NaN (0x7f, 0xff): such a code can reach all queries of a tile of
  * 64 tokens.  A NaN or infinite scale, or a NaN in a rotary key, reaches the queries
  * that see its row and no others.

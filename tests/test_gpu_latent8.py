@@ -323,6 +323,19 @@ def test_shared(groups, alone, Q, H, L, R, page, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Q,H", [(1, 130), (5, 64), (2, 257), (7, 100), (3, 241), (1, 1024)])
+def test_shared_rows_of_many_blocks(Q, H, fp8):
+    """3, 5, 9, 11, 12 and 16 blocks of 64 query rows a sequence; a prefix's blocks are no multiple of those."""
+    gen = torch.Generator().manual_seed(Q * H)
+    groups, alone = [(700, [800, 720, 705, 700, 1200]), (64, [70, 200]), (130, [131, 150, 10])], (300, 0, 1)
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, groups, 16, 128, 64, fp8, Q, H, alone)
+    got = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "many blocks")
+    got = _run_shared(store, table, lens, [0], [], q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "many blocks, no groups")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("many", ["sequences", "groups", "room"])
 def test_shared_plans_of_large_batches(many, fp8):
     """More sequences or groups than the kernels plan by themselves, and a table with more room than 31 bits of tiles."""
