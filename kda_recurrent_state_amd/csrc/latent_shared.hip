@@ -997,8 +997,8 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
 }
 
 // Blocks of 16 query rows a workgroup takes at once: as few as hold a sequence's or the
-// batch's rows (64 x 4000 tokens in 8 bits, 16 heads: 63 us with one block, 68 with two,
-// 80 with four; 32 heads: 77 with two, 86 with four).
+// batch's rows (64 x 4000 tokens in 8 bits, 16 heads: 57 us with one block, 63 with two,
+// 76 with four; 32 heads: 64 with two, 77 with four).
 int blocks_of(int64_t N, int64_t Q, int64_t H, int64_t G) {
   const int64_t rows = G > 0 ? N * Q * H : Q * H;
   return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
@@ -1110,7 +1110,7 @@ hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t s
   if (e == hipSuccess) e = f8 ? launch_l<true>(p, nb, stream) : launch_l<false>(p, nb, stream);
   if (e != hipSuccess) return e;
   // Few rows: more waves share a row's pieces, 4096 waves in all (a call on 1 x 4000 tokens with 32
-  // heads takes 28 us, with one wave a row 45; the join of 64 x 128 rows 14 us, with up to 16384
+  // heads takes 27 us, with one wave a row 42; the join of 64 x 128 rows 14 us, with up to 16384
   // waves 20; of 64 x 16 rows of 30 pieces 15, with up to 8192 18).
   int parts = kWaves;
   while (parts > 1 && (int64_t)p.rows * p.N * parts > 512 * kWaves) parts >>= 1;
