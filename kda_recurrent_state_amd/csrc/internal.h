@@ -45,6 +45,10 @@ size_t latent_decode_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L)
 hipError_t launch_latent_shared(const kda_latent_shared_args_t& a, hipStream_t stream);
 size_t latent_shared_workspace_bytes(int64_t N, int64_t Q, int64_t H, int64_t L, int64_t G);
 
+// Rows that one launch of the 8-bit cache's kernels takes, of ``rows`` a workgroup of 256 threads: HIP launches fewer
+// than 2^32 threads a grid dimension.
+constexpr int64_t cache_slice_rows(int rows) { return (((int64_t)1 << 24) - 1) * rows; }
+
 // The 8-bit latent cache; arguments already validated.
 hipError_t launch_latent_quantize_scatter(const kda_latent_store_t& s, const void* c, int64_t c_stride,
                                           const void* k_rope, int64_t k_rope_stride, bool bf16, const void* slots,

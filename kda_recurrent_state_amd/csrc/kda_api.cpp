@@ -433,7 +433,8 @@ kda_status_t check_latent_store(const kda_latent_store_t* s, Span* spans) {
   return KDA_OK;
 }
 
-// Rows of a call on the 8-bit cache: 2^24 workgroups of 16 at most.
+// Rows of a call on the 8-bit cache: the kernels count them in 31 bits to the end of the last workgroup.  (A call of
+// more than a launch takes goes in several.)
 constexpr int64_t kMostRows = ((int64_t)1 << 28) - 1;
 
 kda_status_t check_latent_shared(const kda_latent_shared_args_t* a) {

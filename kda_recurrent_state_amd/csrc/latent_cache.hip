@@ -248,23 +248,38 @@ __global__ __launch_bounds__(kThreads) void dequantize_gather_kernel(CacheParams
 // not hold from whatever wrote them (32768 rows, 38 MB, read again and again: 13.1 against
 // 12.2; 98304 rows, 113 MB: 29 against 34).  Four rows a lane group took 30 and 34 us, eight 33 and 35.
 template <bool kWrite, typename T, typename Index, int LANES>
-hipError_t launch_lanes(const CacheParams& p, hipStream_t stream) {
+hipError_t launch_lanes(const CacheParams& call, hipStream_t stream) {
   constexpr int kRows = 64 / LANES * kWaves;
-  const bool many = kWrite ? (int64_t)p.n * (p.L + p.R) * (int)sizeof(T) > (64 << 20) : p.n > 1024 * kRows;
+  const bool many =
+      kWrite ? (int64_t)call.n * (call.L + call.R) * (int)sizeof(T) > (64 << 20) : call.n > 1024 * kRows;
   const int rows = kRows * (many ? 2 : 1);
-  const dim3 grid((unsigned)(((int64_t)p.n + rows - 1) / rows)), block(kThreads);
-  if (kWrite) {
-    if (many)
-      hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
-  } else {
-    if (many)
-      hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
+  const int64_t most = cache_slice_rows(rows);
+  for (int64_t done = 0; done < call.n; done += most) {
+    CacheParams p = call;
+    p.n = (int)(call.n - done < most ? call.n - done : most);
+    p.slots = static_cast<const Index*>(call.slots) + done;
+    if (kWrite) {
+      p.c += done * call.c_stride;
+      p.k_rope += done * call.k_rope_stride;  // (strides in bytes)
+    } else {
+      p.out += done * ((call.L + call.R) * (int)sizeof(T));
+    }
+    const dim3 grid((unsigned)(((int64_t)p.n + rows - 1) / rows)), block(kThreads);
+    if (kWrite) {
+      if (many)
+        hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
+      else
+        hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
+    } else {
+      if (many)
+        hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
+      else
+        hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 template <bool kWrite, typename T, typename Index>

@@ -105,6 +105,62 @@ def test_written_rows_of_a_large_batch(T, L, R, page, dtype):
     assert (got[0][~hit] == 0x55).all() and (got[1][~hit] == -7).all() and (got[2][~hit] == 3).all()
 
 
+def _at_the_ends(n, border):
+    """Rows of a call of n: its first and last ones, and those around ``border``, where a second launch begins."""
+    return torch.cat([torch.arange(4), torch.arange(border - 4, border + 4), torch.arange(n - 4, n)])
+
+
+@pytest.mark.parametrize("n,L,R,index", [((1 << 27) + 5, 272, 8, torch.int32), ((1 << 28) - 1, 144, 0, torch.int64)])
+def test_written_rows_of_the_largest_calls(n, L, R, index):
+    """More rows than a launch of fewer than 2^32 threads takes: 8 rows (L > 256) or 16 a workgroup of 256.  The input's
+    rows overlap (one begins 8 values behind the one before), and few of them are written."""
+    import kda_recurrent_state_amd as kda
+    at = _at_the_ends(n, ((1 << 24) - 1) * (8 if L > 256 else 16))
+    codes, scales, rope = _empty_store(3, 16, L, R)
+    base = torch.arange(1009, device="cuda").to(BF16).repeat((8 * n + L) // 1009 + 1)
+    c = torch.as_strided(base, (n, L), (8, 1))
+    k_rope = torch.as_strided(base, (n, R), (8, 1)) if R else None
+    slots = torch.full((n,), -1, dtype=index, device="cuda")
+    places = torch.randperm(48, generator=torch.Generator().manual_seed(1))[: len(at)]
+    slots[at.cuda()] = places.to(index).cuda()
+    kda.kda_latent_quantize_scatter(c, k_rope, slots, codes, scales, rope)
+    rows = torch.stack([c[int(t)] for t in at]).cpu()
+    want, scale = ref8.quantize(rows.double())
+    hit = torch.zeros(48, dtype=torch.bool)
+    hit[places] = True
+    got = codes.cpu().view(-1, L), scales.cpu().view(-1)
+    assert torch.equal(got[0][places], want) and torch.equal(got[1][places].double(), scale)
+    assert (got[0][~hit] == 0x55).all() and (got[1][~hit] == -7).all()
+    if R:
+        assert torch.equal(rope.cpu().view(-1, R)[places], rows[:, :R]) and (rope.cpu().view(-1, R)[~hit] == 3).all()
+    del base, c, k_rope, slots
+    torch.cuda.empty_cache()
+
+
+def test_read_rows_of_the_largest_calls():
+    """The same of reading; most entries are no slot and give zeros."""
+    import kda_recurrent_state_amd as kda
+    n, L = (1 << 27) + 5, 272
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 75 GB for the rows")
+    gen = torch.Generator().manual_seed(4)
+    at = _at_the_ends(n, ((1 << 24) - 1) * 8)
+    codes, scales, _ = _cache8(gen, 3, 16, L, 0)
+    places = torch.randint(0, 48, (len(at),), generator=gen)
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    slots[at.cuda()] = places.int().cuda()
+    out = kda.kda_latent_dequantize_gather(codes.cuda(), scales.cuda(), None, slots)
+    want = (ref8.VALUES[codes.long()].float() * scales[..., None]).to(BF16).view(-1, L)[places]
+    assert torch.equal(torch.stack([out[int(t)] for t in at]).cpu(), want)
+    for t in at:
+        out[int(t)].zero_()
+    for part in out.split(1 << 23):
+        assert not part.view(torch.int32).any()
+    del out, part, slots
+    torch.cuda.empty_cache()
+
+
 def test_rows_that_are_not_finite():
     import kda_recurrent_state_amd as kda
     codes, scales, rope = _empty_store(2, 4, 128, 8)
