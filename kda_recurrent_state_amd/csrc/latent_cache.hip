@@ -6,10 +6,12 @@
 // values).  The scale is a power of two: 2^e with the smallest e >= -126 for which the
 // row's largest magnitude is at most 448 2^e.  A division by it is exact, so a
 // code is the value itself rounded once (half a step: 2^-4 of the value down to
-// 2^-6 of the scale), reading back to bf16 is exact, and writing again what was
-// read gives the same values.  One scale a row, not one a block: e4m3 is
-// a floating format, and a value keeps its four bits down to 2^-14 of the row's
-// largest; and a scale per row leaves both products of decode as products of codes.
+// 2^-6 of the scale), reading back is exact in fp32, and in bf16 too for rows written from
+// bf16 and scales of 2^-124 and more (below, the smallest code, 2^-9 of the scale, lies under
+// bf16's smallest subnormal, 2^-133, and is rounded), and writing again what was
+// read exactly gives the same values.  One scale a row, not one a block: e4m3 is
+// a floating format, and a value keeps its four bits down to 2^-13 of the row's
+// largest, which is above 224 scales; and a scale per row leaves both products of decode as products of codes.
 //
 // Both kernels move each byte once and are bound by HBM.  A lane has 8
 // values; 16, 32 or 64 lanes have a row.  98304 rows of 512 + 64 values (171 MB) are

@@ -213,6 +213,34 @@ def test_written_and_read_and_written_again():
     assert torch.equal(ref8.values(*b), ref8.values(*a))
 
 
+def test_rows_of_the_smallest_magnitudes():
+    """fp32 rows down to the smallest subnormals, whose scale is 2^-126 to 2^-124: the fp32 read is exact, the bf16 read
+    its rounding (a code can be worth 2^-135, bf16 ends at 2^-133), exact from the scale 2^-124 on; and rows whose small
+    values lie 2^-13 below the largest keep four bits."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(6)
+    exps = torch.arange(-149, -114, dtype=torch.float64)
+    x = torch.randn(len(exps), 128, generator=gen, dtype=torch.float64) * torch.exp2(exps)[:, None]
+    x[-1] = 2.0 ** -117 * 225                                   # a largest one just above 224 scales
+    x[-1, 1:] *= 2.0 ** -13 * (1 + torch.rand(127, generator=gen, dtype=torch.float64))
+    x = x.float()
+    store = _empty_store(4, 16, 128, 0)[:2]
+    slots = torch.arange(len(x), device="cuda")
+    kda.kda_latent_quantize_scatter(x.cuda(), None, slots, *store)
+    codes, scales = ref8.quantize(x.double())
+    assert torch.equal(store[0].cpu().view(-1, 128)[:len(x)], codes)
+    assert torch.equal(store[1].cpu().view(-1)[:len(x)].double(), scales)
+    want = ref8.VALUES[codes.long()] * scales[:, None]          # multiples of 2^-135: fp32 holds them
+    assert torch.equal(want.float().double(), want)
+    assert ((want[-1] - x[-1].double()).abs() <= 2.0 ** -4 * x[-1].double().abs()).all()
+    assert torch.equal(kda.kda_latent_dequantize_gather(*store, None, slots, dtype=torch.float32).cpu(), want.float())
+    got = kda.kda_latent_dequantize_gather(*store, None, slots).cpu()
+    assert torch.equal(got, want.float().to(BF16))
+    fine = scales >= 2.0 ** -124
+    assert fine.any() and torch.equal(got[fine].double(), want[fine])
+    assert not torch.equal(got[~fine].double(), want[~fine])
+
+
 # --- decode -----------------------------------------------------------------
 
 def _cache8(gen, pages, page, L, R, spread=1.0):
