@@ -411,7 +411,10 @@ kda_status_t kda_ckpt_dequantize_gather(const kda_int8_store_t* store, const voi
  * Precision: products of bf16 operands with fp32 sums; scores (and their
  * products with log2 e, which count as infinite beyond fp32), the running
  * maximum and sum and the output accumulate in fp32; the softmax weights are
- * rounded to bf16 as operands of the second product.
+ * rounded to bf16 as operands of the second product.  The weights are taken against a
+ * maximum that may be 2^8 too small, and the output is divided by their sum at the end:
+ * where the keys that a query sees times the largest magnitude of a value pass 2^119, it
+ * can be infinite or NaN although the formula's result is not.
  * A NaN or infinite value row v_j can reach queries that do not see key j but
  * see another key of the same 64 (their weight 0 multiplies it); keys and
  * rotary keys that a query does not see never reach it.
@@ -610,7 +613,8 @@ kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const
  * Precision: as kda_latent_decode; in 8 bits the codes enter both products as
  * bf16, which holds them whole, a token's scale multiplies its latent score in fp32,
  * and the softmax weight times the scale is rounded to bf16 once (below 2^-126 it
- * may count as 0).
+ * may count as 0).  Infinite results by large values are as there (2^119), in 8 bits by a
+ * row's scale of 2^119 and more too.
  * Codes must not be NaN (0x7f, 0xff): such a code can reach all queries of a tile of
  * 64 tokens.  A NaN or infinite scale, or a NaN in a rotary key, reaches the queries
  * that see its row and no others.

@@ -563,6 +563,32 @@ def test_scores_of_any_size(size, fp8):
         assert (got[1][n].double().cpu() - (top + math.log(len(seen)))).abs().max() <= 2.0 ** -20 * top + 1e-4
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_values_as_large_as_documented(fp8):
+    """500 tokens with values up to 2^109 (their product is below 2^119: 2^8 times it is fp32), and scores that rise by 7.6 units of log2, so
+    that the maximum in use stays behind: the results are those of the formula."""
+    gen = torch.Generator().manual_seed(21)
+    N, page, L, R, H = 200, 64, 128, 8, 8
+    lens = [500 - n % 3 for n in range(N)]
+    table, pages = _table(gen, lens, page)
+    latent = torch.randn(pages * page, L, generator=gen).clamp(-4, 4) * 2.0 ** 107
+    k_rope = torch.zeros(pages * page, R)
+    for n in range(N):
+        j = torch.arange(lens[n])
+        k_rope[table[n].long()[j // page] * page + j % page, 2] = j * (7.6 / 512)
+    if fp8:
+        codes, scales = ref8.quantize(latent.double())
+        store = (codes.view(pages, page, L), scales.float().view(pages, page), k_rope.to(BF16).view(pages, page, R))
+    else:
+        store = (torch.cat([latent, k_rope], 1).to(BF16).view(pages, page, L + R),)
+    q, q_rope = _queries(gen, N, 1, H, L, R)
+    q = q * 0
+    q_rope = q_rope * 0
+    q_rope[..., 2] = math.log(2) / SCALE
+    got = _run_shared(store, table, lens, [0], [], q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "large values")
+
+
 def test_decode8_query_that_is_not_finite():
     import kda_recurrent_state_amd as kda
     gen = torch.Generator().manual_seed(16)
