@@ -213,6 +213,24 @@ def test_written_and_read_and_written_again():
     assert torch.equal(ref8.values(*b), ref8.values(*a))
 
 
+def test_slots_that_are_rows_in_their_low_32_bits_alone():
+    import kda_recurrent_state_amd as kda
+    store = _empty_store(2, 16, 128, 8)
+    c, k_rope = _rows(9, 128, 8, BF16, 7)
+    slots = torch.tensor([3, 2 ** 32 + 4, -2 ** 32 + 5, 2 ** 62, -2 ** 62, 2 ** 62 + 6, -2 ** 62 + 7, 2 ** 63 - 1, 8])
+    fine = torch.tensor([True] + [False] * 7 + [True])
+    kda.kda_latent_quantize_scatter(c, k_rope, slots.cuda(), *store)
+    want, _ = ref8.quantize(c.cpu().double())
+    got, at = store[0].cpu().view(-1, 128), slots[fine]
+    rest = torch.ones(32, dtype=torch.bool)
+    rest[at] = False
+    assert torch.equal(got[at], want[fine]) and (got[rest] == 0x55).all()
+    assert (store[1].cpu().view(-1)[rest] == -7).all() and (store[2].cpu().view(-1, 8)[rest] == 3).all()
+    rows = kda.kda_latent_dequantize_gather(*store, slots.cuda()).cpu()
+    assert (rows[~fine] == 0).all()
+    assert torch.equal(rows[fine].double(), ref8.values(*store).view(-1, 136)[at])
+
+
 def test_rows_of_the_smallest_magnitudes():
     """fp32 rows down to the smallest subnormals, whose scale is 2^-126 to 2^-124: the fp32 read is exact, the bf16 read
     its rounding (a code can be worth 2^-135, bf16 ends at 2^-133), exact from the scale 2^-124 on; and rows whose small
@@ -417,6 +435,31 @@ def test_shared_rows_of_many_blocks(Q, H, fp8):
     _check_shared(store, table, lens, q, q_rope, got, "many blocks")
     got = _run_shared(store, table, lens, [0], [], q, q_rope)
     _check_shared(store, table, lens, q, q_rope, got, "many blocks, no groups")
+
+
+@pytest.mark.parametrize("L,R", [(8, 0), (8, 56), (24, 8), (136, 0), (136, 64), (504, 56), (504, 0)])
+@pytest.mark.parametrize("groups,Q,H", [
+    ([(100, [130, 101])], 1, 8), ([(70, [71, 200])], 2, 8), ([(200, [260, 201, 199]), (64, [65, 300])], 1, 24)])
+def test_shared_dims_of_8_more_than_16s(groups, Q, H, L, R):
+    """The 16-bit cache takes any multiple of 8; with 1, 2 and 4 blocks of 16 query rows a workgroup."""
+    gen = torch.Generator().manual_seed(L + R)
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, groups, 16, L, R, False, Q, H)
+    got = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "dims")
+    got = _run_shared(store, table, lens, [0], [], q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "dims, no groups")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("seqs", [5, 9])
+def test_shared_prefix_of_many_chunks(seqs, fp8):
+    """Two and three row blocks behind 32768 tokens: shares of 4 and 6 of its 512 tiles, so 128 and 85 chunks, and the
+    join looks up 64 at a time."""
+    gen = torch.Generator().manual_seed(seqs)
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, [(32768, [32769 + 3 * i for i in range(seqs)])], 64, 128,
+                                                               64, fp8, 1, 16)
+    got = _run_shared(store, table, lens, cu, shared, q, q_rope)
+    _check_shared(store, table, lens, q, q_rope, got, "many chunks")
 
 
 @pytest.mark.parametrize("fp8", [False, True])
