@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "latent_plan.h"
 #include "latent_tile.h"
 
 namespace kda {
@@ -48,32 +49,7 @@ using namespace latent;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kShares = 256;       // workgroups, one a CU
 constexpr int kPlanThreads = 512;
-// Room before a unit of an entity of one chunk, in tiles: 40 sequences of 64 to 1024 tokens behind
-// a prefix, 256 query rows each, take 436 us with 4, 476 with 3 and 525 with 2 (the shares with many
-// units come last) and 433 with 6, where 200 ragged ones take 109, 110, 116 and 112.
-constexpr int kEnd = 4;
-
-struct Entity {
-  int64_t base, first;     // place on the line, and the number of its first tile
-  int32_t tiles, row_blocks;  // row_blocks: a team's, of ``team`` blocks of MB rows each
-  int32_t chunks, chunk;   // and the tiles of one; the first ``longer`` ones have one more
-  int32_t longer;
-  int32_t row0, rows;      // query rows
-  int32_t seq, t0, t1;     // tokens [t0, t1) of this sequence
-  int32_t slot;            // of its first row block's pieces that no share cuts and that are not chunks
-  int32_t group;           // of a sequence: the entity of its prefix, or -1
-
-  __device__ __forceinline__ int room() const { return chunks == 1 ? kEnd : 0; }
-  // place on the line, from the entity's, of row block rb of chunk k (its room, then its tiles)
-  __device__ __forceinline__ int64_t unit_begin(int k, int rb) const {
-    return (int64_t)chunk_begin(k) * row_blocks + (int64_t)rb * (chunk_tiles(k) + room());
-  }
-  __device__ __forceinline__ int64_t line() const { return (int64_t)row_blocks * (tiles + room()); }
-  __device__ __forceinline__ int chunk_begin(int k) const { return k * chunk + min(k, longer); }
-  __device__ __forceinline__ int chunk_tiles(int k) const { return chunk + (k < longer ? 1 : 0); }
-};
 
 struct Start {  // where a workgroup begins: tile t of a team's row block rb of chunk k of entity e
   int32_t left, w, e, k, rb, t;  // left: tiles of the share, 0: none; w: share * team + member
@@ -115,36 +91,6 @@ __device__ __forceinline__ int tokens_of(const SharedParams& p, int len) {
   return len < 0 ? 0 : (len > room ? (int)room : len);
 }
 __device__ __forceinline__ int seq_tokens(const SharedParams& p, int n) { return tokens_of(p, p.lengths[n]); }
-
-// a / b of 0 <= a < 2^52, 0 < b, or with ``narrow`` (the same in all lanes) < 2^31.  (The quotient
-// in fp64 is off by less than one; a division of 64-bit integers is four times the
-// instructions, and the plan's and the join's time is much of their own code's way
-// into the caches.)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b, bool narrow) {
-  if (narrow) return (unsigned)a / (unsigned)b;
-  const int64_t q = (int64_t)((double)a / (double)b), r = a - q * b;
-  return q + (r < 0 ? -1 : (r >= b ? 1 : 0));
-}
-
-// The line in equal shares, none empty (fewer of them where there are fewer tiles).
-struct Shares {
-  int64_t quot;
-  int rem, count;
-  bool narrow;  // whether the line has fewer than 2^31 places
-};
-__device__ __forceinline__ Shares shares_of(const SharedParams& p, int64_t total) {
-  const unsigned most = kShares / (unsigned)p.team;
-  const bool few = total < most;
-  return {few ? 1 : (int64_t)((uint64_t)total / most), few ? 0 : (int)((uint64_t)total % most),
-          few ? (int)total : (int)most, total >> 31 == 0};
-}
-__device__ __forceinline__ int64_t share_begin(const Shares& s, int w) { return w * s.quot + min(w, s.rem); }
-// the share that holds place x
-__device__ __forceinline__ int share_at(const Shares& s, int64_t x) {
-  const int64_t longer = s.rem * (s.quot + 1);
-  const bool in = x < longer;
-  return (in ? 0 : s.rem) + (int)quotient(in ? x : x - longer, in ? s.quot + 1 : s.quot, s.narrow);
-}
 
 // Inclusive sums of two numbers over the workgroup's threads up to this one;
 // *all_x, *all_y: over all of them.
@@ -277,7 +223,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     block_scan(n, zero, sums, &all, &zero);
     total += all;
   }
-  const long long quot = shares_of(p, total).quot;
+  const long long quot = shares_of(p.team, total).quot;
   const unsigned share = quot > (1 << 30) ? 1u << 30 : (unsigned)quot;
   long long base = 0, first = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
@@ -286,9 +232,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     if (e < E) {
       if (!few) mine = entity(e);
       if (mine.tiles > 0) {
-        mine.chunks = mine.row_blocks == 1 ? 1 : (int)max(1u, (unsigned)mine.tiles / share);
-        mine.chunk = (int)((unsigned)mine.tiles / (unsigned)mine.chunks);
-        mine.longer = mine.tiles - mine.chunk * mine.chunks;
+        mine.cut(share);
         n = mine.line();
         tiles = (long long)mine.tiles * mine.row_blocks;
       }
@@ -307,7 +251,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
   if (tid == 0) *p.total = base;
   if (tid < kShares) p.starts[tid].left = 0;
   __syncthreads();
-  const Shares sh = shares_of(p, base);
+  const Shares sh = shares_of(p.team, base);
   Start s;
   const int w = (unsigned)tid / (unsigned)p.team;  // thread: a member of this share's team
   if (w < sh.count) {
@@ -317,20 +261,12 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
       const int mid = (lo + hi) >> 1;
       if (ents[mid].base <= from) lo = mid; else hi = mid;
     }
-    // the unit and tile of that place; a unit's room counts as its first tile
     s.ent = ents[lo];
     const Entity& x = s.ent;
-    const int64_t in = from - x.base;
-    if (x.chunks == 1) {
-      s.k = 0;
-      s.rb = (int)quotient(in, x.tiles + kEnd, sh.narrow);
-    } else {
-      const unsigned y = (unsigned)quotient(in, x.row_blocks, sh.narrow), longer = x.longer * (x.chunk + 1);
-      s.k = (int)(y < longer ? y / (unsigned)(x.chunk + 1) : x.longer + (y - longer) / (unsigned)x.chunk);
-      s.rb = (int)quotient(in - x.unit_begin(s.k, 0), x.chunk_tiles(s.k), sh.narrow);
-    }
-    const int64_t rest = in - x.unit_begin(s.k, s.rb) - x.room();
-    s.t = rest > 0 ? (int)rest : 0;
+    const Spot at = x.at(from - x.base, sh.narrow);
+    s.k = at.k;
+    s.rb = at.rb;
+    s.t = at.t;
     s.e = lo;
     s.w = tid;
     number[w] = x.first + (int64_t)x.chunk_begin(s.k) * x.row_blocks + (int64_t)s.rb * x.chunk_tiles(s.k) + s.t;
@@ -892,7 +828,7 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
     if (p.lse && lane == 0) p.lse[grow] = -INFINITY;
     return;
   }
-  const Shares sh = shares_of(p, scalar_load(p.total));
+  const Shares sh = shares_of(p.team, scalar_load(p.total));
   // a sequence that one piece holds whole has its output
   if (own.t0 == 0 && own.chunks == 1) {
     const int rb = (blockIdx.x * (kWaves / parts)) / MB;  // (that of all the workgroup's rows)
