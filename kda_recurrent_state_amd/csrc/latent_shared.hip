@@ -223,7 +223,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
     block_scan(n, zero, sums, &all, &zero);
     total += all;
   }
-  const long long quot = shares_of(p.team, total).quot;
+  const long long quot = shares_of(p, total).quot;
   const unsigned share = quot > (1 << 30) ? 1u << 30 : (unsigned)quot;
   long long base = 0, first = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedParams 
   if (tid == 0) *p.total = base;
   if (tid < kShares) p.starts[tid].left = 0;
   __syncthreads();
-  const Shares sh = shares_of(p.team, base);
+  const Shares sh = shares_of(p, base);
   Start s;
   const int w = (unsigned)tid / (unsigned)p.team;  // thread: a member of this share's team
   if (w < sh.count) {
@@ -828,7 +828,7 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
     if (p.lse && lane == 0) p.lse[grow] = -INFINITY;
     return;
   }
-  const Shares sh = shares_of(p.team, scalar_load(p.total));
+  const Shares sh = shares_of(p, scalar_load(p.total));
   // a sequence that one piece holds whole has its output
   if (own.t0 == 0 && own.chunks == 1) {
     const int rb = (blockIdx.x * (kWaves / parts)) / MB;  // (that of all the workgroup's rows)

@@ -4,6 +4,14 @@
 
 using namespace kda::latent;
 
+namespace {
+
+struct Team {
+  int team;
+};
+
+}  // namespace
+
 extern "C" {
 
 int64_t cache_slice_rows(int rows) { return kda::cache_slice_rows(rows); }
@@ -12,14 +20,14 @@ int64_t plan_quotient(int64_t a, int64_t b, int narrow) { return quotient(a, b, 
 
 // quot, rem, count, narrow
 void plan_shares(int team, int64_t total, int64_t* out) {
-  const Shares s = shares_of(team, total);
+  const Shares s = shares_of(Team{team}, total);
   out[0] = s.quot;
   out[1] = s.rem;
   out[2] = s.count;
   out[3] = s.narrow;
 }
-int64_t plan_share_begin(int team, int64_t total, int w) { return share_begin(shares_of(team, total), w); }
-int plan_share_at(int team, int64_t total, int64_t x) { return share_at(shares_of(team, total), x); }
+int64_t plan_share_begin(int team, int64_t total, int w) { return share_begin(shares_of(Team{team}, total), w); }
+int plan_share_at(int team, int64_t total, int64_t x) { return share_at(shares_of(Team{team}, total), x); }
 
 // An entity's chunks and line: chunks, chunk, longer, room, line
 void plan_cut(int tiles, int row_blocks, unsigned share, int64_t* out) {
