@@ -244,16 +244,19 @@ __global__ __launch_bounds__(kThreads) void dequantize_gather_kernel(CacheParams
   }
 }
 
-// Which calls have many rows.  Reading: those of more than 1024 workgroups (8192 rows of
-// 512 + 64 bf16 values 9.4 us either way, 32768 10.7 against 12.2 with a row a lane group and
+// Which calls have many rows: in bf16 alone.  Reading: those of more than 1024 workgroups (8192 rows of
+// 512 + 64 values 9.4 us either way, 32768 10.7 against 12.2 with a row a lane group and
 // plain stores, 120000 34 against 54).  Writing: inputs of more than 64 MiB, which the caches do
 // not hold from whatever wrote them (32768 rows, 38 MB, read again and again: 13.1 against
 // 12.2; 98304 rows, 113 MB: 29 against 34).  Four rows a lane group took 30 and 34 us, eight 33 and 35.
+// In fp32 a lane has 32 bytes and an instruction moves 16 of each 32, which past the caches
+// does not come together (32768 and 65536 rows read 26 and 51 us against 17 and 29, 131072 105
+// against 95, of 128 + 64 values 33 against 22; 65536 and 98304 written 38 and 56 against 35 and 51).
 template <bool kWrite, typename T, typename Index, int LANES>
 hipError_t launch_lanes(const CacheParams& call, hipStream_t stream) {
   constexpr int kRows = 64 / LANES * kWaves;
-  const bool many =
-      kWrite ? (int64_t)call.n * (call.L + call.R) * (int)sizeof(T) > (64 << 20) : call.n > 1024 * kRows;
+  constexpr bool kBf16 = sizeof(T) == 2;
+  const bool many = kBf16 && (kWrite ? (int64_t)call.n * (call.L + call.R) * 2 > (64 << 20) : call.n > 1024 * kRows);
   const int rows = kRows * (many ? 2 : 1);
   const int64_t most = cache_slice_rows(rows);
   for (int64_t done = 0; done < call.n; done += most) {
@@ -269,12 +272,12 @@ hipError_t launch_lanes(const CacheParams& call, hipStream_t stream) {
     const dim3 grid((unsigned)(((int64_t)p.n + rows - 1) / rows)), block(kThreads);
     if (kWrite) {
       if (many)
-        hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, kBf16>), grid, block, 0, stream, p);
       else
         hipLaunchKernelGGL((quantize_scatter_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
     } else {
       if (many)
-        hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, true>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, kBf16>), grid, block, 0, stream, p);
       else
         hipLaunchKernelGGL((dequantize_gather_kernel<T, Index, LANES, false>), grid, block, 0, stream, p);
     }

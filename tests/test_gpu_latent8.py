@@ -110,14 +110,16 @@ def _at_the_ends(n, border):
     return torch.cat([torch.arange(4), torch.arange(border - 4, border + 4), torch.arange(n - 4, n)])
 
 
-@pytest.mark.parametrize("n,L,R,index", [((1 << 27) + 5, 272, 8, torch.int32), ((1 << 28) - 1, 144, 0, torch.int64)])
-def test_written_rows_of_the_largest_calls(n, L, R, index):
-    """More rows than a launch of fewer than 2^32 threads takes: 8 rows (L > 256) or 16 a workgroup of 256.  The input's
+@pytest.mark.parametrize("n,L,R,index,dtype,rows", [
+    ((1 << 27) + 5, 272, 8, torch.int32, BF16, 8), ((1 << 28) - 1, 144, 0, torch.int64, BF16, 16),
+    ((1 << 26) + 5, 272, 8, torch.int32, torch.float32, 4)])
+def test_written_rows_of_the_largest_calls(n, L, R, index, dtype, rows):
+    """More rows than a launch of fewer than 2^32 threads takes, of ``rows`` a workgroup of 256.  The input's
     rows overlap (one begins 8 values behind the one before), and few of them are written."""
     import kda_recurrent_state_amd as kda
-    at = _at_the_ends(n, ((1 << 24) - 1) * (8 if L > 256 else 16))
+    at = _at_the_ends(n, ((1 << 24) - 1) * rows)
     codes, scales, rope = _empty_store(3, 16, L, R)
-    base = torch.arange(1009, device="cuda").to(BF16).repeat((8 * n + L) // 1009 + 1)
+    base = torch.arange(1009, device="cuda").to(dtype).repeat((8 * n + L) // 1009 + 1)
     c = torch.as_strided(base, (n, L), (8, 1))
     k_rope = torch.as_strided(base, (n, R), (8, 1)) if R else None
     slots = torch.full((n,), -1, dtype=index, device="cuda")
@@ -132,7 +134,7 @@ def test_written_rows_of_the_largest_calls(n, L, R, index):
     assert torch.equal(got[0][places], want) and torch.equal(got[1][places].double(), scale)
     assert (got[0][~hit] == 0x55).all() and (got[1][~hit] == -7).all()
     if R:
-        assert torch.equal(rope.cpu().view(-1, R)[places], rows[:, :R]) and (rope.cpu().view(-1, R)[~hit] == 3).all()
+        assert torch.equal(rope.cpu().view(-1, R)[places], rows[:, :R].to(BF16)) and (rope.cpu().view(-1, R)[~hit] == 3).all()
     del base, c, k_rope, slots
     torch.cuda.empty_cache()
 
