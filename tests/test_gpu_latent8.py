@@ -490,6 +490,35 @@ def test_shared_plans_of_large_batches(many, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("per", [1, 2, 3, 65535])
+def test_shared_as_many_sequences_as_there_can_be(per, fp8):
+    """65535 sequences, in as many groups, in pairs, in threes and in one group; with queries of 0 the output is the mean
+    of the two rows that a sequence sees, the first one of which is that of its group's first sequence."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(per)
+    N, L, page = 65535, 16, 1
+    G = -(-N // per)
+    codes = torch.randint(0, 120, (2 * N, page, L), generator=gen).to(torch.uint8)
+    scales = torch.exp2(torch.randint(-2, 2, (2 * N, page), generator=gen).float())
+    values = ref8.values(codes, scales, None)
+    store = (codes, scales, None) if fp8 else (values.to(BF16),)   # (4 bits: bf16 holds them)
+    perm = torch.randperm(2 * N, generator=gen).int()
+    table = torch.stack([perm[:N], perm[N:]], 1)
+    cu = (torch.arange(G + 1) * per).clamp(max=N)
+    if per > 1:                                                     # what the others' tables have there is not read
+        table[torch.arange(N) % per != 0, 0] = -1
+    q = torch.zeros(N, 2, L, dtype=BF16, device="cuda")
+    out, lse = kda.kda_latent_decode_shared(_gpu(store) if fp8 else store[0].cuda(), table.cuda(), _i32([2] * N),
+                                            cu.int().cuda(), _i32([1] * G), q, scale=1.0, with_lse=True)
+    rows = values.view(-1, L)
+    first = table[torch.arange(N) // per * per, 0].long()
+    want = (rows[first] + rows[table[:, 1].long()]) / 2
+    # the mean is rounded once to bf16 and four times in fp32
+    assert ((out.cpu().double() - want[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -20) * want[:, None]).all()
+    assert (lse.cpu().double() - math.log(2)).abs().max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_shared_groups_that_are_no_offsets(fp8):
     """Bounds that fall are raised to the largest before, and clamped to the batch; shared lengths are clamped."""
     gen = torch.Generator().manual_seed(11)
@@ -570,6 +599,28 @@ def test_shared_twice_is_the_same(fp8):
     a = _run_shared(store, table, lens, cu, shared, q, q_rope)
     b = _run_shared(store, table, lens, cu, shared, q, q_rope)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("groups,alone,Q,H", [
+    ([], (4000,), 1, 32), ([(700, [800, 720, 705, 700])], (300, 0, 1), 1, 4), ([(3000, [3100 + 7 * i for i in range(9)])], (900,), 1, 20),
+    ([(640, [700, 1300, 641])] * 6, (), 1, 64), ([], tuple(range(20, 3000, 41)), 2, 40), ([(9000, [9001 + i for i in range(20)])], (), 1, 130)])
+def test_shared_results_are_the_workspaces_own(groups, alone, Q, H, fp8):
+    """Whatever a workspace holds before the call, the results are the same to the bit: nothing is read that the call has
+    not written."""
+    import kda_recurrent_state_amd as kda
+    gen = torch.Generator().manual_seed(22 + H)
+    store, table, lens, cu, shared, q, q_rope = _shared_inputs(gen, groups, 16, 128, 64, fp8, Q, H, alone)
+    if not groups:
+        cu = [0]
+    need = kda.kda_latent_shared_workspace_size(len(lens), Q, H, 128, len(shared))
+    got = []
+    for fill in (0, 0xff, 0x7f, 0x01):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        got.append(_run_shared(store, table, lens, cu, shared, q, q_rope, workspace=ws))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    _check_shared(store, table, lens, q, q_rope, got[0], "workspaces")
 
 
 @pytest.mark.parametrize("fp8", [False, True])
