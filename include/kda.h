@@ -532,6 +532,8 @@ kda_status_t kda_latent_decode(const kda_latent_decode_args_t* args, void* strea
  *             Pages are dense inside; from page to page lie codes_page_stride
  *             bytes (a multiple of 16), scales_page_stride fp32 and
  *             rope_page_stride bf16 (a multiple of 8).
+ *             The three byte ranges, first page to last, lie apart (arrays that take turns
+ *             page by page in one block of memory are refused, as by kda_page_fork).
  *  num_pages, page_size -- positive, num_pages * page_size below 2^31.
  *  L, R    -- latent dim (16..512, a multiple of 16), rotary key dim (0..64, a
  *             multiple of 8).
@@ -606,6 +608,15 @@ kda_status_t kda_latent_dequantize_gather(const kda_latent_store_t* store, const
  *                     page strides lie below 2^32 bytes.
  *  workspace       -- device scratch, 16-byte aligned, of at least
  *                     kda_latent_shared_workspace_size(N, Q, H, L, G) bytes.
+ *                     (With groups it holds at least a block of 16, 32 or, above 32 query rows in
+ *                     the batch, 64 rows of fp32 outputs for each sequence and group.)
+ * When to share: a prefix is read once for 64 query rows and not once a sequence,
+ * but the products stay the same and joining costs a launch's time.  On MI355X it
+ * pays from about 64 sequences of up to 32 query rows (Q H) behind 4096 to 8192 tokens on (64
+ * of 8 rows behind 32768 in one group: 86 us against 220), and does not for few sequences,
+ * short prefixes (64 of 32 rows behind 1024: 43 against 37) and 128 rows and more, where
+ * products bound both.  A shared length that is no multiple of 8, and pages of no multiple
+ * of 8 tokens, cost up to a sixth more (tokens are then looked up one by one).
  * The result is that of kda_latent_decode, whose rules on lengths, pages, empty
  * rows and order of workgroups hold.  With a shared prefix, query rows see the
  * first rows through the first sequence's table: where that has no page, no sequence

@@ -30,12 +30,14 @@
 //
 // What bounds it: the phases of a tile, which follow one another within the CU's
 // one workgroup.  64 sequences of 12000 to 20000 tokens with 128 heads, 512 + 64
-// components, take 385 us in 8 bits (660 MB, 131 us at a copy's rate; products 250 us at a large
+// components, take 385 us in 8 bits (660 MB, 131 us at a copy's rate; products 204 us at a large
 // matrix product's); a tile of 64 rows takes 2.8 us, the matrix unit is busy for a third of
 // it, and without its fetches, scores, softmax or output product the call is 75, 90, 40 or
 // 72 us shorter.  40 sequences of 256 query rows behind 16384 shared tokens: 430 us in 16
-// bits, 505 in 8 (products 334), where decode that reads the prefix for each sequence
-// computes the same and reads 40 times as much.  The plan takes 5 to 9 us, the join 6 to 18.
+// bits, 505 in 8 (products 273), where decode that reads the prefix for each sequence computes
+// the same and reads 40 times as much, which at so many query rows takes no longer (426 and 493).  64
+// sequences of 16 rows behind 32768 tokens take 130 us, and 221 without sharing.  The plan takes 5 to 9
+// us, the join 6 to 18.
 #include <type_traits>
 
 #include "internal.h"
@@ -932,9 +934,13 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedParams p, i
   if (p.lse && lane == 0) p.lse[grow] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
-// Blocks of 16 query rows a workgroup takes at once: as few as hold a sequence's or the
-// batch's rows (64 x 4000 tokens in 8 bits, 16 heads: 57 us with one block, 63 with two,
-// 76 with four; 32 heads: 64 with two, 77 with four).
+// Blocks of 16 query rows a workgroup takes at once: as few as hold a sequence's rows (64 x 4000
+// tokens in 8 bits, 16 heads: 57 us with one block, 63 with two, 76 with four; 32 heads: 64
+// with two, 77 with four), with groups the whole batch's, whatever the sizes of the groups.  That suits prefixes
+// of many rows (4096 tokens and 100 of each sequence's own in 8 bits: 8 groups of 12 sequences with 32 heads 114
+// us with one block, 92 with two, 85 with four; one group of 64 with 16 heads 61, 57 and 60; in 16 bits 113, 86 and 78,
+// and 58, 54 and 57) and costs groups of few (64 pairs with 8 heads 59, 65 and 79, 128 pairs with 4 heads 95, 106
+// and 134; in 16 bits, which the bytes bound, 86, 86 and 87, and 144, 144 and 146).
 int blocks_of(int64_t N, int64_t Q, int64_t H, int64_t G) {
   const int64_t rows = G > 0 ? N * Q * H : Q * H;
   return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);

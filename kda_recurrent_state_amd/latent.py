@@ -419,7 +419,9 @@ def kda_latent_decode_shared(cache, page_table: torch.Tensor, lengths: torch.Ten
     cu_groups[g+1] - 1; shared: [G] int32, how many first tokens its sequences
     have in common (the same rows, as after a fork: they are read through the
     table of the group's first sequence).  Sequences of no group share
-    nothing.  The rest, and the results, as for :func:`kda_latent_decode`; the
+    nothing.  It pays for many sequences of few query rows behind a long prefix (64 with up
+    to 32 rows each behind 8192 tokens, say); for few sequences, short prefixes or 128 rows
+    and more :func:`kda_latent_decode` is as fast or faster.  The rest, and the results, as for :func:`kda_latent_decode`; the
     workspace has :func:`kda_latent_shared_workspace_size` bytes.
     """
     what = "kda_latent_decode_shared"

@@ -65,7 +65,7 @@ def test_quotients_of_the_plan(host):
 @pytest.mark.parametrize("team", [1, 2, 3, 5, 11, 16])
 def test_shares_of_the_line(host, team):
     """They cover the line one behind the other, differ by one place at most, and each place is found in its share: short
-    lines, those around 2^31 places and the longest, of 2^42 and more."""
+    lines, those around 2^31 places and the longest, beyond 2^42."""
     rng = random.Random(team)
     most = 256 // team
     for total in [1, 2, most - 1, most, most + 1, 3 * most - 1, 12345, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 1, 2 ** 32 + 5,
